@@ -439,8 +439,199 @@ rf_status ridgefill_solve_ex(const void* state, size_t state_bytes, int32_t d_in
                              int32_t n_layers, double lambda, float* A_out, float* b_out,
                              uint16_t* A_bf16_out, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * The cache beyond the fill.  Exact rows, the tail and the generated tokens run the upper
+ * layers themselves (section "Two numbers set the skip range"): their keys and values go
+ * into the same paged cache, and their queries attend over it.  The calls below rotate and
+ * append such rows, attend over the cache, accumulate the attention weight that its rows
+ * receive (the scores of section "Which rows to compute exactly"), and shorten it.  They
+ * work on one layer's pools (the eviction on all of them) and on a batch of sequences.
+ *
+ * A batch of sequences in one pool.  Row t of sequence b lies in page
+ * block_tables[b * table_stride + t / page_size], slot t % page_size.  Lengths are read on
+ * the device, so a captured call replays with new ones; max_len is the host's bound on them
+ * and sizes grids and workspaces.  A sequence whose length is not in [0, max_len] sets
+ * RF_E_ROWS and is skipped (its outputs are left as they were); rows on a page outside
+ * [0, num_pages) set RF_E_ROWS and are taken as not there.
+ * ------------------------------------------------------------------------------ */
+typedef struct rf_paged_batch {
+  const int32_t* block_tables;  /* device int32 [batch][table_stride]                       */
+  const int32_t* lengths;       /* device int32 [batch]: rows each sequence has in the cache
+                                   (not read by ridgefill_append_rows, which takes NULL)    */
+  int64_t table_stride;         /* >= ceil(max_len / page_size)                             */
+  int32_t batch;                /* 1 .. 65535                                               */
+  int32_t max_len;              /* >= 1                                                     */
+  int32_t page_size, num_pages; /* >= 1; num_pages * page_size < 2^31                       */
+  int32_t n_kv_heads;           /* 1 .. 256                                                 */
+  int32_t head_dim;             /* 64 or 128; for ridgefill_append_rows a multiple of 16 up to 256 */
+} rf_paged_batch;
+
+/* ------------------------------------------------------------------------------
+ * Rotary positions.  Pair j of a head (of rotary_dim / 2 pairs) turns by the angle
+ * position * f_j, f_j = theta^(-2j / rotary_dim) where nothing is scaled:
+ *     a' = m (a cos - b sin),   b' = m (b cos + a sin)
+ * with (a, b) the features (j, j + rotary_dim/2) (RF_ROPE_HALF, as the fill rotates) or
+ * (2j, 2j+1) (RF_ROPE_INTERLEAVED); features from rotary_dim on pass unchanged.  Scaling for
+ * contexts s = factor times as long as the trained length L = orig_len:
+ *   RF_ROPE_LINEAR  f_j / s
+ *   RF_ROPE_NTK     theta * s^(r / (r - 2)) in place of theta, r = rotary_dim > 2
+ *   RF_ROPE_BANDS   by turns n = L f_j / (2 pi) over the trained length: n < low: f_j / s;
+ *                   n > high: f_j; between them (1 - t) f_j / s + t f_j,
+ *                   t = (n - low) / (high - low)
+ *   RF_ROPE_YARN    with d(n) = r ln(L / (2 pi n)) / (2 ln theta), p = max(floor d(high), 0),
+ *                   q = min(ceil d(low), r - 1), t = clamp((j - p) / max(q - p, 0.001), 0, 1):
+ *                   t f_j / s + (1 - t) f_j
+ * m = mscale; 0 means 1, for RF_ROPE_YARN 0.1 ln s + 1.  Angles are formed in fp64, cos and
+ * sin in fp32, and results rounded once to the output's type.
+ * ------------------------------------------------------------------------------ */
+#define RF_ROPE_HALF 0
+#define RF_ROPE_INTERLEAVED 1
+#define RF_ROPE_PLAIN 0
+#define RF_ROPE_LINEAR 1
+#define RF_ROPE_NTK 2
+#define RF_ROPE_BANDS 3
+#define RF_ROPE_YARN 4
+typedef struct rf_rope {
+  double theta;         /* base, > 1                                                     */
+  int32_t rotary_dim;   /* 0: the whole head; else a multiple of 16, <= head_dim         */
+  int32_t layout;       /* RF_ROPE_HALF or RF_ROPE_INTERLEAVED                           */
+  int32_t scaling;      /* RF_ROPE_PLAIN .. RF_ROPE_YARN                                 */
+  int32_t orig_len;     /* >= 1 for RF_ROPE_BANDS and RF_ROPE_YARN                       */
+  double factor;        /* >= 1 where scaling is not RF_ROPE_PLAIN                       */
+  double low, high;     /* 0 < low < high for RF_ROPE_BANDS and RF_ROPE_YARN             */
+  double mscale;        /* >= 0                                                          */
+} rf_rope;
+
+/* Element types of ridgefill_rope. */
+#define RF_TYPE_BF16 0
+#define RF_TYPE_F32 1
+
+/* Rotates x [n_rows][n_heads][head_dim] (rows x_stride elements apart) into out (the same,
+ * out_stride apart; out = x with equal strides rotates in place, other overlaps are not
+ * allowed).  transpose = 1 turns by the negative angle, times m: the transposed rotation,
+ * which takes the gradient of out to the gradient of x.
+ *   x, out      device, of x_type (RF_TYPE_BF16 or RF_TYPE_F32), 16-byte aligned; strides
+ *               >= n_heads * head_dim and multiples of 8 (bf16) or 4 (fp32) elements
+ *   positions   device int32 [n_rows]; any value, negative ones too
+ * head_dim: a multiple of 16 up to 256. */
+rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int64_t n_rows,
+                         int32_t n_heads, int32_t head_dim, int64_t x_stride,
+                         const int32_t* positions, void* out, int64_t out_stride,
+                         int32_t transpose, void* stream);
+
+/* Appends n_rows rows to the paged cache of one layer: k is rotated (as it comes if rope is
+ * NULL) and written with v to cache row rows[i] of sequence seq[i]; q, if given, is rotated
+ * into q_out.  Everything in one pass over the rows.
+ *   q           device bf16 [n_rows][n_q_heads][head_dim] or NULL (then n_q_heads = 0)
+ *   q_out       device bf16, the same shape; q_out = q rotates in place
+ *   k, v        device bf16 [n_rows][n_kv_heads][head_dim]; the strides (elements between
+ *               rows) are multiples of 8, all pointers 16-byte aligned
+ *   seq         device int32 [n_rows] or NULL (all rows belong to sequence 0); a negative
+ *               entry marks a padding row: nothing of it is read or written
+ *   rows        device int32 [n_rows]: cache rows in [0, kv->max_len)
+ *   positions   device int32 [n_rows], the angles' positions, or NULL (the cache rows)
+ *   status      device uint32 (4-byte aligned): receives the device status word of the
+ *               call.  A sequence, row or page out of range sets RF_E_ROWS there and that
+ *               row's k and v are not written (its q is rotated all the same).
+ * The (seq, rows) pairs of one call must differ from one another. */
+rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, const uint16_t* q,
+                                int32_t n_q_heads, int64_t q_stride, uint16_t* q_out,
+                                int64_t q_out_stride, const uint16_t* k, int64_t k_stride,
+                                const uint16_t* v, int64_t v_stride, int64_t n_rows,
+                                const int32_t* seq, const int32_t* rows, const int32_t* positions,
+                                uint16_t* k_pages, uint16_t* v_pages, uint32_t* status,
+                                void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Attention of the last rows of each sequence over its cache: a tree of drafted tokens, a
+ * chain of them, or one token.  Queries q_start[b] .. q_start[b+1]-1 belong to sequence b
+ * (n of them) and stand for the last n of its lengths[b] cached rows, which are in the cache
+ * already; query i (0-based among them) sees the c = lengths[b] - n rows before, and of the
+ * n rows those j whose bit is set in its word of tree_mask (without tree_mask: j <= i).
+ *     s = scale q . k,   lse = ln sum exp s,   out = sum exp(s - lse) v
+ * over the visible rows.  Query head h reads key head h / (n_q_heads / n_kv_heads).  A query
+ * that sees no row, or only scores of -inf, gives out = 0 and lse = -inf.  A row that a query
+ * does not see has no influence on it, whatever the row holds (NaN included).
+ *   q           device bf16 [n_q][n_q_heads][head_dim], rows q_stride elements apart
+ *               (multiple of 8), 16-byte aligned; n_q_heads a multiple of n_kv_heads
+ *   q_start     device int32 [batch + 1], ascending; sequences may have no queries.  One
+ *               with more than max_q queries, more queries than rows, or outside [0, n_q)
+ *               sets RF_E_ROWS and is skipped.  Queries of no sequence are left as they were.
+ *   max_q       1 .. 64: the host's bound on one sequence's queries
+ *   tree_mask   device uint64 [n_q] or NULL
+ *   out         device bf16 [n_q][n_q_heads][head_dim], rows out_stride elements apart
+ *               (multiple of 8), 16-byte aligned; or NULL (only lse; v_pages may then be NULL)
+ *   lse         device fp32 [n_q][n_q_heads] or NULL (one of out, lse is needed)
+ *   ws          >= ridgefill_tree_attention_workspace_bytes(kv, n_q_heads, max_q), 256-byte
+ *               aligned; its first 256 bytes hold the status
+ * Scores, maxima, sums and outputs are held in fp32; exp(s - max) is rounded to bf16 as the
+ * matrix cores' operand of the product with v, and out once at the end.
+ * Neither call reads kv->lengths on the host.  Size query: 0 on invalid input.
+ * ------------------------------------------------------------------------------ */
+size_t ridgefill_tree_attention_workspace_bytes(const rf_paged_batch* kv, int32_t n_q_heads,
+                                                int32_t max_q);
+rf_status ridgefill_tree_attention(const rf_paged_batch* kv, const uint16_t* k_pages,
+                                   const uint16_t* v_pages, const uint16_t* q, int32_t n_q_heads,
+                                   int64_t q_stride, const int32_t* q_start, int64_t n_q,
+                                   int32_t max_q, const uint64_t* tree_mask, float scale,
+                                   uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Accumulated attention weight.  For every row t of every sequence that has queries,
+ *     acc_out[b][t] = decay * acc[b][t] + sum over queries i that see t, and heads h, of
+ *                     exp(scale q_ih . k_t - lse_ih)
+ * Queries, q_start, max_q, tree_mask and scale as in ridgefill_tree_attention, whose lse this
+ * takes (entries of -inf give nothing).  With the last 64 tokens of a prompt as queries this
+ * is the score of section "Which rows to compute exactly" that ridgefill_select_rows ranks.
+ *   acc         device fp32 [batch][acc_stride] or NULL (nothing accumulated so far)
+ *   acc_out     device fp32 [batch][acc_stride]; acc_out = acc accumulates in place.  Entries
+ *               from lengths[b] on, and sequences without queries, are left as they were.
+ *   acc_stride  >= max_len
+ *   ws          >= ridgefill_attention_weight_workspace_bytes(kv, n_q_heads, max_q)
+ * Sums are held in fp32 and added in a fixed order: results do not vary between runs.
+ * ------------------------------------------------------------------------------ */
+size_t ridgefill_attention_weight_workspace_bytes(const rf_paged_batch* kv, int32_t n_q_heads,
+                                                  int32_t max_q);
+rf_status ridgefill_attention_weight(const rf_paged_batch* kv, const uint16_t* k_pages,
+                                     const uint16_t* q, int32_t n_q_heads, int64_t q_stride,
+                                     const int32_t* q_start, int64_t n_q, int32_t max_q,
+                                     const uint64_t* tree_mask, float scale, const float* lse,
+                                     float decay, const float* acc, float* acc_out,
+                                     int64_t acc_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Eviction.  Every sequence of more than n_keep rows is cut to n_keep, in every given
+ * layer's pools.  The kept rows are, in this order, the protected ones (position < n_sink,
+ * or among the n_recent highest positions: position > highest - n_recent) and the others by
+ * falling weight; ties go to the lower cache row.  -0.0 ties with +0.0; a NaN weight ranks
+ * lowest and sets RF_E_INVALID.  Kept rows below n_keep stay; the kept rows from n_keep on
+ * move, in ascending order, into the rows below n_keep that were not kept, in ascending
+ * order.  Keys carry their positions already, so attention does not depend on the order;
+ * positions_out says which position each row holds.
+ *   layers        host array [n_layers]; only k_pages and v_pages are used (16-byte aligned)
+ *   acc           device fp32 [batch][stride]: weights (ridgefill_attention_weight)
+ *   positions     device int32 [batch][stride]: position of each cached row
+ *   acc_out, positions_out   device, the same shapes: those of the rows after the cut;
+ *                 acc_out is 0 for the rows cut off (from the new length to the old one);
+ *                 entries from the old length on are left as they were.  Each may be the input.
+ *   lengths_out   device int32 [batch]: the new lengths; may be kv->lengths
+ *   stride        >= max_len
+ *   n_keep, n_sink, n_recent >= 0
+ *   ws            >= ridgefill_evict_workspace_bytes(kv, n_keep), 256-byte aligned; its first
+ *                 256 bytes hold the status.  A moving row on a bad page is not moved.
+ * The cut off pages stay in the block table; their rows are free for new ones.  Sequences of
+ * one call must not share pages that the cut writes.
+ * ------------------------------------------------------------------------------ */
+size_t ridgefill_evict_workspace_bytes(const rf_paged_batch* kv, int32_t n_keep);
+rf_status ridgefill_evict_rows(const rf_paged_batch* kv, const rf_layer* layers, int32_t n_layers,
+                               const float* acc, const int32_t* positions, int64_t stride,
+                               int32_t n_keep, int32_t n_sink, int32_t n_recent, float* acc_out,
+                               int32_t* positions_out, int32_t* lengths_out, void* ws,
+                               size_t ws_bytes, void* stream);
+
 /* Waits for `stream`, then returns the device status word of a fill, solve or selection
- * workspace: RF_OK, RF_E_ROWS, RF_E_NOT_SPD, RF_E_WORKSPACE for a solve on a calibration
+ * workspace (or of the cache calls' workspaces): RF_OK, RF_E_ROWS, RF_E_NOT_SPD, RF_E_WORKSPACE for a solve on a calibration
  * state whose header disagrees with the solve's sizes or that a calibrate call marked bad,
  * or RF_E_INVALID for a NaN score.  Each call
  * clears that word on the stream before its own kernels run, so the word reflects the

@@ -45,6 +45,14 @@ EXPORTED = [
     "ridgefill_solve",
     "ridgefill_solve_workspace_bytes_ex",
     "ridgefill_solve_ex",
+    "ridgefill_rope",
+    "ridgefill_append_rows",
+    "ridgefill_tree_attention_workspace_bytes",
+    "ridgefill_tree_attention",
+    "ridgefill_attention_weight_workspace_bytes",
+    "ridgefill_attention_weight",
+    "ridgefill_evict_workspace_bytes",
+    "ridgefill_evict_rows",
     "ridgefill_read_status",
     "ridgefill_solve_info",
     "ridgefill_profile_enable",
@@ -83,6 +91,22 @@ class rf_paged_kv(C.Structure):
     _fields_ = [("block_table", C.c_void_p), ("n_logical", C.c_int64),
                 ("page_size", C.c_int32), ("num_pages", C.c_int32)]
 
+
+class rf_paged_batch(C.Structure):
+    _fields_ = [("block_tables", C.c_void_p), ("lengths", C.c_void_p), ("table_stride", C.c_int64),
+                ("batch", C.c_int32), ("max_len", C.c_int32), ("page_size", C.c_int32),
+                ("num_pages", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class rf_rope(C.Structure):
+    _fields_ = [("theta", C.c_double), ("rotary_dim", C.c_int32), ("layout", C.c_int32),
+                ("scaling", C.c_int32), ("orig_len", C.c_int32), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double), ("mscale", C.c_double)]
+
+
+RF_ROPE_HALF, RF_ROPE_INTERLEAVED = range(2)
+RF_ROPE_PLAIN, RF_ROPE_LINEAR, RF_ROPE_NTK, RF_ROPE_BANDS, RF_ROPE_YARN = range(5)
+RF_TYPE_BF16, RF_TYPE_F32 = range(2)
 
 _lib = None
 
@@ -131,6 +155,18 @@ def lib() -> C.CDLL:
         "ridgefill_calibrate_ex": (st, [vp, sz, i32, i32, i32, vp, C.POINTER(vp), i64, vp]),
         "ridgefill_solve_workspace_bytes_ex": (sz, [i32, i32, i32]),
         "ridgefill_solve_ex": (st, [vp, sz, i32, i32, i32, C.c_double, vp, vp, vp, vp, sz, vp]),
+        "ridgefill_rope": (st, [vp, vp, i32, i64, i32, i32, i64, vp, vp, i64, i32, vp]),
+        "ridgefill_append_rows": (st, [vp, vp, vp, i32, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp,
+                                       vp, vp, vp, vp, vp]),
+        "ridgefill_tree_attention_workspace_bytes": (sz, [vp, i32, i32]),
+        "ridgefill_tree_attention": (st, [vp, vp, vp, vp, i32, i64, vp, i64, i32, vp, C.c_float, vp,
+                                          i64, vp, vp, sz, vp]),
+        "ridgefill_attention_weight_workspace_bytes": (sz, [vp, i32, i32]),
+        "ridgefill_attention_weight": (st, [vp, vp, vp, i32, i64, vp, i64, i32, vp, C.c_float, vp,
+                                            C.c_float, vp, vp, i64, vp, sz, vp]),
+        "ridgefill_evict_workspace_bytes": (sz, [vp, i32]),
+        "ridgefill_evict_rows": (st, [vp, C.POINTER(rf_layer), i32, vp, vp, i64, i32, i32, i32, vp,
+                                      vp, vp, vp, sz, vp]),
         "ridgefill_read_status": (st, [vp, vp]),
         "ridgefill_solve_info": (st, [vp, C.POINTER(C.c_double), C.POINTER(i32), vp]),
         "ridgefill_profile_enable": (st, [i32]),
@@ -309,6 +345,238 @@ def ridgefill_value_scale(shape: rf_shape, x_S_tail, x_l_tail: list, layers: lis
                                        int(x_S_tail.shape[0]), arr, len(layers), _ptr(out),
                                        _ptr(ws), int(ws.numel() * ws.element_size()),
                                        _stream(stream)))
+
+
+# ------------------------------------------------------------------------------ the cache
+#
+# These calls check what the C side cannot see (types, devices, shapes of the tensors), run on
+# the tensors' own device and, unless a stream is given, on that device's current stream.
+
+def _need(name: str, t, dtype, device, ndim: int) -> None:
+    if t.dtype != dtype or t.device != device or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {dtype} tensor of {ndim} dimensions on {device}, not "
+                         f"{t.dtype} of {t.dim()} on {t.device}")
+
+
+def _flat(name: str, t, dtype, device, ndim: int, shape: tuple | None = None) -> None:
+    """A contiguous tensor, of the given shape where one is given."""
+    _need(name, t, dtype, device, ndim)
+    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be contiguous" + (f" {shape}" if shape else "") +
+                         f", not {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _rows_of(name: str, t, dtype, device, width: int, n: int | None = None) -> int:
+    """Elements between the rows of [rows][heads][head_dim]; each row lies in one piece."""
+    _need(name, t, dtype, device, 3)
+    rows, heads, hd = t.shape
+    a, b, c = t.stride()
+    if heads == 0 or hd != width or (n is not None and rows != n) or c != 1 or (heads > 1 and b != hd):
+        raise ValueError(f"{name} must be [{'rows' if n is None else n}][heads][{width}] with each "
+                         f"row in one piece, not {tuple(t.shape)} with strides {t.stride()}")
+    return a if rows > 1 else max(heads * hd, a)
+
+
+def _go(f, device, stream, *args) -> None:
+    """f(*args, stream) with `device` current."""
+    import torch
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, handle)
+    if status != RF_OK:
+        _check(status)
+
+
+def make_rope(theta: float = 500000.0, rotary_dim: int = 0, layout: int = RF_ROPE_HALF,
+              scaling: int = RF_ROPE_PLAIN, factor: float = 1.0, orig_len: int = 0,
+              low: float = 0.0, high: float = 0.0, mscale: float = 0.0) -> rf_rope:
+    return rf_rope(theta, rotary_dim, layout, scaling, orig_len, factor, low, high, mscale)
+
+
+def make_batch(block_tables, lengths, page_size: int, num_pages: int, n_kv_heads: int,
+               head_dim: int, max_len: int | None = None) -> rf_paged_batch:
+    """Descriptor of a batch of sequences in a paged pool: block_tables int32 [batch][pages],
+    lengths int32 [batch] (None where only rows are appended).  max_len bounds the lengths
+    (default: all the rows that a table holds).  It keeps both tensors alive."""
+    import torch
+    dev = block_tables.device
+    _need("block_tables", block_tables, torch.int32, dev, 2)
+    batch, per = block_tables.shape
+    if block_tables.stride(1) != 1 and per > 1:
+        raise ValueError("the entries of a block table must lie in one piece")
+    if lengths is not None:
+        _flat("lengths", lengths, torch.int32, dev, 1, (batch,))
+    kv = rf_paged_batch(block_tables.data_ptr(), _ptr(lengths),
+                        block_tables.stride(0) if batch > 1 else per, batch,
+                        per * page_size if max_len is None else max_len, page_size, num_pages,
+                        n_kv_heads, head_dim)
+    if per * page_size < kv.max_len:
+        raise ValueError(f"a block table of {per} pages holds fewer than max_len = {kv.max_len} rows")
+    kv._keep = (block_tables, lengths)
+    kv._pool = (num_pages, page_size, n_kv_heads, head_dim)
+    kv._device = dev
+    return kv
+
+
+def make_pools(k_pages: list, v_pages: list):
+    """Array of layers that carry only their page pools, for ridgefill_evict_rows; it keeps
+    the pools alive."""
+    pools = (rf_layer * max(len(k_pages), 1))()
+    for i, (k, v) in enumerate(zip(k_pages, v_pages, strict=True)):
+        pools[i].k_pages, pools[i].v_pages = k.data_ptr(), v.data_ptr()
+    pools._keep = (list(k_pages), list(v_pages))
+    return pools
+
+
+def ridgefill_rope(rope: rf_rope, x, positions, out, transpose: bool = False, stream=None) -> None:
+    """x [rows][heads][head_dim] (bf16 or fp32) rotated by positions (int32 [rows]) into out
+    (may be x); transpose=True takes the gradient of out to the gradient of x."""
+    import torch
+    dev, hd = x.device, x.shape[-1]
+    kind = RF_TYPE_F32 if x.dtype == torch.float32 else RF_TYPE_BF16
+    dtype = torch.float32 if kind else torch.bfloat16
+    xs = _rows_of("x", x, dtype, dev, hd)
+    n, heads = x.shape[0], x.shape[1]
+    os_ = _rows_of("out", out, dtype, dev, hd, n)
+    if out.shape[1] != heads:
+        raise ValueError(f"out has {out.shape[1]} heads, x {heads}")
+    _flat("positions", positions, torch.int32, dev, 1, (n,))
+    _go(lib().ridgefill_rope, dev, stream, C.byref(rope), x.data_ptr(), kind, n, heads, hd, xs,
+        positions.data_ptr(), out.data_ptr(), os_, 1 if transpose else 0)
+
+
+def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, k_pages, v_pages,
+                          status, seq=None, positions=None, q=None, q_out=None, stream=None) -> None:
+    """k (rotated) and v, bf16 [n][n_kv][head_dim], into cache rows `rows` (int32 [n]) of
+    sequences `seq` (int32 [n]; None: sequence 0; negative: a padding row); q rotated into
+    q_out.  positions (int32 [n]) default to the rows.  status: device int32 tensor."""
+    import torch
+    dev, n, hd = kv._device, k.shape[0], kv.head_dim
+    ks = _rows_of("k", k, torch.bfloat16, dev, hd, n)
+    vs = _rows_of("v", v, torch.bfloat16, dev, hd, n)
+    if k.shape[1] != kv.n_kv_heads or v.shape[1] != kv.n_kv_heads:
+        raise ValueError(f"k and v must have {kv.n_kv_heads} heads")
+    _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
+    _flat("v_pages", v_pages, torch.bfloat16, dev, 4, kv._pool)
+    _flat("rows", rows, torch.int32, dev, 1, (n,))
+    if seq is not None:
+        _flat("seq", seq, torch.int32, dev, 1, (n,))
+    if positions is not None:
+        _flat("positions", positions, torch.int32, dev, 1, (n,))
+    if status.device != dev or status.numel() < 1 or status.element_size() != 4:
+        raise ValueError("status must be a 4-byte integer tensor on the cache's device")
+    heads = qs = qos = 0
+    if q is not None:
+        qs = _rows_of("q", q, torch.bfloat16, dev, hd, n)
+        qos = _rows_of("q_out", q_out, torch.bfloat16, dev, hd, n)
+        heads = q.shape[1]
+        if q_out.shape[1] != heads:
+            raise ValueError(f"q_out has {q_out.shape[1]} heads, q {heads}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _go(lib().ridgefill_append_rows, dev, stream, None if rope is None else C.byref(rope),
+        C.byref(kv), _ptr(q), heads, qs, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, n,
+        _ptr(seq), rows.data_ptr(), _ptr(positions), k_pages.data_ptr(), v_pages.data_ptr(),
+        status.data_ptr())
+
+
+def ridgefill_tree_attention_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int) -> int:
+    return int(lib().ridgefill_tree_attention_workspace_bytes(C.byref(kv), n_q_heads, max_q))
+
+
+def _queries(kv: rf_paged_batch, k_pages, q, q_start, tree_mask, lse, ws) -> int:
+    """Checks shared by the attention and the weight accumulation; q's row stride."""
+    import torch
+    dev = kv._device
+    if kv._keep[1] is None:
+        raise ValueError("the batch was made without lengths")
+    stride = _rows_of("q", q, torch.bfloat16, dev, kv.head_dim)
+    _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
+    _flat("q_start", q_start, torch.int32, dev, 1, (kv.batch + 1,))
+    n, heads = q.shape[0], q.shape[1]
+    if tree_mask is not None:
+        _flat("tree_mask", tree_mask, torch.int64, dev, 1, (n,))
+    if lse is not None:
+        _flat("lse", lse, torch.float32, dev, 2, (n, heads))
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    return stride
+
+
+def ridgefill_tree_attention(kv: rf_paged_batch, k_pages, v_pages, q, q_start, max_q: int,
+                             scale: float, out, ws, lse=None, tree_mask=None, stream=None) -> None:
+    """Attention of q (bf16 [n][heads][head_dim]), the last rows of each sequence, over the
+    cache.  q_start int32 [batch + 1]; tree_mask int64 [n] (bit j: sees draft j) or None (a
+    chain); out bf16 like q or None; lse fp32 [n][heads] or None."""
+    import torch
+    qs = _queries(kv, k_pages, q, q_start, tree_mask, lse, ws)
+    os_ = 0
+    if out is not None:
+        _flat("v_pages", v_pages, torch.bfloat16, kv._device, 4, kv._pool)
+        os_ = _rows_of("out", out, torch.bfloat16, kv._device, kv.head_dim, q.shape[0])
+        if out.shape[1] != q.shape[1]:
+            raise ValueError(f"out has {out.shape[1]} heads, q {q.shape[1]}")
+    _go(lib().ridgefill_tree_attention, kv._device, stream, C.byref(kv), k_pages.data_ptr(),
+        _ptr(v_pages), q.data_ptr(), q.shape[1], qs, q_start.data_ptr(), q.shape[0], max_q,
+        _ptr(tree_mask), scale, _ptr(out), os_, _ptr(lse), ws.data_ptr(), _nbytes(ws))
+
+
+def ridgefill_attention_weight_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int) -> int:
+    return int(lib().ridgefill_attention_weight_workspace_bytes(C.byref(kv), n_q_heads, max_q))
+
+
+def ridgefill_attention_weight(kv: rf_paged_batch, k_pages, q, q_start, max_q: int, scale: float,
+                               lse, acc_out, ws, acc=None, decay: float = 1.0, tree_mask=None,
+                               stream=None) -> None:
+    """acc_out (fp32 [batch][>= max_len]) = decay * acc + the weight that q's queries, with
+    their lse, give to each cached row; acc=None where nothing is accumulated yet."""
+    import torch
+    qs = _queries(kv, k_pages, q, q_start, tree_mask, lse, ws)
+    dev = kv._device
+    _flat("acc_out", acc_out, torch.float32, dev, 2)
+    if acc_out.shape[0] != kv.batch:
+        raise ValueError(f"acc_out has {acc_out.shape[0]} rows for {kv.batch} sequences")
+    if acc is not None:
+        _flat("acc", acc, torch.float32, dev, 2, tuple(acc_out.shape))
+    _go(lib().ridgefill_attention_weight, dev, stream, C.byref(kv), k_pages.data_ptr(), q.data_ptr(),
+        q.shape[1], qs, q_start.data_ptr(), q.shape[0], max_q, _ptr(tree_mask), scale,
+        lse.data_ptr(), decay, _ptr(acc), acc_out.data_ptr(), acc_out.shape[1], ws.data_ptr(),
+        _nbytes(ws))
+
+
+def ridgefill_evict_workspace_bytes(kv: rf_paged_batch, n_keep: int) -> int:
+    return int(lib().ridgefill_evict_workspace_bytes(C.byref(kv), n_keep))
+
+
+def ridgefill_evict_rows(kv: rf_paged_batch, layers, acc, positions, n_keep: int, acc_out,
+                         positions_out, lengths_out, ws, n_sink: int = 0, n_recent: int = 0,
+                         stream=None) -> None:
+    """Every sequence of more than n_keep rows cut to them, in the pools of `layers` (from
+    make_pools, or dicts with k_pages and v_pages).  acc fp32 and positions int32
+    [batch][>= max_len]; the three outputs may be the inputs."""
+    import torch
+    dev = kv._device
+    if kv._keep[1] is None:
+        raise ValueError("the batch was made without lengths")
+    if isinstance(layers, (list, tuple)):
+        layers = make_pools([l["k_pages"] for l in layers], [l["v_pages"] for l in layers])
+    for pool in layers._keep[0] + layers._keep[1]:
+        _flat("k_pages and v_pages", pool, torch.bfloat16, dev, 4, kv._pool)
+    shape = (kv.batch, acc.shape[-1])
+    _flat("acc", acc, torch.float32, dev, 2, shape)
+    _flat("acc_out", acc_out, torch.float32, dev, 2, shape)
+    _flat("positions", positions, torch.int32, dev, 2, shape)
+    _flat("positions_out", positions_out, torch.int32, dev, 2, shape)
+    _flat("lengths_out", lengths_out, torch.int32, dev, 1, (kv.batch,))
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    _go(lib().ridgefill_evict_rows, dev, stream, C.byref(kv), layers, len(layers._keep[0]),
+        acc.data_ptr(), positions.data_ptr(), shape[1], n_keep, n_sink, n_recent,
+        acc_out.data_ptr(), positions_out.data_ptr(), lengths_out.data_ptr(), ws.data_ptr(),
+        _nbytes(ws))
 
 
 # ------------------------------------------------------------------------------ calibration

@@ -12,13 +12,15 @@
 #include <string>
 #include <vector>
 
+#include "rf_error.h"
 #include "rf_internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-rf_status fail(rf_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace rf {
+
 rf_status fail(rf_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -37,6 +39,14 @@ rf_status ok() {
 rf_status hip_fail(hipError_t e, const char* what) {
   return fail(RF_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace rf
+
+namespace {
+
+using rf::fail;
+using rf::hip_fail;
+using rf::ok;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
