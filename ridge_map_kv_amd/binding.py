@@ -380,6 +380,8 @@ def _rows_of(name: str, t, dtype, device, width: int, n: int | None = None) -> i
 def _go(f, device, stream, *args) -> None:
     """f(*args, stream) with `device` current."""
     import torch
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be in GPU memory, not on {device}")
     handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     if device.index == torch.cuda.current_device():
         status = f(*args, handle)
