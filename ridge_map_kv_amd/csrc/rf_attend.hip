@@ -1,9 +1,27 @@
-// Attention of drafted tokens over the paged cache, and the attention weight that its rows
-// receive, on gfx950 (sections "Two numbers set the skip range" and "Which rows to compute
-// exactly" of the English RidgeFill review).
+// Attention of drafted tokens over the paged cache, on gfx950 (section "Two numbers set the
+// skip range" of the English RidgeFill review: rows that are not filled attend over the cache).
 //
-// The plain kernels: one wave per (query, head) walks the rows with a running maximum and
-// sum; one wave per row adds up the weights of all queries and heads.
+// For one key head, the n queries of a sequence and the G query heads that share it are M = n G
+// rows of one matrix: S = Q K^T, softmax over the cache rows, O = P V.  K and V are read once
+// for all of them, so with M of a few rows the call is bound by that read (2 hd bytes a row
+// and head for each of K and V against 4 M hd operations), with M of some hundreds by the
+// matrix cores and the exponentials.
+//
+// A wave computes the transposed products with 16x16x32 MFMAs and needs no LDS for them:
+//   S^T (16 cache rows x 16 queries) = K Q^T: A = K, lane (c, g) = (lane % 16, lane / 16) holds
+//     row c, features 8 g .. 8 g + 7 of each 32: one 16-byte load of the cache row;
+//   the result has query c in lane (c, g) and cache rows 4 g + r: the softmax statistics of a
+//     query are a running maximum and sum per lane, joined over g by two lane exchanges;
+//   O^T (16 features x 16 queries) += V^T P^T over 32 cache rows: P^T as the B operand is what
+//     the lane already holds, with the cache rows taken in the order k = 8 g + j <->
+//     row 16 (j / 4) + 4 g + j % 4.  The A operand needs, for one feature, those eight rows'
+//     values: the lane loads 16 bytes of each of the eight rows (hd 128; features 8 c ..
+//     8 c + 7) and transposes the 8 x 8 block in its registers by byte permutes, so feature
+//     tile m consists of the features 8 c + m.  O^T then has features 8 (4 g + r) + m in
+//     lane (c, g): eight in a row for each r.
+// The wave loads the next 32 rows while it computes; block-table entries are read two steps
+// ahead.  A workgroup's four waves take the 32-row tiles of its row range in turn and are joined
+// in LDS; long caches are split over workgroups, whose partial results (fp32) a second kernel joins.
 #include "rf_cache.h"
 #include "rf_common.h"
 
@@ -11,134 +29,549 @@ namespace rf {
 
 namespace {
 
-__device__ __forceinline__ int pool_slot(const Batch& b, int seq, int row) {
-  const int page = b.tables[(int64_t)seq * b.table_stride + row / b.page_size];
-  if (page < 0 || page >= b.num_pages) return -1;
-  return page * b.page_size + row % b.page_size;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32;             // cache rows of one step of a wave
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Division of 0 .. 2^31 - 1 by a divisor known on the host: (mulhi(x, m) + x) >> s.
+struct Divide {
+  unsigned m, s, d;
+};
+Divide divide_by(unsigned d) {
+  Divide v{0u, 0u, d};
+  while ((1ull << v.s) < d) ++v.s;
+  v.m = (unsigned)((((1ull << v.s) - d) << 32) / d + 1);
+  return v;
+}
+__device__ __forceinline__ unsigned quotient(unsigned x, Divide v) {
+  return (__umulhi(x, v.m) + x) >> v.s;
 }
 
-// Sequence `seq`: its length, its queries; false if it is to be skipped (with *bad set where
-// that is an error).
+struct AttendArgs {
+  Batch b;
+  Queries q;
+  const uint16_t* kp;
+  const uint16_t* vp;
+  uint16_t* out;
+  float* lse;
+  unsigned* status;
+  float* part_o;                // [batch][n_kv][splits][max_q G][hd]
+  float2* part_ml;              // [batch][n_kv][splits][max_q G]: running maximum (log2), sum
+  int64_t out_stride;
+  Divide page;
+  int splits, chunk;            // row ranges of a sequence, rows in each (a multiple of 128)
+  int mblocks;                  // blocks of query rows
+  int group;                    // query heads of a key head
+  int scan;                     // 1: the workgroup past the grid looks all pages over for the status
+};
+
+// Sequence `seq`: its length, first query and number of queries; false if it is to be skipped
+// (with *bad set where that is an error).
 __device__ __forceinline__ bool sequence_of(const Batch& b, const Queries& q, int seq, int* len,
                                             int* first, int* n, bool* bad) {
   *len = b.lengths[seq];
   *first = q.start[seq];
-  *n = q.start[seq + 1] - *first;
-  *bad = *len < 0 || *len > b.max_len || *first < 0 || *n < 0 || *n > q.max_q || *n > *len ||
-         (int64_t)*first + *n > q.n_q;
+  const int end = q.start[seq + 1];
+  *n = (int)((unsigned)end - (unsigned)*first);
+  *bad = *len < 0 || *len > b.max_len || *first < 0 || end < *first || *n > q.max_q || *n > *len ||
+         end > q.n_q;
   return !*bad && *n > 0;
 }
 
-__device__ __forceinline__ bool sees(const Queries& q, int query, int i, int draft) {
-  if (draft < 0) return true;
-  return q.mask ? (q.mask[query] >> draft) & 1 : draft <= i;
+// The status word from one workgroup: every sequence and every page that it uses.
+__device__ void scan_status(const Batch& b, const Queries& q, unsigned* status) {
+  int bits = 0;
+  for (int s = 0; s < b.batch; ++s) {
+    int len, first, n;
+    bool bad;
+    if (sequence_of(b, q, s, &len, &first, &n, &bad)) {
+      const int pages = (len + b.page_size - 1) / b.page_size;
+      for (int i = threadIdx.x; i < pages; i += blockDim.x) {
+        const int page = b.tables[(int64_t)s * b.table_stride + i];
+        if (page < 0 || page >= b.num_pages) bits = 1;
+      }
+    }
+    if (bad) bits = 1;
+  }
+  bits = __syncthreads_or(bits);
+  if (threadIdx.x == 0) *status = bits ? kStatusRowsBit : 0u;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half) {
+  return __builtin_amdgcn_perm(hi, lo, half ? 0x07060302u : 0x05040100u);
+}
+
+template <int HD>
+struct Tile {                   // 32 cache rows of one head, as a wave holds them
+  static constexpr int kSteps = HD / 32;
+  u32x4 k[2][kSteps];           // rows 16 t + c, features 32 s + 8 g ..
+  uint32_t v[8][HD / 32];       // rows 16 (j/4) + 4 g + j % 4, features (HD/16) c ..
+};
+
+template <int HD, bool kV>
+__device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, const uint16_t* kh,
+                                          const uint16_t* vh, int slot, int c, int g) {
+  const int64_t row = (int64_t)a.b.n_kv * HD;
 #pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  for (int h = 0; h < 2; ++h) {
+    const uint16_t* p = kh + (int64_t)__shfl(slot, 16 * h + c) * row + 8 * g;
+#pragma unroll
+    for (int s = 0; s < HD / 32; ++s) t.k[h][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
+  }
+  if constexpr (kV) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint16_t* p = vh + (int64_t)__shfl(slot, 16 * (j / 4) + 4 * g + j % 4) * row + (HD / 16) * c;
+      if constexpr (HD == 128) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.v[j][i] = w[i];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        t.v[j][0] = w[0];
+        t.v[j][1] = w[1];
+      }
+    }
+  }
 }
 
-__global__ void attend_plain_kernel(Batch b, const uint16_t* kp, const uint16_t* vp, Queries q,
-                                    uint16_t* out, int64_t out_stride, float* lse,
-                                    unsigned* status) {
-  const int seq = blockIdx.z, h = blockIdx.y, i = blockIdx.x, lane = threadIdx.x;
+// MT tiles of 16 query rows.  kOut: with the product with V (else only the statistics).
+template <int HD, int MT, bool kOut>
+__global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(AttendArgs a) {
+  constexpr int kSteps = HD / 32, kFeat = HD / 16;
+  __shared__ float sh_o[kWaves / 2][16 * MT][HD + 4];
+  __shared__ float2 sh_ml[kWaves / 2][16 * MT];
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
+  // blocks of query rows of one row range go to one XCD (blockIdx % 8), side by side
+  int unit = blockIdx.x, mb = 0;
+  if (a.mblocks > 1) {
+    const int per = 8 * a.mblocks, full = (a.b.batch * a.b.n_kv * a.splits) / 8 * per;
+    if (unit < full) {
+      mb = unit % per / 8;
+      unit = unit / per * 8 + unit % 8;
+    } else {
+      const int rest = unit - full;
+      mb = rest % a.mblocks;
+      unit = full / a.mblocks + rest / a.mblocks;
+    }
+  }
+  const int split = unit % a.splits, sh = unit / a.splits;
+  const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+
   int len, first, n;
   bool bad;
-  const bool go = sequence_of(b, q, seq, &len, &first, &n, &bad);
-  if (bad) atomicOr(status, kStatusRowsBit);
-  if (!go || i >= n) return;
-  const int per = b.hd / 64, kh = h / (q.n_heads / b.n_kv), ctx = len - n;
-  const uint16_t* qp = q.q + (first + i) * q.q_stride + h * b.hd;
-  float x[2], o[2] = {0.f, 0.f}, m = -INFINITY, sum = 0.f;
-  for (int e = 0; e < per; ++e) x[e] = bf16_to_f32(qp[lane * per + e]);
-  for (int t = 0; t < len; ++t) {
-    if (!sees(q, first + i, i, t - ctx)) continue;
-    const int slot = pool_slot(b, seq, t);
-    if (slot < 0) {
-      atomicOr(status, kStatusRowsBit);
+  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
+  if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  const int m_rows = n * a.group, m0 = mb * 16 * MT;
+  const int begin = split * a.chunk;
+  if (!go || m0 >= m_rows || (begin >= len && split > 0)) return;
+  const int end = len < begin + a.chunk ? len : begin + a.chunk;
+  const int ctx = len - n;
+
+  // Q^T fragments: query row m0 + 16 t + c of the block, zero past the last
+  bf16x8 qf[MT][kSteps];
+  uint64_t words[MT];
+  int qi[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + c;
+    const bool in = m < m_rows;
+    const int i = in ? m / a.group : 0, h = in ? kh * a.group + m % a.group : 0;
+    const uint16_t* p = a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * g;
+    qi[t] = i;
+    words[t] = a.q.mask ? a.q.mask[first + i] : (i < 63 ? (2ull << i) - 1 : ~0ull);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (in) w = *reinterpret_cast<const u32x4*>(p + 32 * s);
+      qf[t][s] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+
+  f32x4 o[MT][kOut ? kFeat : 1];
+  float m_run[MT], l_run[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    m_run[t] = -INFINITY;
+    l_run[t] = 0.f;
+#pragma unroll
+    for (int f = 0; f < (kOut ? kFeat : 1); ++f) o[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
+  const uint16_t* kbase = a.kp + kh * HD;
+  const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
+  const float scale2 = a.q.scale * kLog2e;
+  int page_err = 0;
+  // page of row r (the last row for rows past it), then the pool slot: -1 on a bad page
+  const auto page_of = [&](int base) -> int {
+    const int r = base + (lane & 31);
+    return table[quotient((unsigned)(r < len ? r : len - 1), a.page)];
+  };
+  const auto slot_of = [&](int base, int page) -> int {
+    const int r0 = base + (lane & 31), r = r0 < len ? r0 : len - 1;
+    if (page < 0 || page >= a.b.num_pages) return -1;
+    return page * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
+  };
+
+  int base = begin + wave * kRows;
+  constexpr int kStride = kWaves * kRows;
+  Tile<HD> cur;
+  int page_next = 0, slot = -1;
+  if (base < end) {
+    slot = slot_of(base, page_of(base));
+    load_tile<HD, kOut>(cur, a, kbase, vbase, slot < 0 ? 0 : slot, c, g);
+    page_next = page_of(base + kStride);
+  }
+  for (; base < end; base += kStride) {
+    // the next rows on their way (rows past the end repeat the last one, and are not used)
+    const int slot_next = slot_of(base + kStride, page_next);
+    Tile<HD> next;
+    if (base + kStride < end) load_tile<HD, kOut>(next, a, kbase, vbase, slot_next < 0 ? 0 : slot_next, c, g);
+    page_next = page_of(base + 2 * kStride);
+
+    const uint64_t good64 = __ballot(slot >= 0);
+    const uint32_t good = (uint32_t)good64;
+    const bool masked = base + kRows > ctx || base + kRows > end || good != 0xffffffffu;
+    if (good != 0xffffffffu) page_err = 1;
+    uint32_t there = good;                            // rows of this step that exist
+    if (end - base < 32) there &= (1u << (end - base)) - 1u;
+
+    // V^T fragments
+    bf16x8 vf[kOut ? kFeat : 1];
+    bool wild = false;                                // a value that is not finite
+    if constexpr (kOut) {
+      if (masked) {
+        bool w = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool in = there >> (16 * (j / 4) + 4 * g + j % 4) & 1;
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {
+            if (!in) cur.v[j][i] = 0u;
+            w |= (cur.v[j][i] & 0x7f80u) == 0x7f80u || (cur.v[j][i] & 0x7f800000u) == 0x7f800000u;
+          }
+        }
+        wild = __any(w);
+      }
+#pragma unroll
+      for (int f = 0; f < kFeat; ++f) {
+        u32x4 w;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) w[p] = half_pair(cur.v[2 * p][f / 2], cur.v[2 * p + 1][f / 2], f & 1);
+        vf[f] = __builtin_bit_cast(bf16x8, w);
+      }
+    }
+
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, cur.k[h][st]), qf[t][st], s[h]);
+      uint32_t seen = 0xffffffffu;                    // rows that this lane's query sees
+      if (masked) {
+        seen = there;
+        if (base + kRows > ctx) {
+          const int d = base - ctx;                   // draft of the step's first row
+          uint64_t w = words[t];
+          uint32_t vis;
+          if (d >= 0)
+            vis = d < 64 ? (uint32_t)(w >> d) : 0u;
+          else
+            vis = (uint32_t)(w << -d) | ((1u << -d) - 1u);
+          seen &= vis;
+        }
+      }
+      float x[8], top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = s[j / 4][j % 4] * scale2;
+        if (masked && !(seen >> (16 * (j / 4) + 4 * g + j % 4) & 1)) x[j] = -INFINITY;
+        top = fmaxf(top, x[j]);
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m_new = fmaxf(m_run[t], top);
+      const float zero = m_new == -INFINITY ? 0.f : m_new;
+      if (__any(m_new > m_run[t])) {
+        const float shrink = __builtin_amdgcn_exp2f(m_run[t] - zero);
+        l_run[t] *= shrink;
+        if constexpr (kOut) {
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f) o[t][f] *= shrink;
+        }
+      }
+      m_run[t] = m_new;
+      float p[8], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(x[j] - zero);
+        sum += p[j];
+      }
+      l_run[t] += sum;
+      if constexpr (kOut) {
+        u32x4 pw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pw[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+        if (!wild) {
+          const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f) o[t][f] = mfma16(vf[f], pf, o[t][f]);
+        } else {
+          // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
+          // for the queries that see the row.
+          for (int r = 0; r < kRows; ++r) {
+            const int rg = r % 16 / 4, j = r / 16 * 4 + r % 4;
+            const bool vis = __shfl(seen, 16 * rg + c) >> r & 1;
+            const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
+            u32x4 pr;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pr[i] = g == rg && i == j / 2 ? pw[i] & keep : 0u;
+#pragma unroll
+            for (int f = 0; f < kFeat; ++f) {
+              const u32x4 vw = __builtin_bit_cast(u32x4, vf[f]);
+              u32x4 vr;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) vr[i] = g == rg && i == j / 2 ? vw[i] & keep : 0u;
+              const f32x4 add = mfma16(__builtin_bit_cast(bf16x8, vr), __builtin_bit_cast(bf16x8, pr),
+                                       f32x4{0.f, 0.f, 0.f, 0.f});
+              if (vis) o[t][f] += add;
+            }
+          }
+        }
+      }
+    }
+    cur = next;
+    slot = slot_next;
+  }
+  if (page_err && !a.scan && lane == 0) atomicOr(a.status, kStatusRowsBit);
+
+  // sums over g, then the waves: 2 and 3 into 0 and 1, then 1 into 0
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    l_run[t] += __shfl_xor(l_run[t], 16);
+    l_run[t] += __shfl_xor(l_run[t], 32);
+  }
+  for (int half = kWaves / 2; half; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+      const int w = wave - half;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (g == 0) sh_ml[w][16 * t + c] = make_float2(m_run[t], l_run[t]);
+        if constexpr (kOut) {
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sh_o[w][16 * t + c][kFeat * (4 * g + r) + f] = o[t][f][r];
+        }
+      }
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const float2 ml = sh_ml[wave][16 * t + c];
+        const float m_new = fmaxf(m_run[t], ml.x), zero = m_new == -INFINITY ? 0.f : m_new;
+        const float mine = __builtin_amdgcn_exp2f(m_run[t] - zero), theirs = __builtin_amdgcn_exp2f(ml.x - zero);
+        m_run[t] = m_new;
+        l_run[t] = l_run[t] * mine + ml.y * theirs;
+        if constexpr (kOut) {
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              o[t][f][r] = o[t][f][r] * mine + sh_o[wave][16 * t + c][kFeat * (4 * g + r) + f] * theirs;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+  const int64_t part = ((int64_t)sh * a.splits + split) * (a.q.max_q * a.group);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int m = m0 + 16 * t + c;
+    if (m >= m_rows) continue;
+    if (a.splits > 1) {
+      if (g == 0) a.part_ml[part + m] = make_float2(m_run[t], l_run[t]);
+      if constexpr (kOut) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float* p = a.part_o + (part + m) * HD + kFeat * (4 * g + r);
+#pragma unroll
+          for (int f = 0; f < kFeat; f += 4)
+            *reinterpret_cast<f32x4*>(p + f) = f32x4{o[t][f][r], o[t][f + 1][r], o[t][f + 2][r], o[t][f + 3][r]};
+        }
+      }
       continue;
     }
-    const int64_t at = ((int64_t)slot * b.n_kv + kh) * b.hd + lane * per;
-    float s = 0.f;
-    for (int e = 0; e < per; ++e) s += x[e] * bf16_to_f32(kp[at + e]);
-    s = wave_sum(s) * q.scale;
-    const float top = fmaxf(m, s), base = top == -INFINITY ? 0.f : top;
-    const float old = expf(m - base), p = expf(s - base);
-    sum = sum * old + p;
-    m = top;
-    if (out)
-      for (int e = 0; e < per; ++e) o[e] = o[e] * old + p * bf16_to_f32(vp[at + e]);
-  }
-  const bool none = sum == 0.f;
-  if (out)
-    for (int e = 0; e < per; ++e)
-      out[(first + i) * out_stride + h * b.hd + lane * per + e] =
-          (uint16_t)f32_to_bf16(none ? 0.f : o[e] / sum);
-  if (lse && lane == 0) lse[(int64_t)(first + i) * q.n_heads + h] = none ? -INFINITY : m + logf(sum);
-}
-
-__global__ void weight_plain_kernel(Batch b, const uint16_t* kp, Queries q, const float* lse,
-                                    float decay, const float* acc, float* acc_out,
-                                    int64_t acc_stride, unsigned* status) {
-  const int seq = blockIdx.y, t = blockIdx.x, lane = threadIdx.x;
-  int len, first, n;
-  bool bad;
-  const bool go = sequence_of(b, q, seq, &len, &first, &n, &bad);
-  if (bad) atomicOr(status, kStatusRowsBit);
-  if (!go || t >= len) return;
-  const int per = b.hd / 64, group = q.n_heads / b.n_kv, ctx = len - n;
-  const int slot = pool_slot(b, seq, t);
-  float w = 0.f;
-  if (slot < 0) {
-    atomicOr(status, kStatusRowsBit);
-  } else {
-    for (int kh = 0; kh < b.n_kv; ++kh) {
-      const int64_t at = ((int64_t)slot * b.n_kv + kh) * b.hd + lane * per;
-      for (int i = 0; i < n; ++i) {
-        if (!sees(q, first + i, i, t - ctx)) continue;
-        for (int h = kh * group; h < (kh + 1) * group; ++h) {
-          const uint16_t* qp = q.q + (first + i) * q.q_stride + h * b.hd + lane * per;
-          const float l = lse[(int64_t)(first + i) * q.n_heads + h];
-          float s = 0.f;
-          for (int e = 0; e < per; ++e) s += bf16_to_f32(qp[e]) * bf16_to_f32(kp[at + e]);
-          s = wave_sum(s) * q.scale;
-          if (l != -INFINITY) w += expf(s - l);
+    const int h = kh * a.group + m % a.group;
+    const int64_t row = first + m / a.group;
+    const bool none = l_run[t] == 0.f;
+    if (a.lse && g == 0)
+      a.lse[row * a.q.n_heads + h] = none ? -INFINITY : m_run[t] * kLn2 + __logf(l_run[t]);
+    if constexpr (kOut) {
+      const float inv = none ? 0.f : 1.f / l_run[t];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint16_t* p = a.out + row * a.out_stride + h * HD + kFeat * (4 * g + r);
+#pragma unroll
+        for (int f = 0; f < kFeat; f += 4) {
+          u32x2 w;
+          w[0] = pack_bf16x2(o[t][f][r] * inv, o[t][f + 1][r] * inv);
+          w[1] = pack_bf16x2(o[t][f + 2][r] * inv, o[t][f + 3][r] * inv);
+          *reinterpret_cast<u32x2*>(p + f) = none ? u32x2{0u, 0u} : w;
         }
       }
     }
   }
-  if (lane == 0) {
-    const int64_t a = seq * acc_stride + t;
-    acc_out[a] = acc ? decay * acc[a] + w : w;
+}
+
+// Joins the splits of one output row per wave.
+template <int HD>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
+  const int rows = a.q.max_q * a.group;
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int sh = (int)(id / rows), m = (int)(id % rows);
+  if (sh >= a.b.batch * a.b.n_kv) return;
+  const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
+  int len, first, n;
+  bool bad;
+  if (!sequence_of(a.b, a.q, seq, &len, &first, &n, &bad) || m >= n * a.group) return;
+  const int parts = (len + a.chunk - 1) / a.chunk;
+  const int64_t at = (int64_t)sh * a.splits * rows + m;
+  float top = -INFINITY;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[at + (int64_t)s * rows].x);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float zero = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, o[HD / 64];
+#pragma unroll
+  for (int e = 0; e < HD / 64; ++e) o[e] = 0.f;
+  for (int s = 0; s < parts; ++s) {
+    const float2 ml = a.part_ml[at + (int64_t)s * rows];
+    const float w = __builtin_amdgcn_exp2f(ml.x - zero);
+    sum += ml.y * w;
+    if (a.out) {
+      const float* p = a.part_o + (at + (int64_t)s * rows) * HD + lane * (HD / 64);
+#pragma unroll
+      for (int e = 0; e < HD / 64; ++e) o[e] += p[e] * w;
+    }
   }
+  const int h = kh * a.group + m % a.group;
+  const int64_t row = first + m / a.group;
+  const bool none = sum == 0.f;
+  if (a.lse && lane == 0) a.lse[row * a.q.n_heads + h] = none ? -INFINITY : top * kLn2 + __logf(sum);
+  if (a.out) {
+    uint16_t* p = a.out + row * a.out_stride + h * HD + lane * (HD / 64);
+#pragma unroll
+    for (int e = 0; e < HD / 64; ++e) p[e] = (uint16_t)f32_to_bf16(none ? 0.f : o[e] / sum);
+  }
+}
+
+// How a call is laid out.
+struct AttendPlan {
+  int mt, mblocks, group, splits, chunk;
+  size_t ml, o, total;
+};
+AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
+  AttendPlan p;
+  p.group = n_heads / b.n_kv;
+  const int rows = max_q * p.group;
+  p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  p.mblocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
+  // enough workgroups for the chip, of at least 128 rows (one step of the four waves)
+  const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
+  const int64_t want = p.mt == 4 ? 512 : 1024;
+  const int most = (b.max_len + 127) / 128;
+  int64_t s = (want + units - 1) / units;
+  if (s > most) s = most;
+  p.chunk = (int)((((int64_t)b.max_len + s - 1) / s + 127) / 128 * 128);
+  p.splits = (b.max_len + p.chunk - 1) / p.chunk;
+  const size_t parts = p.splits > 1 ? (size_t)b.batch * b.n_kv * p.splits * rows : 0;
+  p.ml = kStatusBytes;
+  p.o = p.ml + align256(parts * sizeof(float2));
+  p.total = p.o + align256(parts * b.hd * sizeof(float));
+  return p;
+}
+
+template <int HD, int MT>
+void launch_tiles(const AttendArgs& a, unsigned grid, hipStream_t stream) {
+  if (a.out)
+    hipLaunchKernelGGL((attend_kernel<HD, MT, true>), dim3(grid), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<HD, MT, false>), dim3(grid), dim3(kThreads), 0, stream, a);
+}
+
+template <int HD>
+void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStream_t stream) {
+  if (p.mt == 1)
+    launch_tiles<HD, 1>(a, grid, stream);
+  else if (p.mt == 2)
+    launch_tiles<HD, 2>(a, grid, stream);
+  else
+    launch_tiles<HD, 4>(a, grid, stream);
+  if (p.splits > 1) {
+    const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
+    hipLaunchKernelGGL((join_kernel<HD>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                       stream, a);
+  }
+}
+
+// The status word is written by a workgroup that scans the tables beside the others where that
+// takes no longer than they do (8,192 entries: a few microseconds); else cleared first.
+bool scans(const Batch& b) {
+  return (int64_t)b.batch * ((b.max_len + b.page_size - 1) / b.page_size) <= 8192;
 }
 
 }  // namespace
 
-size_t attend_workspace(const Batch&, int, int) { return kStatusBytes; }
-size_t weight_workspace(const Batch&, int, int) { return kStatusBytes; }
+size_t attend_workspace(const Batch& b, int n_heads, int max_q) {
+  return attend_plan(b, n_heads, max_q).total;
+}
 
 hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp, const Queries& q,
                          uint16_t* out, int64_t out_stride, float* lse, void* ws,
                          hipStream_t stream) {
-  unsigned* status = static_cast<unsigned*>(ws);
-  const hipError_t e = launch_clear_status(status, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(attend_plain_kernel, dim3(q.max_q, q.n_heads, b.batch), dim3(64), 0, stream, b,
-                     kp, vp, q, out, out_stride, lse, status);
-  return hipGetLastError();
-}
-
-hipError_t launch_weight(const Batch& b, const uint16_t* kp, const Queries& q, const float* lse,
-                         float decay, const float* acc, float* acc_out, int64_t acc_stride,
-                         void* ws, hipStream_t stream) {
-  unsigned* status = static_cast<unsigned*>(ws);
-  const hipError_t e = launch_clear_status(status, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(weight_plain_kernel, dim3(b.max_len, b.batch), dim3(64), 0, stream, b, kp, q,
-                     lse, decay, acc, acc_out, acc_stride, status);
+  const AttendPlan p = attend_plan(b, q.n_heads, q.max_q);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  AttendArgs a = {};
+  a.b = b;
+  a.q = q;
+  a.kp = kp;
+  a.vp = vp;
+  a.out = out;
+  a.lse = lse;
+  a.status = reinterpret_cast<unsigned*>(w);
+  a.part_ml = reinterpret_cast<float2*>(w + p.ml);
+  a.part_o = reinterpret_cast<float*>(w + p.o);
+  a.out_stride = out_stride;
+  a.page = divide_by((unsigned)b.page_size);
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  a.mblocks = p.mblocks;
+  a.group = p.group;
+  a.scan = scans(b) ? 1 : 0;
+  if (!a.scan) {
+    const hipError_t e = launch_clear_status(a.status, stream);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t grid = (int64_t)b.batch * b.n_kv * p.splits * p.mblocks + a.scan;
+  if (b.hd == 128)
+    launch_head<128>(a, p, (unsigned)grid, stream);
+  else
+    launch_head<64>(a, p, (unsigned)grid, stream);
   return hipGetLastError();
 }
 
