@@ -22,8 +22,7 @@
 // The wave loads the next 32 rows while it computes; block-table entries are read two steps
 // ahead.  A workgroup's four waves take the 32-row tiles of its row range in turn and are joined
 // in LDS; long caches are split over workgroups, whose partial results (fp32) a second kernel joins.
-#include "rf_cache.h"
-#include "rf_common.h"
+#include "rf_cache_dev.h"
 
 namespace rf {
 
@@ -32,22 +31,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32;             // cache rows of one step of a wave
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-// Division of 0 .. 2^31 - 1 by a divisor known on the host: (mulhi(x, m) + x) >> s.
-struct Divide {
-  unsigned m, s, d;
-};
-Divide divide_by(unsigned d) {
-  Divide v{0u, 0u, d};
-  while ((1ull << v.s) < d) ++v.s;
-  v.m = (unsigned)((((1ull << v.s) - d) << 32) / d + 1);
-  return v;
-}
-__device__ __forceinline__ unsigned quotient(unsigned x, Divide v) {
-  return (__umulhi(x, v.m) + x) >> v.s;
-}
 
 struct AttendArgs {
   Batch b;
@@ -66,42 +49,6 @@ struct AttendArgs {
   int group;                    // query heads of a key head
   int scan;                     // 1: the workgroup past the grid looks all pages over for the status
 };
-
-// Sequence `seq`: its length, first query and number of queries; false if it is to be skipped
-// (with *bad set where that is an error).
-__device__ __forceinline__ bool sequence_of(const Batch& b, const Queries& q, int seq, int* len,
-                                            int* first, int* n, bool* bad) {
-  *len = b.lengths[seq];
-  *first = q.start[seq];
-  const int end = q.start[seq + 1];
-  *n = (int)((unsigned)end - (unsigned)*first);
-  *bad = *len < 0 || *len > b.max_len || *first < 0 || end < *first || *n > q.max_q || *n > *len ||
-         end > q.n_q;
-  return !*bad && *n > 0;
-}
-
-// The status word from one workgroup: every sequence and every page that it uses.
-__device__ void scan_status(const Batch& b, const Queries& q, unsigned* status) {
-  int bits = 0;
-  for (int s = 0; s < b.batch; ++s) {
-    int len, first, n;
-    bool bad;
-    if (sequence_of(b, q, s, &len, &first, &n, &bad)) {
-      const int pages = (len + b.page_size - 1) / b.page_size;
-      for (int i = threadIdx.x; i < pages; i += blockDim.x) {
-        const int page = b.tables[(int64_t)s * b.table_stride + i];
-        if (page < 0 || page >= b.num_pages) bits = 1;
-      }
-    }
-    if (bad) bits = 1;
-  }
-  bits = __syncthreads_or(bits);
-  if (threadIdx.x == 0) *status = bits ? kStatusRowsBit : 0u;
-}
-
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
 
 __device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half) {
   return __builtin_amdgcn_perm(hi, lo, half ? 0x07060302u : 0x05040100u);
@@ -187,7 +134,7 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
     const int i = in ? m / a.group : 0, h = in ? kh * a.group + m % a.group : 0;
     const uint16_t* p = a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * g;
     qi[t] = i;
-    words[t] = a.q.mask ? a.q.mask[first + i] : (i < 63 ? (2ull << i) - 1 : ~0ull);
+    words[t] = draft_word(a.q, first + i, i);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       u32x4 w = {0u, 0u, 0u, 0u};
@@ -281,16 +228,7 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
       uint32_t seen = 0xffffffffu;                    // rows that this lane's query sees
       if (masked) {
         seen = there;
-        if (base + kRows > ctx) {
-          const int d = base - ctx;                   // draft of the step's first row
-          uint64_t w = words[t];
-          uint32_t vis;
-          if (d >= 0)
-            vis = d < 64 ? (uint32_t)(w >> d) : 0u;
-          else
-            vis = (uint32_t)(w << -d) | ((1u << -d) - 1u);
-          seen &= vis;
-        }
+        if (base + kRows > ctx) seen &= seen_rows(words[t], base - ctx);
       }
       float x[8], top = -INFINITY;
 #pragma unroll
@@ -527,12 +465,6 @@ void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStr
     hipLaunchKernelGGL((join_kernel<HD>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
                        stream, a);
   }
-}
-
-// The status word is written by a workgroup that scans the tables beside the others where that
-// takes no longer than they do (8,192 entries: a few microseconds); else cleared first.
-bool scans(const Batch& b) {
-  return (int64_t)b.batch * ((b.max_len + b.page_size - 1) / b.page_size) <= 8192;
 }
 
 }  // namespace

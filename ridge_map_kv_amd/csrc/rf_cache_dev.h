@@ -1,0 +1,80 @@
+// Device helpers shared by the kernels that read the paged cache.
+#pragma once
+
+#include "rf_cache.h"
+#include "rf_common.h"
+
+namespace rf {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Division of 0 .. 2^31 - 1 by a divisor known on the host: (mulhi(x, m) + x) >> s.
+struct Divide {
+  unsigned m, s, d;
+};
+inline Divide divide_by(unsigned d) {
+  Divide v{0u, 0u, d};
+  while ((1ull << v.s) < d) ++v.s;
+  v.m = (unsigned)((((1ull << v.s) - d) << 32) / d + 1);
+  return v;
+}
+__device__ __forceinline__ unsigned quotient(unsigned x, Divide v) {
+  return (__umulhi(x, v.m) + x) >> v.s;
+}
+
+// Sequence `seq`: its length, first query and number of queries; false if it is to be skipped
+// (with *bad set where that is an error).
+__device__ __forceinline__ bool sequence_of(const Batch& b, const Queries& q, int seq, int* len,
+                                            int* first, int* n, bool* bad) {
+  *len = b.lengths[seq];
+  *first = q.start[seq];
+  const int end = q.start[seq + 1];
+  *n = (int)((unsigned)end - (unsigned)*first);
+  *bad = *len < 0 || *len > b.max_len || *first < 0 || end < *first || *n > q.max_q || *n > *len ||
+         end > q.n_q;
+  return !*bad && *n > 0;
+}
+
+// What a query sees of its sequence's drafts, a bit each: its word of the mask, or a chain.
+__device__ __forceinline__ uint64_t draft_word(const Queries& q, int query, int i) {
+  return q.mask ? q.mask[query] : i < 63 ? (2ull << i) - 1 : ~0ull;
+}
+
+// Which of the 32 cache rows from `base` on a query sees; d = base less the row of the first
+// draft, > -32.
+__device__ __forceinline__ uint32_t seen_rows(uint64_t word, int d) {
+  if (d >= 0) return d < 64 ? (uint32_t)(word >> d) : 0u;
+  return (uint32_t)(word << -d) | ((1u << -d) - 1u);
+}
+
+// The status word from one workgroup: every sequence and every page that it uses.
+__device__ inline void scan_status(const Batch& b, const Queries& q, unsigned* status) {
+  int bits = 0;
+  for (int s = 0; s < b.batch; ++s) {
+    int len, first, n;
+    bool bad;
+    if (sequence_of(b, q, s, &len, &first, &n, &bad)) {
+      const int pages = (len + b.page_size - 1) / b.page_size;
+      for (int i = threadIdx.x; i < pages; i += blockDim.x) {
+        const int page = b.tables[(int64_t)s * b.table_stride + i];
+        if (page < 0 || page >= b.num_pages) bits = 1;
+      }
+    }
+    if (bad) bits = 1;
+  }
+  bits = __syncthreads_or(bits);
+  if (threadIdx.x == 0) *status = bits ? kStatusRowsBit : 0u;
+}
+
+// The status word is written by a workgroup that scans the tables beside the others where that
+// takes no longer than they do (8,192 entries: a few microseconds); else cleared first.
+inline bool scans(const Batch& b) {
+  return (int64_t)b.batch * ((b.max_len + b.page_size - 1) / b.page_size) <= 8192;
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+}  // namespace rf

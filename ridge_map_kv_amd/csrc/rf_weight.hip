@@ -1,91 +1,384 @@
 // The attention weight that the rows of the paged cache receive, on gfx950 (section "Which
-// rows to compute exactly" of the English RidgeFill review).
+// rows to compute exactly" of the English RidgeFill review: the attention that a prompt's last
+// tokens pay to its rows ranks them).
 //
-// The plain kernel: one wave per row adds up the weights of all queries and heads.
-#include "rf_cache.h"
-#include "rf_common.h"
+// With the queries' log-sum-exp at hand one pass over K suffices: a row's weight is the sum of
+// exp(scale q.k - lse) over the queries and heads.  As in the attention, the n queries of a
+// sequence and the G query heads of one key head are M = n G rows of a matrix Q, and a wave
+// computes S^T = K Q^T (16x16x32 MFMAs, A = 16 cache rows straight from memory, B = 16 query
+// rows): lane (c, g) holds rows 4 g + r of query c, so the sum over queries is a lane's own
+// over the query tiles, and one over the 16 lanes c at the end.  Sums run in a fixed order.
+//
+// M <= 64 (decoding, small trees): bound by the read of K.  A workgroup takes 64 or more cache
+// rows and all key heads (its waves share them out), joins the heads in LDS and writes the
+// accumulated weight: one launch.
+// M > 64: bound by the exponentials (16 cycles a wave of 64) and the matrix cores.  Q of one key
+// head (256 rows a block) lies in LDS and a workgroup walks a long range of cache rows with it;
+// the heads' sums meet in a second launch.
+#include "rf_cache_dev.h"
 
 namespace rf {
 
 namespace {
 
-__device__ __forceinline__ int pool_slot(const Batch& b, int seq, int row) {
-  const int page = b.tables[(int64_t)seq * b.table_stride + row / b.page_size];
-  if (page < 0 || page >= b.num_pages) return -1;
-  return page * b.page_size + row % b.page_size;
-}
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 64;             // cache rows of one step of a wave
+constexpr int kBlock = 256;           // query rows in LDS
 
-// Sequence `seq`: its length, its queries; false if it is to be skipped (with *bad set where
-// that is an error).
-__device__ __forceinline__ bool sequence_of(const Batch& b, const Queries& q, int seq, int* len,
-                                            int* first, int* n, bool* bad) {
-  *len = b.lengths[seq];
-  *first = q.start[seq];
-  *n = q.start[seq + 1] - *first;
-  *bad = *len < 0 || *len > b.max_len || *first < 0 || *n < 0 || *n > q.max_q || *n > *len ||
-         (int64_t)*first + *n > q.n_q;
-  return !*bad && *n > 0;
-}
+struct WeightArgs {
+  Batch b;
+  Queries q;
+  const uint16_t* kp;
+  const float* lse;
+  const float* acc;
+  float* acc_out;
+  unsigned* status;
+  float* part;                  // [batch][n_kv mblocks][max_len]
+  int64_t acc_stride;
+  Divide page;
+  float decay;
+  int chunk, splits;            // cache rows of a workgroup, workgroups along them
+  int mblocks, group;
+  int scan;
+};
 
-__device__ __forceinline__ bool sees(const Queries& q, int query, int i, int draft) {
-  if (draft < 0) return true;
-  return q.mask ? (q.mask[query] >> draft) & 1 : draft <= i;
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+// Sum over the 16 lanes of a row of the wave, in every one of them.
+__device__ __forceinline__ float sum16(float v) {
+#define RF_ROR(n) \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + n, 0xf, 0xf, false))
+  RF_ROR(8);
+  RF_ROR(4);
+  RF_ROR(2);
+  RF_ROR(1);
+#undef RF_ROR
   return v;
 }
 
-__global__ void weight_plain_kernel(Batch b, const uint16_t* kp, Queries q, const float* lse,
-                                    float decay, const float* acc, float* acc_out,
-                                    int64_t acc_stride, unsigned* status) {
-  const int seq = blockIdx.y, t = blockIdx.x, lane = threadIdx.x;
+// What a query sees of the 64 cache rows from `base` on, d = base less the first draft's row.
+__device__ __forceinline__ uint64_t seen64(uint64_t word, int d) {
+  if (d >= 0) return d < 64 ? word >> d : 0ull;
+  return d <= -64 ? ~0ull : word << -d | ((1ull << -d) - 1ull);
+}
+
+template <int HD>
+struct Keys {                   // 64 cache rows of one head
+  u32x4 k[4][HD / 32];          // rows 16 t + c, features 32 s + 8 g ..
+};
+
+template <int HD>
+__device__ __forceinline__ void load_keys(Keys<HD>& t, const uint16_t* kh, int64_t row, int slot,
+                                          int c, int g) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint16_t* p = kh + (int64_t)__shfl(slot, 16 * h + c) * row + 8 * g;
+#pragma unroll
+    for (int s = 0; s < HD / 32; ++s) t.k[h][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
+  }
+}
+
+// Adds the weights that 16 queries give to the 64 rows.  `some`: not all of them see all rows;
+// then `seen` says which (0 for a lane without a query or whose query sees nothing).
+template <int HD>
+__device__ __forceinline__ void add_weights(const Keys<HD>& keys, const bf16x8 (&q)[HD / 32],
+                                            float scale2, float lse2, bool some, uint64_t seen,
+                                            int g, float (&w)[4][4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < HD / 32; ++st) s = mfma16(__builtin_bit_cast(bf16x8, keys.k[t][st]), q[st], s);
+    if (!some) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[t][r] += __builtin_amdgcn_exp2f(fmaf(s[r], scale2, -lse2));
+    } else {
+      const uint32_t bits = (uint32_t)(seen >> (16 * t + 4 * g));
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        w[t][r] += bits >> r & 1 ? __builtin_amdgcn_exp2f(fmaf(s[r], scale2, -lse2)) : 0.f;
+    }
+  }
+}
+
+// Pool slot of cache row `row`; -1 past the last row and on a bad page (*err).
+__device__ __forceinline__ int key_slot(const WeightArgs& a, const int32_t* table, int row, int len,
+                                        bool* err) {
+  if (row >= len) return -1;
+  const int pi = (int)quotient((unsigned)row, a.page);
+  const int page = table[pi];
+  if (page < 0 || page >= a.b.num_pages) {
+    *err = true;
+    return -1;
+  }
+  return page * a.b.page_size + (row - pi * a.b.page_size);
+}
+
+// M <= 16 MT: workgroup = rows x all heads.  hw waves share the key heads, the others take
+// further rows.
+template <int HD, int MT>
+__global__ __launch_bounds__(kThreads) void weight_rows_kernel(WeightArgs a) {
+  constexpr int kSteps = HD / 32;
+  __shared__ float sh[kWaves][kRows];
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
+  const int seq = blockIdx.x / a.splits, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int hw = a.b.n_kv >= 4 ? 4 : a.b.n_kv >= 2 ? 2 : 1;
   int len, first, n;
   bool bad;
-  const bool go = sequence_of(b, q, seq, &len, &first, &n, &bad);
-  if (bad) atomicOr(status, kStatusRowsBit);
-  if (!go || t >= len) return;
-  const int per = b.hd / 64, group = q.n_heads / b.n_kv, ctx = len - n;
-  const int slot = pool_slot(b, seq, t);
-  float w = 0.f;
-  if (slot < 0) {
-    atomicOr(status, kStatusRowsBit);
-  } else {
-    for (int kh = 0; kh < b.n_kv; ++kh) {
-      const int64_t at = ((int64_t)slot * b.n_kv + kh) * b.hd + lane * per;
-      for (int i = 0; i < n; ++i) {
-        if (!sees(q, first + i, i, t - ctx)) continue;
-        for (int h = kh * group; h < (kh + 1) * group; ++h) {
-          const uint16_t* qp = q.q + (first + i) * q.q_stride + h * b.hd + lane * per;
-          const float l = lse[(int64_t)(first + i) * q.n_heads + h];
-          float s = 0.f;
-          for (int e = 0; e < per; ++e) s += bf16_to_f32(qp[e]) * bf16_to_f32(kp[at + e]);
-          s = wave_sum(s) * q.scale;
-          if (l != -INFINITY) w += expf(s - l);
-        }
+  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
+  if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  const int base = (blockIdx.x % a.splits) * a.chunk + wave / hw * kRows;
+  if (!go || (blockIdx.x % a.splits) * a.chunk >= len) return;
+  const int ctx = len - n, m_rows = n * a.group;
+  const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
+  bool err = false;
+  const int slot = key_slot(a, table, base + lane, len, &err);
+  const uint64_t there = __ballot(slot >= 0);
+  if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
+  const bool part_rows = ~there || base + kRows > ctx;
+
+  float w[4][4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[t][r] = 0.f;
+  const float scale2 = a.q.scale * kLog2e;
+  if (there) {
+    for (int kh = wave % hw; kh < a.b.n_kv; kh += hw) {
+      Keys<HD> keys;
+      load_keys<HD>(keys, a.kp + kh * HD, (int64_t)a.b.n_kv * HD, slot < 0 ? 0 : slot, c, g);
+#pragma unroll
+      for (int qt = 0; qt < MT; ++qt) {
+        const int m = 16 * qt + c;
+        if (16 * qt >= m_rows) break;
+        const bool in = m < m_rows;
+        const int i = in ? m / a.group : 0, h = kh * a.group + (in ? m % a.group : 0);
+        const uint16_t* p = a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * g;
+        bf16x8 q[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const bf16x8*>(p + 32 * s);
+        const float l = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] : -INFINITY;
+        const bool live = l != -INFINITY;
+        uint64_t seen = live ? there : 0ull;
+        if (base + kRows > ctx) seen &= seen64(draft_word(a.q, first + i, i), base - ctx);
+        add_weights<HD>(keys, q, scale2, l * kLog2e, part_rows || __any(!live), seen, g, w);
       }
     }
   }
-  if (lane == 0) {
-    const int64_t a = seq * acc_stride + t;
-    acc_out[a] = acc ? decay * acc[a] + w : w;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[t][r] = sum16(w[t][r]);
+      if (c == 0) sh[wave][16 * t + 4 * g + r] = w[t][r];
+    }
+  __syncthreads();
+  const int row = base + lane;
+  if (wave % hw == 0 && row < len) {
+    float v = 0.f;
+    for (int i = 0; i < hw; ++i) v += sh[wave + i][lane];
+    const int64_t at = seq * a.acc_stride + row;
+    a.acc_out[at] = a.acc ? a.decay * a.acc[at] + v : v;
+  }
+}
+
+// M > 64: workgroup = one key head, a block of its query rows, a range of cache rows.
+template <int HD>
+__global__ __launch_bounds__(kThreads, 2) void weight_heads_kernel(WeightArgs a) {
+  constexpr int kSteps = HD / 32;
+  __shared__ u32x4 sh_q[kBlock / 16][kSteps][64];   // as the lanes read them
+  __shared__ float sh_lse[kBlock];
+  __shared__ uint64_t sh_word[kBlock];
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
+  const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+  const int mb = unit % a.mblocks, kh = unit / a.mblocks % a.b.n_kv, seq = unit / a.mblocks / a.b.n_kv;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  int len, first, n;
+  bool bad;
+  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
+  if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  const int begin = split * a.chunk, m0 = mb * kBlock;
+  const int m_rows = n * a.group - m0 < kBlock ? n * a.group - m0 : kBlock;
+  if (!go || begin >= len || m_rows <= 0) return;
+  const int end = len < begin + a.chunk ? len : begin + a.chunk;
+  const int ctx = len - n, tiles = (m_rows + 15) / 16;
+
+  for (int x = threadIdx.x; x < tiles * 16 * (HD / 8); x += kThreads) {
+    const int m = x / (HD / 8), ch = x % (HD / 8);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (m < m_rows) {
+      const int i = (m0 + m) / a.group, h = kh * a.group + (m0 + m) % a.group;
+      v = *reinterpret_cast<const u32x4*>(a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * ch);
+    }
+    sh_q[m / 16][ch / 4][ch % 4 * 16 + m % 16] = v;
+  }
+  for (int m = threadIdx.x; m < tiles * 16; m += kThreads) {
+    const int i = (m0 + m) / a.group, h = kh * a.group + (m0 + m) % a.group;
+    const bool in = m < m_rows;
+    sh_lse[m] = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] : -INFINITY;
+    sh_word[m] = in ? draft_word(a.q, first + i, i) : 0ull;
+  }
+  __syncthreads();
+
+  const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
+  const uint16_t* kbase = a.kp + kh * HD;
+  const int64_t row_size = (int64_t)a.b.n_kv * HD;
+  float* part = a.part + ((int64_t)(seq * a.b.n_kv + kh) * a.mblocks + mb) * a.b.max_len;
+  const float scale2 = a.q.scale * kLog2e;
+  bool err = false;
+  int base = begin + wave * kRows;
+  Keys<HD> keys;
+  int slot = -1;
+  if (base < end) {
+    slot = key_slot(a, table, base + lane, len, &err);
+    load_keys<HD>(keys, kbase, row_size, slot < 0 ? 0 : slot, c, g);
+  }
+  for (; base < end; base += kWaves * kRows) {
+    const int ahead = base + kWaves * kRows;
+    int slot_next = -1;
+    Keys<HD> next;
+    if (ahead < end) {
+      slot_next = key_slot(a, table, ahead + lane, len, &err);
+      load_keys<HD>(next, kbase, row_size, slot_next < 0 ? 0 : slot_next, c, g);
+    }
+    const uint64_t there = __ballot(slot >= 0);
+    const bool part_rows = ~there || base + kRows > ctx;
+    float w[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[t][r] = 0.f;
+    for (int qt = 0; qt < tiles; ++qt) {
+      bf16x8 q[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(bf16x8, sh_q[qt][s][lane]);
+      const float l = sh_lse[16 * qt + c];
+      const bool live = l != -INFINITY;
+      uint64_t seen = live ? there : 0ull;
+      if (base + kRows > ctx) seen &= seen64(sh_word[16 * qt + c], base - ctx);
+      add_weights<HD>(keys, q, scale2, l * kLog2e, part_rows || __any(!live), seen, g, w);
+    }
+    f32x4 mine = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float v = sum16(w[t][r]);
+        if (c == t) mine[r] = v;
+      }
+    if (c < 4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = base + 16 * c + 4 * g + r;
+        if (row < len) part[row] = mine[r];
+      }
+    }
+    keys = next;
+    slot = slot_next;
+  }
+  if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
+}
+
+// The heads' sums, in order.
+__global__ __launch_bounds__(kThreads) void weight_sum_kernel(WeightArgs a) {
+  const int seq = blockIdx.y, row = blockIdx.x * kThreads + threadIdx.x;
+  int len, first, n;
+  bool bad;
+  if (!sequence_of(a.b, a.q, seq, &len, &first, &n, &bad) || row >= len) return;
+  const int live = (n * a.group + kBlock - 1) / kBlock;    // blocks of query rows
+  const float* p = a.part + (int64_t)seq * a.b.n_kv * a.mblocks * a.b.max_len + row;
+  float v = 0.f;
+  for (int kh = 0; kh < a.b.n_kv; ++kh)
+    for (int mb = 0; mb < live; ++mb) v += p[(int64_t)(kh * a.mblocks + mb) * a.b.max_len];
+  const int64_t at = seq * a.acc_stride + row;
+  a.acc_out[at] = a.acc ? a.decay * a.acc[at] + v : v;
+}
+
+struct WeightPlan {
+  int group, mt, mblocks, chunk, splits;    // mt 0: with Q in LDS
+  size_t part, total;
+};
+WeightPlan weight_plan(const Batch& b, int n_heads, int max_q) {
+  WeightPlan p;
+  p.group = n_heads / b.n_kv;
+  const int rows = max_q * p.group;
+  p.part = kStatusBytes;
+  if (rows <= 64) {
+    p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.mblocks = 1;
+    p.chunk = kRows * (b.n_kv >= 4 ? 1 : b.n_kv >= 2 ? 2 : 4);
+    p.splits = (b.max_len + p.chunk - 1) / p.chunk;
+    p.total = p.part;
+    return p;
+  }
+  p.mt = 0;
+  p.mblocks = (rows + kBlock - 1) / kBlock;
+  // two workgroups to a compute unit, each of at least one step of its waves
+  const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
+  int64_t s = (512 + units - 1) / units;
+  const int step = kWaves * kRows, most = (b.max_len + step - 1) / step;
+  if (s > most) s = most;
+  p.chunk = (int)((((int64_t)b.max_len + s - 1) / s + step - 1) / step * step);
+  p.splits = (b.max_len + p.chunk - 1) / p.chunk;
+  p.total = p.part + align256((size_t)units * b.max_len * sizeof(float));
+  return p;
+}
+
+template <int HD>
+void launch_weight_head(const WeightArgs& a, const WeightPlan& p, hipStream_t stream) {
+  const int64_t units = p.mt ? a.b.batch : (int64_t)a.b.batch * a.b.n_kv * p.mblocks;
+  const dim3 grid((unsigned)(units * p.splits + a.scan)), block(kThreads);
+  if (p.mt == 1) {
+    hipLaunchKernelGGL((weight_rows_kernel<HD, 1>), grid, block, 0, stream, a);
+  } else if (p.mt == 2) {
+    hipLaunchKernelGGL((weight_rows_kernel<HD, 2>), grid, block, 0, stream, a);
+  } else if (p.mt == 4) {
+    hipLaunchKernelGGL((weight_rows_kernel<HD, 4>), grid, block, 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((weight_heads_kernel<HD>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL(weight_sum_kernel, dim3((a.b.max_len + kThreads - 1) / kThreads, a.b.batch),
+                       block, 0, stream, a);
   }
 }
 
 }  // namespace
 
-size_t weight_workspace(const Batch&, int, int) { return kStatusBytes; }
+size_t weight_workspace(const Batch& b, int n_heads, int max_q) {
+  return weight_plan(b, n_heads, max_q).total;
+}
 
 hipError_t launch_weight(const Batch& b, const uint16_t* kp, const Queries& q, const float* lse,
                          float decay, const float* acc, float* acc_out, int64_t acc_stride,
                          void* ws, hipStream_t stream) {
-  unsigned* status = static_cast<unsigned*>(ws);
-  const hipError_t e = launch_clear_status(status, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(weight_plain_kernel, dim3(b.max_len, b.batch), dim3(64), 0, stream, b, kp, q,
-                     lse, decay, acc, acc_out, acc_stride, status);
+  const WeightPlan p = weight_plan(b, q.n_heads, q.max_q);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  WeightArgs a = {};
+  a.b = b;
+  a.q = q;
+  a.kp = kp;
+  a.lse = lse;
+  a.acc = acc;
+  a.acc_out = acc_out;
+  a.status = reinterpret_cast<unsigned*>(w);
+  a.part = reinterpret_cast<float*>(w + p.part);
+  a.acc_stride = acc_stride;
+  a.page = divide_by((unsigned)b.page_size);
+  a.decay = decay;
+  a.chunk = p.chunk;
+  a.splits = p.splits;
+  a.mblocks = p.mblocks;
+  a.group = p.group;
+  a.scan = scans(b) ? 1 : 0;
+  if (!a.scan) {
+    const hipError_t e = launch_clear_status(a.status, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (b.hd == 128)
+    launch_weight_head<128>(a, p, stream);
+  else
+    launch_weight_head<64>(a, p, stream);
   return hipGetLastError();
 }
 
