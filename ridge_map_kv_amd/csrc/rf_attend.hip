@@ -54,6 +54,25 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half
   return __builtin_amdgcn_perm(hi, lo, half ? 0x07060302u : 0x05040100u);
 }
 
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// A workgroup's row range and block of query rows: the blocks of one range go to one XCD
+// (blockIdx % 8), side by side, where they share its cache.
+__device__ __forceinline__ void place_block(const AttendArgs& a, int* unit, int* mb) {
+  if (a.mblocks == 1) return;
+  const int per = 8 * a.mblocks, full = (a.b.batch * a.b.n_kv * a.splits) / 8 * per;
+  const int id = *unit;
+  if (id < full) {
+    *mb = id % per / 8;
+    *unit = id / per * 8 + id % 8;
+  } else {
+    *mb = (id - full) % a.mblocks;
+    *unit = full / a.mblocks + (id - full) / a.mblocks;
+  }
+}
+
 template <int HD>
 struct Tile {                   // 32 cache rows of one head, as a wave holds them
   static constexpr int kSteps = HD / 32;
@@ -95,19 +114,8 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   __shared__ float sh_o[kWaves / 2][16 * MT][HD + 4];
   __shared__ float2 sh_ml[kWaves / 2][16 * MT];
   if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
-  // blocks of query rows of one row range go to one XCD (blockIdx % 8), side by side
   int unit = blockIdx.x, mb = 0;
-  if (a.mblocks > 1) {
-    const int per = 8 * a.mblocks, full = (a.b.batch * a.b.n_kv * a.splits) / 8 * per;
-    if (unit < full) {
-      mb = unit % per / 8;
-      unit = unit / per * 8 + unit % 8;
-    } else {
-      const int rest = unit - full;
-      mb = rest % a.mblocks;
-      unit = full / a.mblocks + rest / a.mblocks;
-    }
-  }
+  place_block(a, &unit, &mb);
   const int split = unit % a.splits, sh = unit / a.splits;
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -375,6 +383,316 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   }
 }
 
+// More than 32 query rows: bound by the matrix cores and the exponentials, so K and V go
+// through LDS and are shared by the waves, each of which keeps 32 query rows (32x32x16 MFMAs,
+// the same transposed products: lane (q, h) = (lane % 32, lane / 32) of S^T holds cache rows
+// 8 (r / 4) + 4 h + r % 4, r < 16).  LDS holds the operands as the lanes read them, 16 bytes each in
+// a row: K as [32 rows][16 features] tiles, V already transposed, as [32 features][16 rows]
+// tiles whose feature d' of tile m is (hd / 32) d' + m.  A loading thread takes eight cache rows of
+// hd / 32 features (8 bytes a row at hd 128) and transposes them in registers on the way, once
+// for all waves.  The next 64 rows are loaded into registers during the products of one
+// buffer and written to the other: one barrier a step.
+constexpr int kTileRows = 64;
+
+template <int HD, int NW, bool kOut>
+__global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(AttendArgs a) {
+  constexpr int kS = HD / 16;                 // MFMA steps over the features
+  constexpr int kF = HD / 32;                 // feature tiles; features of a loaded unit
+  constexpr int kLoad = NW < 4 ? NW : 4;      // waves that load K, and that load V
+  constexpr int kUnits = 4 / kLoad;           // V units of a thread
+  constexpr int kChunks = kTileRows * HD / 8 / (64 * kLoad);   // 16-byte pieces of K of a thread
+  __shared__ u32x4 sh_k[2][2][kS][64];
+  __shared__ u32x4 sh_v[kOut ? 2 : 1][2][2][kOut ? kF : 1][64];
+  __shared__ int sh_wild[2];                  // the step whose V holds a value that is not finite
+  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
+  int unit = blockIdx.x, mb = 0;
+  place_block(a, &unit, &mb);
+  const int split = unit % a.splits, sh = unit / a.splits;
+  const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+
+  int len, first, n;
+  bool bad;
+  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
+  if (bad && !a.scan && tid == 0) atomicOr(a.status, kStatusRowsBit);
+  const int m_rows = n * a.group, m0 = mb * 32 * NW;
+  const int begin = split * a.chunk;
+  if (!go || m0 >= m_rows || (begin >= len && split > 0)) return;
+  const int end = len < begin + a.chunk ? len : begin + a.chunk;
+  const int ctx = len - n;
+
+  // this wave's 32 query rows; a negative scale turns their sign, so that the largest product
+  // is the largest score
+  const int m = m0 + 32 * wave + c;
+  const bool busy = m0 + 32 * wave < m_rows, in = m < m_rows;
+  const int qi = in ? m / a.group : 0;
+  const uint64_t word = draft_word(a.q, first + qi, qi);
+  const float scale2 = fabsf(a.q.scale) * kLog2e;
+  bf16x8 qf[kS];
+  {
+    const uint16_t* p = a.q.q + (int64_t)(first + qi) * a.q.q_stride + (kh * a.group + (in ? m % a.group : 0)) * HD + 8 * h;
+    const uint32_t flip = a.q.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (in) w = *reinterpret_cast<const u32x4*>(p + 16 * s) ^ flip;
+      qf[s] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+  f32x16 o[kOut ? kF : 1];
+#pragma unroll
+  for (int f = 0; f < (kOut ? kF : 1); ++f)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[f][r] = 0.f;
+  float m_run = -INFINITY, l_run = 0.f;
+
+  const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
+  const int64_t row_size = (int64_t)a.b.n_kv * HD;
+  const uint16_t* kbase = a.kp + kh * HD;
+  const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
+  bool err = false;
+  // lane's row of the step at `base`: its page, then its pool slot (-1: not there)
+  const auto page_of = [&](int base) -> int {
+    const int r = base + lane;
+    return table[quotient((unsigned)(r < len ? r : len - 1), a.page)];
+  };
+  const auto slot_of = [&](int base, int page) -> int {
+    const int r = base + lane;
+    if (r >= len) return -1;
+    if (page < 0 || page >= a.b.num_pages) {
+      err = true;
+      return -1;
+    }
+    return page * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
+  };
+
+  u32x4 kr[kChunks];
+  uint32_t vr[kUnits][8][kF / 2];
+  const bool loads_k = NW < 8 || wave >= 4, loads_v = kOut && (NW < 8 || wave < 4);
+  const int lt = NW < 8 ? tid : tid & 255;
+  const auto load = [&](int slot) {
+    const int s0 = slot < 0 ? 0 : slot;
+    if (loads_k) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int x = lt + 64 * kLoad * i;
+        kr[i] = *reinterpret_cast<const u32x4*>(kbase + (int64_t)__shfl(s0, x / (HD / 8)) * row_size + x % (HD / 8) * 8);
+      }
+    }
+    if (loads_v) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = lt + 64 * kLoad * i;              // (group, x, h) of eight rows, features
+        const int r0 = (u >> 7) * 32 + (u >> 6 & 1) * 16 + (u >> 5 & 1) * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint16_t* p = vbase + (int64_t)__shfl(s0, r0 + 8 * (j / 4) + j % 4) * row_size + (u & 31) * kF;
+          if constexpr (HD == 128) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+            vr[i][j][0] = w[0];
+            vr[i][j][1] = w[1];
+          } else {
+            vr[i][j][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+        }
+      }
+    }
+  };
+  // `masked`: not all of the step's rows are there and seen by every query
+  const auto park = [&](int buf, int step, uint64_t there, bool masked) {
+    if (loads_k) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int x = lt + 64 * kLoad * i, row = x / (HD / 8), ch = x % (HD / 8);
+        sh_k[buf][row >> 5][ch >> 1][(((ch & 1) << 5) | (row & 31)) ^ (ch >> 1 & 7)] = kr[i];
+      }
+    }
+    if constexpr (kOut) {
+      if (loads_v) {
+        bool wild = false;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          const int u = lt + 64 * kLoad * i, grp = u >> 7, x = u >> 6 & 1, hh = u >> 5 & 1;
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bool is = there >> (grp * 32 + x * 16 + hh * 4 + 8 * (j / 4) + j % 4) & 1;
+#pragma unroll
+              for (int e = 0; e < kF / 2; ++e) {
+                if (!is) vr[i][j][e] = 0u;
+                wild |= (vr[i][j][e] & 0x7f80u) == 0x7f80u || (vr[i][j][e] & 0x7f800000u) == 0x7f800000u;
+              }
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < kF; ++f) {
+            u32x4 w;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) w[p] = half_pair(vr[i][2 * p][f / 2], vr[i][2 * p + 1][f / 2], f & 1);
+            sh_v[buf][grp][x][f][hh << 5 | (u & 31)] = w;
+          }
+        }
+        if (wild) sh_wild[buf] = step;
+      }
+    }
+  };
+
+  if (tid < 2) sh_wild[tid] = -1;
+  __syncthreads();
+  int slot = slot_of(begin, page_of(begin));
+  load(slot);
+  uint64_t there = __ballot(slot >= 0);
+  bool masked = ~there || begin + kTileRows > ctx;
+  park(0, begin, there, masked);
+  int page_next = page_of(begin + kTileRows);
+  __syncthreads();
+  int buf = 0;
+  for (int base = begin; base < end; base += kTileRows, buf ^= 1) {
+    const bool more = base + kTileRows < end;
+    int slot_next = -1;
+    if (more) {
+      slot_next = slot_of(base + kTileRows, page_next);
+      load(slot_next);
+      page_next = page_of(base + 2 * kTileRows);
+    }
+    if (busy) {
+      f32x16 s[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[e][r] = 0.f;
+#pragma unroll
+      for (int st = 0; st < kS; ++st)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          s[e] = mfma32(__builtin_bit_cast(bf16x8, sh_k[buf][e][st][lane ^ (st & 7)]), qf[st], s[e]);
+      uint64_t seen = ~0ull;
+      if (masked) {
+        seen = there;
+        if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (!(bits >> (8 * (r / 4) + r % 4) & 1)) s[e][r] = -INFINITY;
+        }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // 0 times an infinite product is NaN only where the product is a score
+      top = top == -INFINITY ? top : top * scale2;
+      const float m_new = fmaxf(m_run, top);
+      const float zero = m_new == -INFINITY ? 0.f : m_new;
+      if (__any(m_new > m_run)) {
+        const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
+        l_run *= shrink;
+        if constexpr (kOut) {
+#pragma unroll
+          for (int f = 0; f < kF; ++f) o[f] *= shrink;
+        }
+      }
+      m_run = m_new;
+      float sum = 0.f;
+      u32x4 pw[4];                                    // cache rows 16 x .. of group e: [2 e + x]
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+          float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
+          float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
+          if (masked && a.q.scale == 0.f) {           // -inf times a scale of 0
+            const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
+            if (!(bits >> (8 * (r / 4) + r % 4) & 1)) p0 = 0.f;
+            if (!(bits >> (8 * (r / 4) + r % 4 + 1) & 1)) p1 = 0.f;
+          }
+          sum += p0 + p1;
+          if constexpr (kOut) pw[2 * e + r / 8][r % 8 / 2] = pack_bf16x2(p0, p1);
+        }
+      l_run += sum;
+      if constexpr (kOut) {
+        if (!masked || sh_wild[buf] != base) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int f = 0; f < kF; ++f)
+              o[f] = mfma32(__builtin_bit_cast(bf16x8, sh_v[buf][e >> 1][e & 1][f][lane]),
+                            __builtin_bit_cast(bf16x8, pw[e]), o[f]);
+        } else {
+          // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
+          // for the queries that see the row.
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            for (int r = 0; r < 16; ++r) {
+              const int hh = r / 4 & 1, j = r / 8 * 4 + r % 4;
+              const bool vis = seen >> (16 * e + r) & 1;
+              const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
+              u32x4 pr;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) pr[i] = h == hh && i == j / 2 ? pw[e][i] & keep : 0u;
+#pragma unroll
+              for (int f = 0; f < kF; ++f) {
+                const u32x4 vw = sh_v[buf][e >> 1][e & 1][f][lane];
+                u32x4 vone;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vone[i] = h == hh && i == j / 2 ? vw[i] & keep : 0u;
+                f32x16 add;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) add[i] = 0.f;
+                add = mfma32(__builtin_bit_cast(bf16x8, vone), __builtin_bit_cast(bf16x8, pr), add);
+                if (vis) o[f] += add;
+              }
+            }
+        }
+      }
+    }
+    if (more) {
+      there = __ballot(slot_next >= 0);
+      masked = ~there || base + 2 * kTileRows > ctx;
+      park(buf ^ 1, base + kTileRows, there, masked);
+    }
+    __syncthreads();
+  }
+  if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
+  if (!busy) return;
+
+  l_run += __shfl_xor(l_run, 32);
+  if (!in) return;
+  const int head = kh * a.group + m % a.group;
+  const int64_t row = first + qi, part = ((int64_t)sh * a.splits + split) * (a.q.max_q * a.group) + m;
+  if (a.splits > 1) {
+    if (h == 0) a.part_ml[part] = make_float2(m_run, l_run);
+  } else if (a.lse && h == 0) {
+    a.lse[row * a.q.n_heads + head] = l_run == 0.f ? -INFINITY : m_run * kLn2 + __logf(l_run);
+  }
+  if constexpr (kOut) {
+    // lane (q, h) holds features 8 kF b + 4 kF h + kF r + f for r < 4, f < kF of each b < 4
+    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = kF * (8 * b + 4 * h + r);
+        if (a.splits > 1) {
+          float* p = a.part_o + part * HD + d;
+#pragma unroll
+          for (int f = 0; f < kF; ++f) p[f] = o[f][4 * b + r];
+        } else {
+          uint16_t* p = a.out + row * a.out_stride + head * HD + d;
+#pragma unroll
+          for (int f = 0; f < kF; f += 2)
+            *reinterpret_cast<uint32_t*>(p + f) =
+                l_run == 0.f ? 0u : pack_bf16x2(o[f][4 * b + r] * inv, o[f + 1][4 * b + r] * inv);
+        }
+      }
+  }
+}
+
 // Joins the splits of one output row per wave.
 template <int HD>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
@@ -420,18 +738,19 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
 
 // How a call is laid out.
 struct AttendPlan {
-  int mt, mblocks, group, splits, chunk;
+  int rows;                     // query rows of a workgroup
+  int mblocks, group, splits, chunk;
   size_t ml, o, total;
 };
 AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
   AttendPlan p;
   p.group = n_heads / b.n_kv;
   const int rows = max_q * p.group;
-  p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.mblocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
-  // enough workgroups for the chip, of at least 128 rows (one step of the four waves)
+  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  p.mblocks = (rows + p.rows - 1) / p.rows;
+  // enough workgroups for the chip, of at least 128 rows (one step of four waves)
   const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
-  const int64_t want = p.mt == 4 ? 512 : 1024;
+  const int64_t want = p.rows == 16 ? 1024 : p.rows <= 128 ? 512 : 256;
   const int most = (b.max_len + 127) / 128;
   int64_t s = (want + units - 1) / units;
   if (s > most) s = most;
@@ -444,22 +763,26 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
   return p;
 }
 
-template <int HD, int MT>
-void launch_tiles(const AttendArgs& a, unsigned grid, hipStream_t stream) {
-  if (a.out)
-    hipLaunchKernelGGL((attend_kernel<HD, MT, true>), dim3(grid), dim3(kThreads), 0, stream, a);
+template <int HD, bool kOut>
+void launch_rows(const AttendArgs& a, int rows, unsigned grid, hipStream_t stream) {
+  if (rows == 16)
+    hipLaunchKernelGGL((attend_kernel<HD, 1, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
+  else if (rows == 32)
+    hipLaunchKernelGGL((attend_kernel<HD, 2, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
+  else if (rows == 64)
+    hipLaunchKernelGGL((attend_tile_kernel<HD, 2, kOut>), dim3(grid), dim3(128), 0, stream, a);
+  else if (rows == 128)
+    hipLaunchKernelGGL((attend_tile_kernel<HD, 4, kOut>), dim3(grid), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((attend_kernel<HD, MT, false>), dim3(grid), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_tile_kernel<HD, 8, kOut>), dim3(grid), dim3(512), 0, stream, a);
 }
 
 template <int HD>
 void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStream_t stream) {
-  if (p.mt == 1)
-    launch_tiles<HD, 1>(a, grid, stream);
-  else if (p.mt == 2)
-    launch_tiles<HD, 2>(a, grid, stream);
+  if (a.out)
+    launch_rows<HD, true>(a, p.rows, grid, stream);
   else
-    launch_tiles<HD, 4>(a, grid, stream);
+    launch_rows<HD, false>(a, p.rows, grid, stream);
   if (p.splits > 1) {
     const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
     hipLaunchKernelGGL((join_kernel<HD>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,

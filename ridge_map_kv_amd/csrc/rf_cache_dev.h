@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t seen_rows(uint64_t word, int d) {
   return (uint32_t)(word << -d) | ((1u << -d) - 1u);
 }
 
+// What a query sees of the 64 cache rows from `base` on, d = base less the first draft's row.
+__device__ __forceinline__ uint64_t seen64(uint64_t word, int d) {
+  if (d >= 0) return d < 64 ? word >> d : 0ull;
+  return d <= -64 ? ~0ull : word << -d | ((1ull << -d) - 1ull);
+}
+
 // The status word from one workgroup: every sequence and every page that it uses.
 __device__ inline void scan_status(const Batch& b, const Queries& q, unsigned* status) {
   int bits = 0;

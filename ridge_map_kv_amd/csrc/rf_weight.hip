@@ -55,12 +55,6 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// What a query sees of the 64 cache rows from `base` on, d = base less the first draft's row.
-__device__ __forceinline__ uint64_t seen64(uint64_t word, int d) {
-  if (d >= 0) return d < 64 ? word >> d : 0ull;
-  return d <= -64 ? ~0ull : word << -d | ((1ull << -d) - 1ull);
-}
-
 template <int HD>
 struct Keys {                   // 64 cache rows of one head
   u32x4 k[4][HD / 32];          // rows 16 t + c, features 32 s + 8 g ..
