@@ -58,6 +58,14 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// The same value, unknown to the compiler: what is formed from it in a loop is formed there
+// and not before the loop, where it would stay in registers all along and push others out (a
+// reload of those would wait for the rows in flight).
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // A workgroup's row range and block of query rows: the blocks of one range go to one XCD
 // (blockIdx % 8), side by side, where they share its cache.
 __device__ __forceinline__ void place_block(const AttendArgs& a, int* unit, int* mb) {
@@ -423,12 +431,12 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
   const int ctx = len - n;
 
   // this wave's 32 query rows; a negative scale turns their sign, so that the largest product
-  // is the largest score
+  // is the largest score, and a scale of 0 makes them 0
   const int m = m0 + 32 * wave + c;
   const bool busy = m0 + 32 * wave < m_rows, in = m < m_rows;
   const int qi = in ? m / a.group : 0;
   const uint64_t word = draft_word(a.q, first + qi, qi);
-  const float scale2 = fabsf(a.q.scale) * kLog2e;
+  const float scale2 = (a.q.scale == 0.f ? 1.f : fabsf(a.q.scale)) * kLog2e;
   bf16x8 qf[kS];
   {
     const uint16_t* p = a.q.q + (int64_t)(first + qi) * a.q.q_stride + (kh * a.group + (in ? m % a.group : 0)) * HD + 8 * h;
@@ -436,7 +444,7 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
       u32x4 w = {0u, 0u, 0u, 0u};
-      if (in) w = *reinterpret_cast<const u32x4*>(p + 16 * s) ^ flip;
+      if (in && a.q.scale != 0.f) w = *reinterpret_cast<const u32x4*>(p + 16 * s) ^ flip;
       qf[s] = __builtin_bit_cast(bf16x8, w);
     }
   }
@@ -467,17 +475,22 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
     return page * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
   };
 
-  u32x4 kr[kChunks];
-  uint32_t vr[kUnits][8][kF / 2];
+  // rows on their way; with 8 waves four carry K and four V, in the same registers
+  constexpr int kKWords = 4 * kChunks, kVWords = kUnits * 4 * kF;
+  uint32_t held[NW < 8 && kOut ? kKWords + kVWords : kKWords > kVWords ? kKWords : kVWords];
+  uint32_t* const kr = held;
+  uint32_t* const vr = NW < 8 ? held + kKWords : held;
   const bool loads_k = NW < 8 || wave >= 4, loads_v = kOut && (NW < 8 || wave < 4);
-  const int lt = NW < 8 ? tid : tid & 255;
+  const int lt0 = NW < 8 ? tid : tid & 255;
   const auto load = [&](int slot) {
-    const int s0 = slot < 0 ? 0 : slot;
+    const int s0 = slot < 0 ? 0 : slot, lt = fresh(lt0);
     if (loads_k) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int x = lt + 64 * kLoad * i;
-        kr[i] = *reinterpret_cast<const u32x4*>(kbase + (int64_t)__shfl(s0, x / (HD / 8)) * row_size + x % (HD / 8) * 8);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(kbase + (int64_t)__shfl(s0, x / (HD / 8)) * row_size + x % (HD / 8) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kr[4 * i + e] = w[e];
       }
     }
     if (loads_v) {
@@ -490,10 +503,10 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
           const uint16_t* p = vbase + (int64_t)__shfl(s0, r0 + 8 * (j / 4) + j % 4) * row_size + (u & 31) * kF;
           if constexpr (HD == 128) {
             const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-            vr[i][j][0] = w[0];
-            vr[i][j][1] = w[1];
+            vr[(i * 8 + j) * 2] = w[0];
+            vr[(i * 8 + j) * 2 + 1] = w[1];
           } else {
-            vr[i][j][0] = *reinterpret_cast<const uint32_t*>(p);
+            vr[i * 8 + j] = *reinterpret_cast<const uint32_t*>(p);
           }
         }
       }
@@ -501,11 +514,13 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
   };
   // `masked`: not all of the step's rows are there and seen by every query
   const auto park = [&](int buf, int step, uint64_t there, bool masked) {
+    const int lt = fresh(lt0);
     if (loads_k) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int x = lt + 64 * kLoad * i, row = x / (HD / 8), ch = x % (HD / 8);
-        sh_k[buf][row >> 5][ch >> 1][(((ch & 1) << 5) | (row & 31)) ^ (ch >> 1 & 7)] = kr[i];
+        sh_k[buf][row >> 5][ch >> 1][(((ch & 1) << 5) | (row & 31)) ^ (ch >> 1 & 7)] =
+            u32x4{kr[4 * i], kr[4 * i + 1], kr[4 * i + 2], kr[4 * i + 3]};
       }
     }
     if constexpr (kOut) {
@@ -520,8 +535,9 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
               const bool is = there >> (grp * 32 + x * 16 + hh * 4 + 8 * (j / 4) + j % 4) & 1;
 #pragma unroll
               for (int e = 0; e < kF / 2; ++e) {
-                if (!is) vr[i][j][e] = 0u;
-                wild |= (vr[i][j][e] & 0x7f80u) == 0x7f80u || (vr[i][j][e] & 0x7f800000u) == 0x7f800000u;
+                uint32_t& w = vr[(i * 8 + j) * (kF / 2) + e];
+                if (!is) w = 0u;
+                wild |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
               }
             }
           }
@@ -529,7 +545,7 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
           for (int f = 0; f < kF; ++f) {
             u32x4 w;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) w[p] = half_pair(vr[i][2 * p][f / 2], vr[i][2 * p + 1][f / 2], f & 1);
+            for (int p = 0; p < 4; ++p) w[p] = half_pair(vr[(i * 8 + 2 * p) * (kF / 2) + f / 2], vr[(i * 8 + 2 * p + 1) * (kF / 2) + f / 2], f & 1);
             sh_v[buf][grp][x][f][hh << 5 | (u & 31)] = w;
           }
         }
@@ -557,6 +573,7 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
       page_next = page_of(base + 2 * kTileRows);
     }
     if (busy) {
+      const int ln = fresh(lane);
       f32x16 s[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -566,7 +583,7 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
       for (int st = 0; st < kS; ++st)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          s[e] = mfma32(__builtin_bit_cast(bf16x8, sh_k[buf][e][st][lane ^ (st & 7)]), qf[st], s[e]);
+          s[e] = mfma32(__builtin_bit_cast(bf16x8, sh_k[buf][e][st][ln ^ (st & 7)]), qf[st], s[e]);
       uint64_t seen = ~0ull;
       if (masked) {
         seen = there;
@@ -585,9 +602,7 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      // 0 times an infinite product is NaN only where the product is a score
-      top = top == -INFINITY ? top : top * scale2;
-      const float m_new = fmaxf(m_run, top);
+      const float m_new = fmaxf(m_run, top * scale2);
       const float zero = m_new == -INFINITY ? 0.f : m_new;
       if (__any(m_new > m_run)) {
         const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
@@ -604,13 +619,8 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
-          float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
-          float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
-          if (masked && a.q.scale == 0.f) {           // -inf times a scale of 0
-            const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
-            if (!(bits >> (8 * (r / 4) + r % 4) & 1)) p0 = 0.f;
-            if (!(bits >> (8 * (r / 4) + r % 4 + 1) & 1)) p1 = 0.f;
-          }
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
           sum += p0 + p1;
           if constexpr (kOut) pw[2 * e + r / 8][r % 8 / 2] = pack_bf16x2(p0, p1);
         }
@@ -621,33 +631,27 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
           for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int f = 0; f < kF; ++f)
-              o[f] = mfma32(__builtin_bit_cast(bf16x8, sh_v[buf][e >> 1][e & 1][f][lane]),
+              o[f] = mfma32(__builtin_bit_cast(bf16x8, sh_v[buf][e >> 1][e & 1][f][ln]),
                             __builtin_bit_cast(bf16x8, pw[e]), o[f]);
         } else {
           // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
           // for the queries that see the row.
+          for (int r = 0; r < kTileRows; ++r) {
+            const int e = r >> 4, hh = r >> 2 & 1, j = (r >> 1 & 4) | (r & 3);
+            uint32_t pair = 0u;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            for (int r = 0; r < 16; ++r) {
-              const int hh = r / 4 & 1, j = r / 8 * 4 + r % 4;
-              const bool vis = seen >> (16 * e + r) & 1;
-              const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
-              u32x4 pr;
+            for (int x = 0; x < 16; ++x)
+              if (x == 4 * e + j / 2) pair = pw[x / 4][x % 4];
+            const float p = __shfl(bf16_to_f32(j & 1 ? pair >> 16 : pair & 0xffffu), hh << 5 | c);
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(&sh_v[buf][e >> 1][e & 1][0][hh << 5]) + j;
+            if (seen >> r & 1) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) pr[i] = h == hh && i == j / 2 ? pw[e][i] & keep : 0u;
+              for (int f = 0; f < kF; ++f)
 #pragma unroll
-              for (int f = 0; f < kF; ++f) {
-                const u32x4 vw = sh_v[buf][e >> 1][e & 1][f][lane];
-                u32x4 vone;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vone[i] = h == hh && i == j / 2 ? vw[i] & keep : 0u;
-                f32x16 add;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) add[i] = 0.f;
-                add = mfma32(__builtin_bit_cast(bf16x8, vone), __builtin_bit_cast(bf16x8, pr), add);
-                if (vis) o[f] += add;
-              }
+                for (int i = 0; i < 16; ++i)
+                  o[f][i] += p * bf16_to_f32(v[(64 * f + 8 * (i / 4) + 4 * h + i % 4) * 8]);
             }
+          }
         }
       }
     }
