@@ -394,24 +394,50 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
 // More than 32 query rows: bound by the matrix cores and the exponentials, so K and V go
 // through LDS and are shared by the waves, each of which keeps 32 query rows (32x32x16 MFMAs,
 // the same transposed products: lane (q, h) = (lane % 32, lane / 32) of S^T holds cache rows
-// 8 (r / 4) + 4 h + r % 4, r < 16).  LDS holds the operands as the lanes read them, 16 bytes each in
-// a row: K as [32 rows][16 features] tiles, V already transposed, as [32 features][16 rows]
-// tiles whose feature d' of tile m is (hd / 32) d' + m.  A loading thread takes eight cache rows of
-// hd / 32 features (8 bytes a row at hd 128) and transposes them in registers on the way, once
-// for all waves.  The next 64 rows are loaded into registers during the products of one
-// buffer and written to the other: one barrier a step.
+// 8 (r / 4) + 4 h + r % 4, r < 16).  The rows of a step (64) are copied into LDS as they are, by
+// direct loads that hold no registers, while the other buffer is computed with: one barrier a
+// step.  K^T's fragments are 16-byte reads, V^T's are transposing reads (four rows of one
+// feature a lane).  The 16-byte pieces of a row lie in the order piece ^ (row % 8) for K, piece ^
+// 4 (row % 2) for V, which spreads both kinds of read over all banks.
 constexpr int kTileRows = 64;
+
+// 16 bytes per lane from p to the LDS address lds + 16 lane (lds: the same in the wave).  The
+// compiler does not see the load: dma_wait before the barrier that hands the data on.
+__device__ __forceinline__ void dma_row(const uint16_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// Eight cache rows of one feature: two transposing reads of four rows, eight rows apart.
+__device__ __forceinline__ bf16x8 read_transposed(const unsigned char* p, int apart) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  typedef const __attribute__((address_space(3))) unsigned char lds_byte;
+  struct Pair {
+    s16x4 a, b;
+  } pr = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)p),
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(p + apart))};
+  return __builtin_bit_cast(bf16x8, pr);
+}
 
 template <int HD, int NW, bool kOut>
 __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(AttendArgs a) {
   constexpr int kS = HD / 16;                 // MFMA steps over the features
-  constexpr int kF = HD / 32;                 // feature tiles; features of a loaded unit
-  constexpr int kLoad = NW < 4 ? NW : 4;      // waves that load K, and that load V
-  constexpr int kUnits = 4 / kLoad;           // V units of a thread
-  constexpr int kChunks = kTileRows * HD / 8 / (64 * kLoad);   // 16-byte pieces of K of a thread
-  __shared__ u32x4 sh_k[2][2][kS][64];
-  __shared__ u32x4 sh_v[kOut ? 2 : 1][2][2][kOut ? kF : 1][64];
-  __shared__ int sh_wild[2];                  // the step whose V holds a value that is not finite
+  constexpr int kF = HD / 32;                 // feature tiles
+  constexpr int kRowBytes = 2 * HD, kPieces = HD / 8;
+  constexpr int kLoadRows = 64 / kPieces;     // rows of one direct load of a wave
+  constexpr int kLoads = kTileRows / kLoadRows / NW;      // loads of a wave for K, and for V
+  static_assert(kLoads >= 1 && kLoads * kLoadRows * NW == kTileRows, "rows of a step");
+  __shared__ __attribute__((aligned(256))) unsigned char sh_k[2][kTileRows * kRowBytes];
+  __shared__ __attribute__((aligned(256))) unsigned char sh_v[kOut ? 2 : 1][kOut ? kTileRows * kRowBytes : 16];
+  __shared__ int sh_wild;                     // the last step whose V held a value that is not finite
   if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
   int unit = blockIdx.x, mb = 0;
   place_block(a, &unit, &mb);
@@ -474,193 +500,138 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
     }
     return page * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
   };
-
-  // rows on their way; with 8 waves four carry K and four V, in the same registers
-  constexpr int kKWords = 4 * kChunks, kVWords = kUnits * 4 * kF;
-  uint32_t held[NW < 8 && kOut ? kKWords + kVWords : kKWords > kVWords ? kKWords : kVWords];
-  uint32_t* const kr = held;
-  uint32_t* const vr = NW < 8 ? held + kKWords : held;
-  const bool loads_k = NW < 8 || wave >= 4, loads_v = kOut && (NW < 8 || wave < 4);
-  const int lt0 = NW < 8 ? tid : tid & 255;
-  const auto load = [&](int slot) {
-    const int s0 = slot < 0 ? 0 : slot, lt = fresh(lt0);
-    if (loads_k) {
+  const auto load = [&](int slot, int buf) {
+    const int s0 = slot < 0 ? 0 : slot, ln = fresh(lane);
+    const int at = ln % kPieces;                          // where the lane's piece goes
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int x = lt + 64 * kLoad * i;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(kbase + (int64_t)__shfl(s0, x / (HD / 8)) * row_size + x % (HD / 8) * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) kr[4 * i + e] = w[e];
-      }
-    }
-    if (loads_v) {
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = lt + 64 * kLoad * i;              // (group, x, h) of eight rows, features
-        const int r0 = (u >> 7) * 32 + (u >> 6 & 1) * 16 + (u >> 5 & 1) * 4;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint16_t* p = vbase + (int64_t)__shfl(s0, r0 + 8 * (j / 4) + j % 4) * row_size + (u & 31) * kF;
-          if constexpr (HD == 128) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-            vr[(i * 8 + j) * 2] = w[0];
-            vr[(i * 8 + j) * 2 + 1] = w[1];
-          } else {
-            vr[i * 8 + j] = *reinterpret_cast<const uint32_t*>(p);
-          }
-        }
-      }
-    }
-  };
-  // `masked`: not all of the step's rows are there and seen by every query
-  const auto park = [&](int buf, int step, uint64_t there, bool masked) {
-    const int lt = fresh(lt0);
-    if (loads_k) {
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int x = lt + 64 * kLoad * i, row = x / (HD / 8), ch = x % (HD / 8);
-        sh_k[buf][row >> 5][ch >> 1][(((ch & 1) << 5) | (row & 31)) ^ (ch >> 1 & 7)] =
-            u32x4{kr[4 * i], kr[4 * i + 1], kr[4 * i + 2], kr[4 * i + 3]};
-      }
-    }
-    if constexpr (kOut) {
-      if (loads_v) {
-        bool wild = false;
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-          const int u = lt + 64 * kLoad * i, grp = u >> 7, x = u >> 6 & 1, hh = u >> 5 & 1;
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const bool is = there >> (grp * 32 + x * 16 + hh * 4 + 8 * (j / 4) + j % 4) & 1;
-#pragma unroll
-              for (int e = 0; e < kF / 2; ++e) {
-                uint32_t& w = vr[(i * 8 + j) * (kF / 2) + e];
-                if (!is) w = 0u;
-                wild |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-              }
-            }
-          }
-#pragma unroll
-          for (int f = 0; f < kF; ++f) {
-            u32x4 w;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) w[p] = half_pair(vr[(i * 8 + 2 * p) * (kF / 2) + f / 2], vr[(i * 8 + 2 * p + 1) * (kF / 2) + f / 2], f & 1);
-            sh_v[buf][grp][x][f][hh << 5 | (u & 31)] = w;
-          }
-        }
-        if (wild) sh_wild[buf] = step;
-      }
+    for (int i = 0; i < kLoads; ++i) {
+      const int block = wave * kLoads + i, row = block * kLoadRows + ln / kPieces;
+      const int64_t off = (int64_t)__shfl(s0, row) * row_size;
+      dma_row(kbase + off + (at ^ (row & 7)) * 8, lds_address(sh_k[buf]) + block * 1024);
+      if constexpr (kOut) dma_row(vbase + off + (at ^ (row & 1) << 2) * 8, lds_address(sh_v[buf]) + block * 1024);
     }
   };
 
-  if (tid < 2) sh_wild[tid] = -1;
-  __syncthreads();
+  if (tid == 0) sh_wild = -1;
   int slot = slot_of(begin, page_of(begin));
-  load(slot);
-  uint64_t there = __ballot(slot >= 0);
-  bool masked = ~there || begin + kTileRows > ctx;
-  park(0, begin, there, masked);
   int page_next = page_of(begin + kTileRows);
-  __syncthreads();
+  load(slot, 0);
   int buf = 0;
   for (int base = begin; base < end; base += kTileRows, buf ^= 1) {
-    const bool more = base + kTileRows < end;
-    int slot_next = -1;
-    if (more) {
-      slot_next = slot_of(base + kTileRows, page_next);
-      load(slot_next);
-      page_next = page_of(base + 2 * kTileRows);
+    const uint64_t there = __ballot(slot >= 0);
+    const bool masked = ~there || base + kTileRows > ctx;
+    dma_wait();
+    __syncthreads();
+    if (kOut && masked) {
+      // rows that are not there become 0; is there a value that is not finite among the others?
+      bool wild = false;
+      for (int x = tid; x < kTileRows * kPieces; x += 64 * NW) {
+        u32x4* p = reinterpret_cast<u32x4*>(sh_v[buf]) + x;
+        u32x4 w = *p;
+        if (!(there >> (x / kPieces) & 1)) *p = w = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wild |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+      }
+      if (wild) sh_wild = base;
+      __syncthreads();
     }
-    if (busy) {
-      const int ln = fresh(lane);
-      f32x16 s[2];
+    if (base + kTileRows < end) {
+      slot = slot_of(base + kTileRows, page_next);
+      page_next = page_of(base + 2 * kTileRows);
+      load(slot, buf ^ 1);
+    }
+    if (!busy) continue;
+    const int ln = fresh(lane);
+    f32x16 s[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[e][r] = 0.f;
+      for (int r = 0; r < 16; ++r) s[e][r] = 0.f;
+    {
+      const unsigned char* row = sh_k[buf] + (ln & 31) * kRowBytes;
 #pragma unroll
       for (int st = 0; st < kS; ++st)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          s[e] = mfma32(__builtin_bit_cast(bf16x8, sh_k[buf][e][st][ln ^ (st & 7)]), qf[st], s[e]);
-      uint64_t seen = ~0ull;
-      if (masked) {
-        seen = there;
-        if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
+          s[e] = mfma32(*reinterpret_cast<const bf16x8*>(row + e * 32 * kRowBytes + (((2 * st + (ln >> 5)) ^ (ln & 7)) << 4)),
+                        qf[st], s[e]);
+    }
+    uint64_t seen = ~0ull;
+    if (masked) {
+      seen = there;
+      if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (!(bits >> (8 * (r / 4) + r % 4) & 1)) s[e][r] = -INFINITY;
-        }
+        for (int r = 0; r < 16; ++r)
+          if (!(bits >> (8 * (r / 4) + r % 4) & 1)) s[e][r] = -INFINITY;
       }
-      float top = s[0][0];
+    }
+    float top = s[0][0];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m_new = fmaxf(m_run, top * scale2);
-      const float zero = m_new == -INFINITY ? 0.f : m_new;
-      if (__any(m_new > m_run)) {
-        const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
-        l_run *= shrink;
-        if constexpr (kOut) {
-#pragma unroll
-          for (int f = 0; f < kF; ++f) o[f] *= shrink;
-        }
-      }
-      m_run = m_new;
-      float sum = 0.f;
-      u32x4 pw[4];                                    // cache rows 16 x .. of group e: [2 e + x]
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
-          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
-          sum += p0 + p1;
-          if constexpr (kOut) pw[2 * e + r / 8][r % 8 / 2] = pack_bf16x2(p0, p1);
-        }
-      l_run += sum;
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m_new = fmaxf(m_run, top * scale2);
+    const float zero = m_new == -INFINITY ? 0.f : m_new;
+    if (__any(m_new > m_run)) {
+      const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
+      l_run *= shrink;
       if constexpr (kOut) {
-        if (!masked || sh_wild[buf] != base) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+        for (int f = 0; f < kF; ++f) o[f] *= shrink;
+      }
+    }
+    m_run = m_new;
+    float sum = 0.f;
+    u32x4 pw[4];                                      // of cache rows 16 e ..
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
+        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
+        sum += p0 + p1;
+        if constexpr (kOut) pw[2 * e + r / 8][r % 8 / 2] = pack_bf16x2(p0, p1);
+      }
+    l_run += sum;
+    if constexpr (kOut) {
+      if (!masked || sh_wild != base) {
+        // lane i of 16 reads row i / 4, features 4 (i % 4) .. and gets feature i of the four rows
+        const int i = ln & 15, odd = i >> 2 & 1;
+        const unsigned char* v = sh_v[buf] + (4 * (ln >> 5) + (i >> 2)) * kRowBytes + ((ln >> 4 & 1) * 2 + (i >> 1 & 1)) * 16 + 8 * (i & 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int f = 0; f < kF; ++f)
+            o[f] = mfma32(read_transposed(v + e * 16 * kRowBytes + 64 * (f ^ odd), 8 * kRowBytes),
+                          __builtin_bit_cast(bf16x8, pw[e]), o[f]);
+      } else {
+        // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only for
+        // the queries that see the row.
+        for (int r = 0; r < kTileRows; ++r) {
+          const int e = r >> 4, hh = r >> 2 & 1, j = (r >> 1 & 4) | (r & 3);
+          uint32_t pair = 0u;
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            if (x == 4 * e + j / 2) pair = pw[x / 4][x % 4];
+          const float p = __shfl(bf16_to_f32(j & 1 ? pair >> 16 : pair & 0xffffu), hh << 5 | c);
+          if (seen >> r & 1) {
 #pragma unroll
             for (int f = 0; f < kF; ++f)
-              o[f] = mfma32(__builtin_bit_cast(bf16x8, sh_v[buf][e >> 1][e & 1][f][ln]),
-                            __builtin_bit_cast(bf16x8, pw[e]), o[f]);
-        } else {
-          // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
-          // for the queries that see the row.
-          for (int r = 0; r < kTileRows; ++r) {
-            const int e = r >> 4, hh = r >> 2 & 1, j = (r >> 1 & 4) | (r & 3);
-            uint32_t pair = 0u;
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (x == 4 * e + j / 2) pair = pw[x / 4][x % 4];
-            const float p = __shfl(bf16_to_f32(j & 1 ? pair >> 16 : pair & 0xffffu), hh << 5 | c);
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(&sh_v[buf][e >> 1][e & 1][0][hh << 5]) + j;
-            if (seen >> r & 1) {
-#pragma unroll
-              for (int f = 0; f < kF; ++f)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  o[f][i] += p * bf16_to_f32(v[(64 * f + 8 * (i / 4) + 4 * h + i % 4) * 8]);
-            }
+              for (int i = 0; i < 16; ++i) {
+                const int d = 32 * f + 8 * (i / 4) + 4 * h + i % 4;
+                const uint16_t w = *reinterpret_cast<const uint16_t*>(
+                    sh_v[buf] + r * kRowBytes + ((d >> 3) ^ (r & 1) << 2) * 16 + (d & 7) * 2);
+                o[f][i] += p * bf16_to_f32(w);
+              }
           }
         }
       }
     }
-    if (more) {
-      there = __ballot(slot_next >= 0);
-      masked = ~there || base + 2 * kTileRows > ctx;
-      park(buf ^ 1, base + kTileRows, there, masked);
-    }
-    __syncthreads();
   }
   if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
   if (!busy) return;
@@ -675,23 +646,19 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
     a.lse[row * a.q.n_heads + head] = l_run == 0.f ? -INFINITY : m_run * kLn2 + __logf(l_run);
   }
   if constexpr (kOut) {
-    // lane (q, h) holds features 8 kF b + 4 kF h + kF r + f for r < 4, f < kF of each b < 4
+    // lane (q, h) holds features 32 f + 8 b + 4 h + r for r < 4
     const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int f = 0; f < kF; ++f)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = kF * (8 * b + 4 * h + r);
+      for (int b = 0; b < 4; ++b) {
+        const int d = 32 * f + 8 * b + 4 * h;
+        const f32x4 w = {o[f][4 * b], o[f][4 * b + 1], o[f][4 * b + 2], o[f][4 * b + 3]};
         if (a.splits > 1) {
-          float* p = a.part_o + part * HD + d;
-#pragma unroll
-          for (int f = 0; f < kF; ++f) p[f] = o[f][4 * b + r];
+          *reinterpret_cast<f32x4*>(a.part_o + part * HD + d) = w;
         } else {
-          uint16_t* p = a.out + row * a.out_stride + head * HD + d;
-#pragma unroll
-          for (int f = 0; f < kF; f += 2)
-            *reinterpret_cast<uint32_t*>(p + f) =
-                l_run == 0.f ? 0u : pack_bf16x2(o[f][4 * b + r] * inv, o[f + 1][4 * b + r] * inv);
+          const u32x2 x = {pack_bf16x2(w[0] * inv, w[1] * inv), pack_bf16x2(w[2] * inv, w[3] * inv)};
+          *reinterpret_cast<u32x2*>(a.out + row * a.out_stride + head * HD + d) = l_run == 0.f ? u32x2{0u, 0u} : x;
         }
       }
   }
