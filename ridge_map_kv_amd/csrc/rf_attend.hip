@@ -391,15 +391,21 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   }
 }
 
-// More than 32 query rows: bound by the matrix cores and the exponentials, so K and V go
-// through LDS and are shared by the waves, each of which keeps 32 query rows (32x32x16 MFMAs,
-// the same transposed products: lane (q, h) = (lane % 32, lane / 32) of S^T holds cache rows
-// 8 (r / 4) + 4 h + r % 4, r < 16).  The rows of a step (64) are copied into LDS as they are, by
-// direct loads that hold no registers, while the other buffer is computed with: one barrier a
-// step.  K^T's fragments are 16-byte reads, V^T's are transposing reads (four rows of one
+// More than 64 query rows: bound by the matrix cores and the exponentials, so K and V go
+// through LDS and are shared by the workgroup's eight waves, each of which keeps 32 query rows
+// (32x32x16 MFMAs, the same transposed products: lane (q, h) = (lane % 32, lane / 32) of S^T
+// holds cache rows 8 (r / 4) + 4 h + r % 4, r < 16).  WM of the waves lie along the query rows, with
+// WM = 4 the other four take the second half of a step's cache rows and are added at the end.
+// The rows of a step (64) are copied into LDS as they are, by direct loads that hold no
+// registers, two steps ahead of the products: four buffers, one barrier a step.  K^T's fragments are 16-byte reads, V^T's are transposing reads (four rows of one
 // feature a lane).  The 16-byte pieces of a row lie in the order piece ^ (row % 8) for K, piece ^
-// 4 (row % 2) for V, which spreads both kinds of read over all banks.
+// 4 (row % 2) for V, which spreads both kinds of read over all banks.  The pool slots of the
+// workgroup's rows are looked up beforehand: a table load between the direct loads would wait
+// for those.
 constexpr int kTileRows = 64;
+constexpr int kTileWaves = 8;
+constexpr int kBufs = 4;
+constexpr int kSlots = 4096;          // cache rows whose slots are looked up at a time
 
 // 16 bytes per lane from p to the LDS address lds + 16 lane (lds: the same in the wave).  The
 // compiler does not see the load: dma_wait before the barrier that hands the data on.
@@ -409,10 +415,28 @@ __device__ __forceinline__ void dma_row(const uint16_t* p, uint32_t lds) {
                : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int kLeft>                  // until at most kLeft loads are under way
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Whether one of eight bf16 values is infinite or NaN.
+__device__ __forceinline__ bool not_finite(u32x4 w) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+  return any;
+}
+
+// The value of lane ^ 32.
+__device__ __forceinline__ float other_half(float v) {
+  const int x = __builtin_bit_cast(int, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -427,17 +451,20 @@ __device__ __forceinline__ bf16x8 read_transposed(const unsigned char* p, int ap
   return __builtin_bit_cast(bf16x8, pr);
 }
 
-template <int HD, int NW, bool kOut>
-__global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(AttendArgs a) {
+template <int HD, int WM, bool kOut>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendArgs a) {
   constexpr int kS = HD / 16;                 // MFMA steps over the features
   constexpr int kF = HD / 32;                 // feature tiles
+  constexpr int kE = WM / 4;                  // groups of 32 cache rows of a step that a wave takes
   constexpr int kRowBytes = 2 * HD, kPieces = HD / 8;
   constexpr int kLoadRows = 64 / kPieces;     // rows of one direct load of a wave
-  constexpr int kLoads = kTileRows / kLoadRows / NW;      // loads of a wave for K, and for V
-  static_assert(kLoads >= 1 && kLoads * kLoadRows * NW == kTileRows, "rows of a step");
-  __shared__ __attribute__((aligned(256))) unsigned char sh_k[2][kTileRows * kRowBytes];
-  __shared__ __attribute__((aligned(256))) unsigned char sh_v[kOut ? 2 : 1][kOut ? kTileRows * kRowBytes : 16];
-  __shared__ int sh_wild;                     // the last step whose V held a value that is not finite
+  constexpr int kLoads = kTileRows / kLoadRows / kTileWaves;   // a wave's for K, and for V, of a step
+  constexpr int kAhead = kLoads * (kOut ? 2 : 1);
+  static_assert(kLoads >= 1 && kLoads * kLoadRows * kTileWaves == kTileRows, "rows of a step");
+  constexpr int kBufBytes = kTileRows * kRowBytes;
+  __shared__ __attribute__((aligned(256))) unsigned char sh_kv[kBufs * kBufBytes * (kOut ? 2 : 1)];
+  __shared__ int sh_slot[kSlots];
+  __shared__ unsigned long long sh_wild;      // drafts with a value that is not finite, a bit each
   if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
   int unit = blockIdx.x, mb = 0;
   place_block(a, &unit, &mb);
@@ -445,12 +472,13 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
+  const int wm = wave % WM, e0 = wave / WM;   // this wave's query rows; its first group
 
   int len, first, n;
   bool bad;
   const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
   if (bad && !a.scan && tid == 0) atomicOr(a.status, kStatusRowsBit);
-  const int m_rows = n * a.group, m0 = mb * 32 * NW;
+  const int m_rows = n * a.group, m0 = mb * 32 * WM;
   const int begin = split * a.chunk;
   if (!go || m0 >= m_rows || (begin >= len && split > 0)) return;
   const int end = len < begin + a.chunk ? len : begin + a.chunk;
@@ -458,8 +486,8 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
 
   // this wave's 32 query rows; a negative scale turns their sign, so that the largest product
   // is the largest score, and a scale of 0 makes them 0
-  const int m = m0 + 32 * wave + c;
-  const bool busy = m0 + 32 * wave < m_rows, in = m < m_rows;
+  const int m = m0 + 32 * wm + c;
+  const bool busy = m0 + 32 * wm < m_rows, in = m < m_rows;
   const int qi = in ? m / a.group : 0;
   const uint64_t word = draft_word(a.q, first + qi, qi);
   const float scale2 = (a.q.scale == 0.f ? 1.f : fabsf(a.q.scale)) * kLog2e;
@@ -485,158 +513,249 @@ __global__ __launch_bounds__(64 * NW, NW == 2 ? 1 : 2) void attend_tile_kernel(A
   const int64_t row_size = (int64_t)a.b.n_kv * HD;
   const uint16_t* kbase = a.kp + kh * HD;
   const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
-  bool err = false;
-  // lane's row of the step at `base`: its page, then its pool slot (-1: not there)
-  const auto page_of = [&](int base) -> int {
-    const int r = base + lane;
-    return table[quotient((unsigned)(r < len ? r : len - 1), a.page)];
-  };
-  const auto slot_of = [&](int base, int page) -> int {
-    const int r = base + lane;
-    if (r >= len) return -1;
-    if (page < 0 || page >= a.b.num_pages) {
-      err = true;
-      return -1;
-    }
-    return page * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
-  };
-  const auto load = [&](int slot, int buf) {
-    const int s0 = slot < 0 ? 0 : slot, ln = fresh(lane);
-    const int at = ln % kPieces;                          // where the lane's piece goes
+  const auto k_at = [&](int step) { return sh_kv + step % kBufs * kBufBytes; };
+  const auto v_at = [&](int step) { return sh_kv + (kBufs + step % kBufs) * kBufBytes; };
+  const auto load = [&](int step) {
+    const int ln = fresh(lane), at = ln % kPieces;        // where the lane's piece goes
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int block = wave * kLoads + i, row = block * kLoadRows + ln / kPieces;
-      const int64_t off = (int64_t)__shfl(s0, row) * row_size;
-      dma_row(kbase + off + (at ^ (row & 7)) * 8, lds_address(sh_k[buf]) + block * 1024);
-      if constexpr (kOut) dma_row(vbase + off + (at ^ (row & 1) << 2) * 8, lds_address(sh_v[buf]) + block * 1024);
+      const int slot = sh_slot[step * kTileRows + row];
+      const int64_t off = (int64_t)(slot < 0 ? 0 : slot) * row_size;
+      dma_row(kbase + off + (at ^ (row & 7)) * 8, lds_address(k_at(step)) + block * 1024);
+      if constexpr (kOut) dma_row(vbase + off + (at ^ (row & 1) << 2) * 8, lds_address(v_at(step)) + block * 1024);
     }
   };
 
-  if (tid == 0) sh_wild = -1;
-  int slot = slot_of(begin, page_of(begin));
-  int page_next = page_of(begin + kTileRows);
-  load(slot, 0);
-  int buf = 0;
-  for (int base = begin; base < end; base += kTileRows, buf ^= 1) {
-    const uint64_t there = __ballot(slot >= 0);
-    const bool masked = ~there || base + kTileRows > ctx;
-    dma_wait();
+  for (int part = begin; part < end; part += kSlots) {
+    const int rows = end - part < kSlots ? end - part : kSlots;
+    const int steps = (rows + kTileRows - 1) / kTileRows;
+    if (part > begin) __syncthreads();                    // the slots before are done with
+    bool err = false;
+    for (int x = tid; x < steps * kTileRows; x += 64 * kTileWaves) {
+      int slot = -1;                                      // not there
+      if (part + x < len) {
+        const int pi = (int)quotient((unsigned)(part + x), a.page), page = table[pi];
+        if (page >= 0 && page < a.b.num_pages)
+          slot = page * a.b.page_size + (part + x - pi * a.b.page_size);
+        else
+          err = true;
+      }
+      sh_slot[x] = slot;
+    }
+    if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
+    if (tid == 0 && part == begin) sh_wild = 0ull;
+    __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): only direct loads from here on
     __syncthreads();
-    if (kOut && masked) {
-      // rows that are not there become 0; is there a value that is not finite among the others?
-      bool wild = false;
-      for (int x = tid; x < kTileRows * kPieces; x += 64 * NW) {
-        u32x4* p = reinterpret_cast<u32x4*>(sh_v[buf]) + x;
-        u32x4 w = *p;
-        if (!(there >> (x / kPieces) & 1)) *p = w = u32x4{0u, 0u, 0u, 0u};
+    f32x16 s[kE];
+    // rows of a step that exist, and whether some query does not see all 64
+    const auto there_at = [&](int step) -> uint64_t { return __ballot(sh_slot[step * kTileRows + lane] >= 0); };
+    const auto masked_at = [&](int step, uint64_t there) { return ~there || part + (step + 1) * kTileRows > ctx; };
+    // The order of reads, products and exponentials is pinned: fragments are read four products
+    // ahead, and between two products of V the exponentials of the next sixteen rows.
+    const auto scores = [&](int step) {
+      const int ln = fresh(lane);
+      const unsigned char* row = k_at(step) + (32 * e0 + (ln & 31)) * kRowBytes;
+      const auto fragment = [&](int i) {
+        return *reinterpret_cast<const bf16x8*>(row + i % kE * 32 * kRowBytes + (((2 * (i / kE) + (ln >> 5)) ^ (ln & 7)) << 4));
+      };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wild |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+      for (int e = 0; e < kE; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[e][r] = 0.f;
+      bf16x8 kf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kf[i] = fragment(i);
+#pragma unroll
+      for (int i = 0; i < kE * kS; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        s[i % kE] = mfma32(kf[i % 4], qf[i / kE], s[i % kE]);
+        if (i + 4 < kE * kS) kf[i % 4] = fragment(i + 4);
       }
-      if (wild) sh_wild = base;
-      __syncthreads();
-    }
-    if (base + kTileRows < end) {
-      slot = slot_of(base + kTileRows, page_next);
-      page_next = page_of(base + 2 * kTileRows);
-      load(slot, buf ^ 1);
-    }
-    if (!busy) continue;
-    const int ln = fresh(lane);
-    f32x16 s[2];
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto finish = [&](int step) {
+      const int ln = fresh(lane), base = part + step * kTileRows;
+      const uint64_t there = there_at(step);
+      if (masked_at(step, there)) {
+        uint64_t seen = there;
+        if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < kE; ++e) {
+          const uint32_t bits = (uint32_t)(seen >> (32 * (e0 + e) + 4 * h));
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[e][r] = 0.f;
-    {
-      const unsigned char* row = sh_k[buf] + (ln & 31) * kRowBytes;
-#pragma unroll
-      for (int st = 0; st < kS; ++st)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          s[e] = mfma32(*reinterpret_cast<const bf16x8*>(row + e * 32 * kRowBytes + (((2 * st + (ln >> 5)) ^ (ln & 7)) << 4)),
-                        qf[st], s[e]);
-    }
-    uint64_t seen = ~0ull;
-    if (masked) {
-      seen = there;
-      if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t bits = (uint32_t)(seen >> (32 * e + 4 * h));
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!(bits >> (8 * (r / 4) + r % 4) & 1)) s[e][r] = -INFINITY;
-      }
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m_new = fmaxf(m_run, top * scale2);
-    const float zero = m_new == -INFINITY ? 0.f : m_new;
-    if (__any(m_new > m_run)) {
-      const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
-      l_run *= shrink;
-      if constexpr (kOut) {
-#pragma unroll
-        for (int f = 0; f < kF; ++f) o[f] *= shrink;
-      }
-    }
-    m_run = m_new;
-    float sum = 0.f;
-    u32x4 pw[4];                                      // of cache rows 16 e ..
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e][r], scale2, -zero));
-        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e][r + 1], scale2, -zero));
-        sum += p0 + p1;
-        if constexpr (kOut) pw[2 * e + r / 8][r % 8 / 2] = pack_bf16x2(p0, p1);
-      }
-    l_run += sum;
-    if constexpr (kOut) {
-      if (!masked || sh_wild != base) {
-        // lane i of 16 reads row i / 4, features 4 (i % 4) .. and gets feature i of the four rows
-        const int i = ln & 15, odd = i >> 2 & 1;
-        const unsigned char* v = sh_v[buf] + (4 * (ln >> 5) + (i >> 2)) * kRowBytes + ((ln >> 4 & 1) * 2 + (i >> 1 & 1)) * 16 + 8 * (i & 1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int f = 0; f < kF; ++f)
-            o[f] = mfma32(read_transposed(v + e * 16 * kRowBytes + 64 * (f ^ odd), 8 * kRowBytes),
-                          __builtin_bit_cast(bf16x8, pw[e]), o[f]);
-      } else {
-        // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only for
-        // the queries that see the row.
-        for (int r = 0; r < kTileRows; ++r) {
-          const int e = r >> 4, hh = r >> 2 & 1, j = (r >> 1 & 4) | (r & 3);
-          uint32_t pair = 0u;
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            if (x == 4 * e + j / 2) pair = pw[x / 4][x % 4];
-          const float p = __shfl(bf16_to_f32(j & 1 ? pair >> 16 : pair & 0xffffu), hh << 5 | c);
-          if (seen >> r & 1) {
-#pragma unroll
-            for (int f = 0; f < kF; ++f)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int d = 32 * f + 8 * (i / 4) + 4 * h + i % 4;
-                const uint16_t w = *reinterpret_cast<const uint16_t*>(
-                    sh_v[buf] + r * kRowBytes + ((d >> 3) ^ (r & 1) << 2) * 16 + (d & 7) * 2);
-                o[f][i] += p * bf16_to_f32(w);
-              }
-          }
+          for (int r = 0; r < 16; ++r)
+            if (!(bits >> (8 * (r / 4) + r % 4) & 1)) s[e][r] = -INFINITY;
         }
       }
+      // lane i of 16 reads row i / 4, features 4 (i % 4) .. and gets feature i of the four rows
+      const int i16 = ln & 15, odd = i16 >> 2 & 1;
+      const unsigned char* vs = v_at(step) + 32 * e0 * kRowBytes;
+      const unsigned char* v = vs + (4 * (ln >> 5) + (i16 >> 2)) * kRowBytes + ((ln >> 4 & 1) * 2 + (i16 >> 1 & 1)) * 16 + 8 * (i16 & 1);
+      const auto fragment = [&](int i) {
+        return read_transposed(v + i / kF * 16 * kRowBytes + 64 * (i % kF ^ odd), 8 * kRowBytes);
+      };
+      bf16x8 vf[4];
+      if constexpr (kOut) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vf[i] = fragment(i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
+      top = fmaxf(top, other_half(top));
+      const float m_new = fmaxf(m_run, top * scale2);
+      const float zero = m_new == -INFINITY ? 0.f : m_new;
+      if (__any(m_new > m_run)) {
+        const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
+        l_run *= shrink;
+        if constexpr (kOut) {
+#pragma unroll
+          for (int f = 0; f < kF; ++f) o[f] *= shrink;
+        }
+      }
+      m_run = m_new;
+      // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, packed
+      const auto pair = [&](int x, int i) -> uint32_t {
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i], scale2, -zero));
+        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i + 1], scale2, -zero));
+        l_run += p0 + p1;
+        return pack_bf16x2(p0, p1);
+      };
+      if constexpr (!kOut) {
+#pragma unroll
+        for (int x = 0; x < 2 * kE; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pair(x, i);
+      } else {
+        u32x4 now, next = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = pair(0, i);
+#pragma unroll
+        for (int x = 0; x < 2 * kE; ++x) {
+#pragma unroll
+          for (int f = 0; f < kF; ++f) {
+            const int i = x * kF + f;
+            __builtin_amdgcn_sched_barrier(0);
+            o[f] = mfma32(vf[i % 4], __builtin_bit_cast(bf16x8, now), o[f]);
+            if (i + 4 < 2 * kE * kF) vf[i % 4] = fragment(i + 4);
+            if (x + 1 < 2 * kE) {
+#pragma unroll
+              for (int j = f * (4 / kF); j < (f + 1) * (4 / kF); ++j) next[j] = pair(x + 1, j);
+            }
+          }
+          now = next;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i < steps) load(i);
+    // Hands a step's rows to all waves and sends for those of two steps on.
+    const auto sync = [&](int step) {
+      // the step's loads are done when only those of the next are under way
+      if (steps - step > 1)
+        dma_wait<kAhead>();
+      else
+        dma_wait<0>();
+      __syncthreads();
+      const uint64_t there = there_at(step);
+      if (kOut && masked_at(step, there)) {
+        // 0 times what a query does not see has to be 0: rows that are not there become 0, and so do
+        // pieces of a draft's row with an infinity or NaN, which is remembered for the end
+        for (int x = tid; x < kTileRows * kPieces; x += 64 * kTileWaves) {
+          u32x4* p = reinterpret_cast<u32x4*>(v_at(step)) + x;
+          const int r = x / kPieces, draft = part + step * kTileRows + r - ctx;
+          const bool is = there >> r & 1, wild = is && draft >= 0 && not_finite(*p);
+          if (!is || wild) *p = u32x4{0u, 0u, 0u, 0u};
+          if (wild) atomicOr(&sh_wild, 1ull << draft);
+        }
+        __syncthreads();
+      }
+      if (step + 2 < steps) load(step + 2);
+    };
+    // Waves 0 to 3 meet the others before a step's scores, waves 4 to 7, on the same SIMDs, between
+    // the scores of a step and its exponentials and second product: the products of one run
+    // beside the exponentials of the other.
+    const bool late = wave >= 4;
+    if (late) sync(0);
+    for (int step = 0; step < steps; ++step) {
+      if (!late) sync(step);
+      if (busy) scores(step);
+      if (late && step + 1 < steps) sync(step + 1);
+      if (busy) finish(step);
     }
   }
-  if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
-  if (!busy) return;
 
   l_run += __shfl_xor(l_run, 32);
+  if constexpr (WM == 4) {
+    // the second half's waves hand over to the first's
+    float* sh_o = reinterpret_cast<float*>(sh_kv);        // [4][16 kF + 2][64]
+    constexpr int kWords = (kOut ? 16 * kF : 0) + 2;
+    static_assert(4 * kWords * 256 <= (int)sizeof(sh_kv), "room to hand over");
+    __syncthreads();
+    float* at = sh_o + wm * kWords * 64 + lane;
+    if (e0 == 1 && busy) {
+      at[0] = m_run;
+      at[64] = l_run;
+      if constexpr (kOut) {
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) at[(2 + 16 * f + r) * 64] = o[f][r];
+      }
+    }
+    __syncthreads();
+    if (e0 == 1 || !busy) return;
+    const float mo = at[0], m_new = fmaxf(m_run, mo), zero = m_new == -INFINITY ? 0.f : m_new;
+    const float mine = __builtin_amdgcn_exp2f(m_run - zero), theirs = __builtin_amdgcn_exp2f(mo - zero);
+    m_run = m_new;
+    l_run = l_run * mine + at[64] * theirs;
+    if constexpr (kOut) {
+#pragma unroll
+      for (int f = 0; f < kF; ++f)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[f][r] = o[f][r] * mine + at[(2 + 16 * f + r) * 64] * theirs;
+    }
+  }
+  if (!busy) return;
+  if constexpr (kOut) {
+    // the pieces left out above, for the queries that see their rows
+    for (uint64_t wild = sh_wild; wild; wild &= wild - 1) {
+      const int draft = __ffsll((unsigned long long)wild) - 1, row = ctx + draft;
+      const int pi = (int)quotient((unsigned)row, a.page);
+      const int64_t off = ((int64_t)table[pi] * a.b.page_size + (row - pi * a.b.page_size)) * row_size;
+      float dot = 0.f;
+#pragma unroll
+      for (int s = 0; s < kS; ++s) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(kbase + off + 16 * s + 8 * h), y = __builtin_bit_cast(u32x4, qf[s]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dot += bf16_to_f32(x[i] & 0xffffu) * bf16_to_f32(y[i] & 0xffffu) + bf16_to_f32(x[i] >> 16) * bf16_to_f32(y[i] >> 16);
+      }
+      dot += other_half(dot);
+      const float zero = m_run == -INFINITY ? 0.f : m_run;
+      const float p = __builtin_amdgcn_exp2f(fmaf(dot, scale2, -zero));
+      const bool sees = word >> draft & 1;
+#pragma unroll
+      for (int f = 0; f < kF; ++f)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(vbase + off + 32 * f + 8 * b);
+          if (!sees || !not_finite(x)) continue;
+          const uint32_t lo = h ? x[2] : x[0], hi = h ? x[3] : x[1];
+          o[f][4 * b] += p * bf16_to_f32(lo & 0xffffu);
+          o[f][4 * b + 1] += p * bf16_to_f32(lo >> 16);
+          o[f][4 * b + 2] += p * bf16_to_f32(hi & 0xffffu);
+          o[f][4 * b + 3] += p * bf16_to_f32(hi >> 16);
+        }
+    }
+  }
   if (!in) return;
   const int head = kh * a.group + m % a.group;
   const int64_t row = first + qi, part = ((int64_t)sh * a.splits + split) * (a.q.max_q * a.group) + m;
@@ -740,11 +859,11 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
   AttendPlan p;
   p.group = n_heads / b.n_kv;
   const int rows = max_q * p.group;
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  p.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.mblocks = (rows + p.rows - 1) / p.rows;
   // enough workgroups for the chip, of at least 128 rows (one step of four waves)
   const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
-  const int64_t want = p.rows == 16 ? 1024 : p.rows <= 128 ? 512 : 256;
+  const int64_t want = p.rows == 16 ? 1024 : 256;
   const int most = (b.max_len + 127) / 128;
   int64_t s = (want + units - 1) / units;
   if (s > most) s = most;
@@ -761,12 +880,8 @@ template <int HD, bool kOut>
 void launch_rows(const AttendArgs& a, int rows, unsigned grid, hipStream_t stream) {
   if (rows == 16)
     hipLaunchKernelGGL((attend_kernel<HD, 1, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
-  else if (rows == 32)
-    hipLaunchKernelGGL((attend_kernel<HD, 2, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
-  else if (rows == 64)
-    hipLaunchKernelGGL((attend_tile_kernel<HD, 2, kOut>), dim3(grid), dim3(128), 0, stream, a);
   else if (rows == 128)
-    hipLaunchKernelGGL((attend_tile_kernel<HD, 4, kOut>), dim3(grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((attend_tile_kernel<HD, 4, kOut>), dim3(grid), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((attend_tile_kernel<HD, 8, kOut>), dim3(grid), dim3(512), 0, stream, a);
 }
