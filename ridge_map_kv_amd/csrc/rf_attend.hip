@@ -40,11 +40,11 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   unsigned* status;
-  float* part_o;                // [batch][n_kv][splits][max_q G][hd]
-  float2* part_ml;              // [batch][n_kv][splits][max_q G]: running maximum (log2), sum
+  float* part_o;                // [parts][n_kv][max_q G][hd]
+  float2* part_ml;              // [parts][n_kv][max_q G]: running maximum (log2), sum
   int64_t out_stride;
   Divide page;
-  int splits, chunk;            // row ranges of a sequence, rows in each (a multiple of 128)
+  int parts, goal, least;       // parts of the grid; wanted of all sequences (0: one each), rows of one
   int mblocks;                  // blocks of query rows
   int group;                    // query heads of a key head
   int scan;                     // 1: the workgroup past the grid looks all pages over for the status
@@ -66,11 +66,105 @@ __device__ __forceinline__ int fresh(int v) {
   return v;
 }
 
-// A workgroup's row range and block of query rows: the blocks of one range go to one XCD
-// (blockIdx % 8), side by side, where they share its cache.
+// Long caches are split into parts of about equal length over all sequences, `goal` of them at
+// most: with one workgroup to a compute unit one part too many costs a second round (trees on 4
+// sequences, 35 parts of 8 heads instead of 32: 239 instead of 149 us).  The lengths are known only
+// here, so each wave works the split out for itself.
+constexpr int kGrain = 64;              // parts are multiples of this many rows
+
+// One sequence of a batch as a lane looks it up; grains 0: it is skipped.
+struct Seq {
+  int len, first, n, grains;
+  bool bad;
+};
+__device__ __forceinline__ Seq look_up(const AttendArgs& a, int b) {
+  Seq s = {};
+  if (b < a.b.batch && sequence_of(a.b, a.q, b, &s.len, &s.first, &s.n, &s.bad)) s.grains = (s.len + kGrain - 1) / kGrain;
+  return s;
+}
+
+// Grains of one part, and whether some sequence is in error; `mine`: sequence lane.
+__device__ int grains_of_part(const AttendArgs& a, const Seq& mine, bool* bad) {
+  const int lane = threadIdx.x & 63;
+  long long total = mine.grains;
+  bool some = mine.bad;
+  for (int b = 64 + lane; b < a.b.batch; b += 64) {
+    const Seq s = look_up(a, b);
+    total += s.grains;
+    some |= s.bad;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+  *bad = __any(some);
+  int each = (int)((total + a.goal - 1) / a.goal);
+  if (each < a.least / kGrain) each = a.least / kGrain;
+  for (int tries = 0; tries < 4; ++tries) {
+    int parts = (mine.grains + each - 1) / each;
+    for (int b = 64 + lane; b < a.b.batch; b += 64) parts += (look_up(a, b).grains + each - 1) / each;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) parts += __shfl_xor(parts, d);
+    if (parts <= a.goal) break;
+    each += (each * (parts - a.goal) + a.goal - 1) / a.goal;
+  }
+  return each;
+}
+
+// What a workgroup computes: rows [begin, end) of a sequence, for one key head.
+struct Part {
+  int kh, seq, len, first, n, begin, end, id;
+  bool whole;                           // the sequence's only part
+};
+__device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
+  const int lane = threadIdx.x & 63;
+  bool bad;
+  p->kh = unit % a.b.n_kv;
+  p->id = unit / a.b.n_kv;
+  if (!a.goal) {
+    p->seq = p->id;
+    const bool go = sequence_of(a.b, a.q, p->seq, &p->len, &p->first, &p->n, &bad);
+    if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+    p->begin = 0;
+    p->end = p->len;
+    p->whole = true;
+    return go;
+  }
+  Seq s = look_up(a, lane);
+  const int each = grains_of_part(a, s, &bad);
+  if (bad && !a.scan && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  int before = 0;                       // parts of the sequences before these 64
+  for (int b0 = 0; b0 < a.b.batch; b0 += 64) {
+    if (b0) s = look_up(a, b0 + lane);
+    const int mine = (s.grains + each - 1) / each;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    const uint64_t past = __ballot(before + upto > p->id);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      const int parts = of(mine), split = p->id - before - (of(upto) - parts);
+      p->seq = b0 + l;
+      p->len = of(s.len);
+      p->first = of(s.first);
+      p->n = of(s.n);
+      p->begin = __builtin_amdgcn_readfirstlane(split * each * kGrain);
+      p->end = p->len < p->begin + each * kGrain ? p->len : p->begin + each * kGrain;
+      p->whole = parts == 1;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// A workgroup's unit (part and key head) and block of query rows: the blocks of one unit go to
+// one XCD (blockIdx % 8), side by side, where they share its cache.
 __device__ __forceinline__ void place_block(const AttendArgs& a, int* unit, int* mb) {
   if (a.mblocks == 1) return;
-  const int per = 8 * a.mblocks, full = (a.b.batch * a.b.n_kv * a.splits) / 8 * per;
+  const int per = 8 * a.mblocks, full = (a.parts * a.b.n_kv) / 8 * per;
   const int id = *unit;
   if (id < full) {
     *mb = id % per / 8;
@@ -124,19 +218,13 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
   int unit = blockIdx.x, mb = 0;
   place_block(a, &unit, &mb);
-  const int split = unit % a.splits, sh = unit / a.splits;
-  const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-
-  int len, first, n;
-  bool bad;
-  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
-  if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  Part pt;
+  if (!find_part(a, unit, &pt)) return;
+  const int kh = pt.kh, seq = pt.seq, len = pt.len, first = pt.first, n = pt.n, begin = pt.begin, end = pt.end;
   const int m_rows = n * a.group, m0 = mb * 16 * MT;
-  const int begin = split * a.chunk;
-  if (!go || m0 >= m_rows || (begin >= len && split > 0)) return;
-  const int end = len < begin + a.chunk ? len : begin + a.chunk;
+  if (m0 >= m_rows) return;
   const int ctx = len - n;
 
   // Q^T fragments: query row m0 + 16 t + c of the block, zero past the last
@@ -351,12 +439,12 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
     __syncthreads();
   }
   if (wave != 0) return;
-  const int64_t part = ((int64_t)sh * a.splits + split) * (a.q.max_q * a.group);
+  const int64_t part = ((int64_t)pt.id * a.b.n_kv + kh) * (a.q.max_q * a.group);
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + 16 * t + c;
     if (m >= m_rows) continue;
-    if (a.splits > 1) {
+    if (!pt.whole) {
       if (g == 0) a.part_ml[part + m] = make_float2(m_run[t], l_run[t]);
       if constexpr (kOut) {
 #pragma unroll
@@ -468,20 +556,15 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
   int unit = blockIdx.x, mb = 0;
   place_block(a, &unit, &mb);
-  const int split = unit % a.splits, sh = unit / a.splits;
-  const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
   const int wm = wave % WM, e0 = wave / WM;   // this wave's query rows; its first group
 
-  int len, first, n;
-  bool bad;
-  const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
-  if (bad && !a.scan && tid == 0) atomicOr(a.status, kStatusRowsBit);
+  Part pt;
+  if (!find_part(a, unit, &pt)) return;
+  const int kh = pt.kh, seq = pt.seq, len = pt.len, first = pt.first, n = pt.n, begin = pt.begin, end = pt.end;
   const int m_rows = n * a.group, m0 = mb * 32 * WM;
-  const int begin = split * a.chunk;
-  if (!go || m0 >= m_rows || (begin >= len && split > 0)) return;
-  const int end = len < begin + a.chunk ? len : begin + a.chunk;
+  if (m0 >= m_rows) return;
   const int ctx = len - n;
 
   // this wave's 32 query rows; a negative scale turns their sign, so that the largest product
@@ -532,16 +615,19 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
     const int steps = (rows + kTileRows - 1) / kTileRows;
     if (part > begin) __syncthreads();                    // the slots before are done with
     bool err = false;
-    for (int x = tid; x < steps * kTileRows; x += 64 * kTileWaves) {
-      int slot = -1;                                      // not there
-      if (part + x < len) {
-        const int pi = (int)quotient((unsigned)(part + x), a.page), page = table[pi];
-        if (page >= 0 && page < a.b.num_pages)
-          slot = page * a.b.page_size + (part + x - pi * a.b.page_size);
-        else
-          err = true;
-      }
-      sh_slot[x] = slot;
+    int page[kSlots / 64 / kTileWaves];                   // table loads together
+#pragma unroll
+    for (int i = 0; i < kSlots / 64 / kTileWaves; ++i) {
+      const int x = tid + 64 * kTileWaves * i;
+      page[i] = x < rows ? table[quotient((unsigned)(part + x), a.page)] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kSlots / 64 / kTileWaves; ++i) {
+      const int x = tid + 64 * kTileWaves * i;
+      const bool is = x < rows && page[i] >= 0 && page[i] < a.b.num_pages;
+      if (x < rows && !is) err = true;
+      if (x < steps * kTileRows)                          // -1: not there
+        sh_slot[x] = is ? page[i] * a.b.page_size + (part + x - (int)quotient((unsigned)(part + x), a.page) * a.b.page_size) : -1;
     }
     if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
     if (tid == 0 && part == begin) sh_wild = 0ull;
@@ -758,8 +844,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   }
   if (!in) return;
   const int head = kh * a.group + m % a.group;
-  const int64_t row = first + qi, part = ((int64_t)sh * a.splits + split) * (a.q.max_q * a.group) + m;
-  if (a.splits > 1) {
+  const int64_t row = first + qi, part = ((int64_t)pt.id * a.b.n_kv + kh) * (a.q.max_q * a.group) + m;
+  if (!pt.whole) {
     if (h == 0) a.part_ml[part] = make_float2(m_run, l_run);
   } else if (a.lse && h == 0) {
     a.lse[row * a.q.n_heads + head] = l_run == 0.f ? -INFINITY : m_run * kLn2 + __logf(l_run);
@@ -773,7 +859,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
       for (int b = 0; b < 4; ++b) {
         const int d = 32 * f + 8 * b + 4 * h;
         const f32x4 w = {o[f][4 * b], o[f][4 * b + 1], o[f][4 * b + 2], o[f][4 * b + 3]};
-        if (a.splits > 1) {
+        if (!pt.whole) {
           *reinterpret_cast<f32x4*>(a.part_o + part * HD + d) = w;
         } else {
           const u32x2 x = {pack_bf16x2(w[0] * inv, w[1] * inv), pack_bf16x2(w[2] * inv, w[3] * inv)};
@@ -794,13 +880,20 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
   const int sh = (int)(id / rows), m = (int)(id % rows);
   if (sh >= a.b.batch * a.b.n_kv) return;
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
-  int len, first, n;
   bool bad;
-  if (!sequence_of(a.b, a.q, seq, &len, &first, &n, &bad) || m >= n * a.group) return;
-  const int parts = (len + a.chunk - 1) / a.chunk;
-  const float2* ml = a.part_ml + (int64_t)sh * a.splits * rows + m;
+  const Seq mine = look_up(a, lane), self = look_up(a, seq);
+  const int n = self.n, first = self.first;
+  if (!self.grains || m >= n * a.group) return;
+  const int each = grains_of_part(a, mine, &bad), parts = (self.grains + each - 1) / each;
+  if (parts == 1) return;                           // written by its workgroup
+  int before = lane < seq ? (mine.grains + each - 1) / each : 0;
+  for (int b = 64 + lane; b < seq; b += 64) before += (look_up(a, b).grains + each - 1) / each;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+  const int64_t at = ((int64_t)before * a.b.n_kv + kh) * rows + m, step = (int64_t)a.b.n_kv * rows;
+  const float2* ml = a.part_ml + at;
   float top = -INFINITY;
-  for (int s = lane; s < parts; s += 64) top = fmaxf(top, ml[(int64_t)s * rows].x);
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, ml[s * step].x);
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
   const float zero = top == -INFINITY ? 0.f : top;
@@ -808,15 +901,15 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.f;
   if (a.out) {
-    const float* po = a.part_o + ((int64_t)sh * a.splits * rows + m) * HD + c * kE;
+    const float* po = a.part_o + at * HD + c * kE;
 #pragma unroll 4
     for (int s = g; s < parts; s += 4) {
-      const float2 v = ml[(int64_t)s * rows];
+      const float2 v = ml[s * step];
       const float w = __builtin_amdgcn_exp2f(v.x - zero);
       sum += v.y * w;
 #pragma unroll
       for (int e = 0; e < kE; e += 4) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(po + (int64_t)s * rows * HD + e);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(po + s * step * HD + e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[e + i] += x[i] * w;
       }
@@ -828,7 +921,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
     }
   } else {
     for (int s = g; s < parts; s += 4) {
-      const float2 v = ml[(int64_t)s * rows];
+      const float2 v = ml[s * step];
       sum += v.y * __builtin_amdgcn_exp2f(v.x - zero);
     }
   }
@@ -852,7 +945,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
 // How a call is laid out.
 struct AttendPlan {
   int rows;                     // query rows of a workgroup
-  int mblocks, group, splits, chunk;
+  int mblocks, group, parts, goal, least;
   size_t ml, o, total;
 };
 AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
@@ -861,18 +954,17 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
   const int rows = max_q * p.group;
   p.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.mblocks = (rows + p.rows - 1) / p.rows;
-  // enough workgroups for the chip, of at least 128 rows (one step of four waves)
-  const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
-  const int64_t want = p.rows == 16 ? 1024 : 256;
-  const int most = (b.max_len + 127) / 128;
-  int64_t s = (want + units - 1) / units;
-  if (s > most) s = most;
-  p.chunk = (int)((((int64_t)b.max_len + s - 1) / s + 127) / 128 * 128);
-  p.splits = (b.max_len + p.chunk - 1) / p.chunk;
-  const size_t parts = p.splits > 1 ? (size_t)b.batch * b.n_kv * p.splits * rows : 0;
+  // enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS
+  const int per_part = b.n_kv * p.mblocks, want = p.rows == 16 ? 1024 : 256;
+  p.least = p.rows == 16 ? 256 : 128;
+  p.goal = (want + per_part - 1) / per_part;
+  if (p.goal <= b.batch || b.max_len <= p.least) p.goal = 0;
+  const int64_t most = (int64_t)b.batch * ((b.max_len + p.least - 1) / p.least);
+  p.parts = p.goal == 0 ? b.batch : most < p.goal + b.batch ? (int)most : p.goal + b.batch;
+  const size_t held = p.goal ? (size_t)p.parts * b.n_kv * rows : 0;
   p.ml = kStatusBytes;
-  p.o = p.ml + align256(parts * sizeof(float2));
-  p.total = p.o + align256(parts * b.hd * sizeof(float));
+  p.o = p.ml + align256(held * sizeof(float2));
+  p.total = p.o + align256(held * b.hd * sizeof(float));
   return p;
 }
 
@@ -892,7 +984,7 @@ void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStr
     launch_rows<HD, true>(a, p.rows, grid, stream);
   else
     launch_rows<HD, false>(a, p.rows, grid, stream);
-  if (p.splits > 1) {
+  if (p.goal) {
     const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
     hipLaunchKernelGGL((join_kernel<HD>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
                        stream, a);
@@ -922,8 +1014,9 @@ hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp,
   a.part_o = reinterpret_cast<float*>(w + p.o);
   a.out_stride = out_stride;
   a.page = divide_by((unsigned)b.page_size);
-  a.splits = p.splits;
-  a.chunk = p.chunk;
+  a.parts = p.parts;
+  a.goal = p.goal;
+  a.least = p.least;
   a.mblocks = p.mblocks;
   a.group = p.group;
   a.scan = scans(b) ? 1 : 0;
@@ -931,7 +1024,7 @@ hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp,
     const hipError_t e = launch_clear_status(a.status, stream);
     if (e != hipSuccess) return e;
   }
-  const int64_t grid = (int64_t)b.batch * b.n_kv * p.splits * p.mblocks + a.scan;
+  const int64_t grid = (int64_t)p.parts * b.n_kv * p.mblocks + a.scan;
   if (b.hd == 128)
     launch_head<128>(a, p, (unsigned)grid, stream);
   else
