@@ -353,28 +353,31 @@ def ridgefill_value_scale(shape: rf_shape, x_S_tail, x_l_tail: list, layers: lis
 # the tensors' own device and, unless a stream is given, on that device's current stream.
 
 def _need(name: str, t, dtype, device, ndim: int) -> None:
-    if t.dtype != dtype or t.device != device or t.dim() != ndim:
+    if t.dtype is not dtype or t.device != device or t.dim() != ndim:
         raise ValueError(f"{name} must be a {dtype} tensor of {ndim} dimensions on {device}, not "
                          f"{t.dtype} of {t.dim()} on {t.device}")
 
 
 def _flat(name: str, t, dtype, device, ndim: int, shape: tuple | None = None) -> None:
     """A contiguous tensor, of the given shape where one is given."""
+    if (t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (t.shape == shape if shape is not None else t.dim() == ndim)):
+        return
     _need(name, t, dtype, device, ndim)
-    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be contiguous" + (f" {shape}" if shape else "") +
-                         f", not {tuple(t.shape)} with strides {t.stride()}")
+    raise ValueError(f"{name} must be contiguous" + (f" {shape}" if shape else "") +
+                     f", not {tuple(t.shape)} with strides {t.stride()}")
 
 
 def _rows_of(name: str, t, dtype, device, width: int, n: int | None = None) -> int:
     """Elements between the rows of [rows][heads][head_dim]; each row lies in one piece."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is dtype and t.device == device and len(shape) == 3 and shape[2] == width
+            and stride[2] == 1 and (stride[1] == width or shape[1] == 1) and shape[1] > 0
+            and (n is None or shape[0] == n)):
+        return stride[0] if shape[0] > 1 else max(shape[1] * width, stride[0])
     _need(name, t, dtype, device, 3)
-    rows, heads, hd = t.shape
-    a, b, c = t.stride()
-    if heads == 0 or hd != width or (n is not None and rows != n) or c != 1 or (heads > 1 and b != hd):
-        raise ValueError(f"{name} must be [{'rows' if n is None else n}][heads][{width}] with each "
-                         f"row in one piece, not {tuple(t.shape)} with strides {t.stride()}")
-    return a if rows > 1 else max(heads * hd, a)
+    raise ValueError(f"{name} must be [{'rows' if n is None else n}][heads][{width}] with each "
+                     f"row in one piece, not {tuple(shape)} with strides {stride}")
 
 
 def _go(f, device, stream, *args) -> None:
@@ -382,8 +385,12 @@ def _go(f, device, stream, *args) -> None:
     import torch
     if device.type != "cuda":
         raise ValueError(f"the tensors must be in GPU memory, not on {device}")
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
+    index = device.index
+    if stream is None:      # the handle alone: a stream object takes longer to make than the checks
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream.cuda_stream
+    if index == torch.cuda.current_device():
         status = f(*args, handle)
     else:
         with torch.cuda.device(device):
