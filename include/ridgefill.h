@@ -527,7 +527,7 @@ rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int
  *   k, v        device bf16 [n_rows][n_kv_heads][head_dim]; the strides (elements between
  *               rows) are multiples of 8, all pointers 16-byte aligned
  *   seq         device int32 [n_rows] or NULL (all rows belong to sequence 0); a negative
- *               entry marks a padding row: nothing of it is read or written
+ *               entry marks a padding row: nothing of it is written
  *   rows        device int32 [n_rows]: cache rows in [0, kv->max_len)
  *   positions   device int32 [n_rows], the angles' positions, or NULL (the cache rows)
  *   status      device uint32 (4-byte aligned): receives the device status word of the

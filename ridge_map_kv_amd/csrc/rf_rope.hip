@@ -6,9 +6,10 @@
 // heads, so a workgroup forms them once per row, in LDS: the angle in turns as an fp64
 // product, its nearest integer taken off in fp64 (positions up to 2^31 keep an error below
 // 1e-6 turns at f = 1/(2 pi)), then cos and sin of pi times the fp32 rest.
-// Everything else is one read and one write of the data, 16 bytes per lane.
-#include "rf_cache.h"
-#include "rf_common.h"
+// Everything else is one read and one write of the data.  A thread turns units of two 16-byte
+// pieces half the rotated width apart, in either layout, so that neighbouring lanes read
+// neighbouring pieces; its first units are on their way while cos and sin are formed.
+#include "rf_cache_dev.h"
 #include "ridgefill.h"
 
 namespace rf {
@@ -17,15 +18,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sixteen features of a head: the first 8 and the last 8 are loaded 16 (bf16) or 32 (fp32)
-// bytes at a time.
+// 16 bytes of a head: 8 (bf16) or 4 (fp32) features.
 template <typename T>
-struct Half8;
+struct Piece;
 template <>
-struct Half8<uint16_t> {
+struct Piece<uint16_t> {
+  static constexpr int kN = 8;
   u32x4 r;
-  __device__ void load(const uint16_t* p) { r = *reinterpret_cast<const u32x4*>(p); }
-  __device__ void store(uint16_t* p) const { *reinterpret_cast<u32x4*>(p) = r; }
   __device__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -39,29 +38,16 @@ struct Half8<uint16_t> {
   }
 };
 template <>
-struct Half8<float> {
-  f32x4 a, b;
-  __device__ void load(const float* p) {
-    a = *reinterpret_cast<const f32x4*>(p);
-    b = *reinterpret_cast<const f32x4*>(p + 4);
-  }
-  __device__ void store(float* p) const {
-    *reinterpret_cast<f32x4*>(p) = a;
-    *reinterpret_cast<f32x4*>(p + 4) = b;
-  }
-  __device__ void get(float (&f)[8]) const {
+struct Piece<float> {
+  static constexpr int kN = 4;
+  u32x4 r;
+  __device__ void get(float (&f)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i];
-      f[4 + i] = b[i];
-    }
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
   }
-  __device__ void set(const float (&f)[8]) {
+  __device__ void set(const float (&f)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = f[i];
-      b[i] = f[4 + i];
-    }
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(f[i]);
   }
 };
 
@@ -74,39 +60,34 @@ __device__ __forceinline__ float2 turn_of(const RopeFreq& f, int j, int pos, flo
   return make_float2(f.m * c, sign * f.m * s);
 }
 
-// Where unit u (16 features) of a head lies: the offsets of its two runs of 8 features and,
-// when they rotate, its first pair.  Units past the rotated part pass unchanged (pair < 0).
+// Where the two pieces of unit u of a head lie, and the first pair of each when they rotate.  Units
+// past the rotated part pass unchanged (pair < 0).
 struct Unit {
-  int lo, hi, pair;
+  int lo, hi, pair_lo, pair_hi;
 };
-__device__ __forceinline__ Unit unit_of(const RopeFreq& f, int u) {
-  Unit w;
-  if (u * 16 >= f.rot) {
-    w.lo = u * 16;
-    w.hi = u * 16 + 8;
-    w.pair = -1;
-  } else if (f.layout == RF_ROPE_HALF) {
-    w.lo = u * 8;
-    w.hi = f.rot / 2 + u * 8;
-    w.pair = u * 8;
-  } else {
-    w.lo = u * 16;
-    w.hi = u * 16 + 8;
-    w.pair = u * 8;
+template <typename T>
+__device__ __forceinline__ Unit unit_of(const RopeFreq& f, int hd, int u) {
+  constexpr int kN = Piece<T>::kN;
+  const int turned = f.rot / (2 * kN), half = f.rot / 2;
+  if (u >= turned) {
+    const int lo = f.rot + (u - turned) * kN;
+    return {lo, lo + (hd - f.rot) / 2, -1, -1};
   }
-  return w;
+  if (f.layout == RF_ROPE_HALF) return {u * kN, half + u * kN, u * kN, u * kN};
+  return {u * kN, half + u * kN, u * kN / 2, (half + u * kN) / 2};
 }
 
 template <typename T>
-__device__ __forceinline__ void turn_unit(Half8<T>& lo, Half8<T>& hi, const float2* cs,
+__device__ __forceinline__ void turn_unit(Piece<T>& lo, Piece<T>& hi, const float2* cs, const Unit& u,
                                           bool interleaved) {
-  float a[8], b[8];
+  constexpr int kN = Piece<T>::kN;
+  float a[kN], b[kN];
   lo.get(a);
   hi.get(b);
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = cs[i], q = cs[4 + i];
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 p = cs[u.pair_lo + i], q = cs[u.pair_hi + i];
       const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
       a[2 * i] = a0 * p.x - a1 * p.y;
       a[2 * i + 1] = a1 * p.x + a0 * p.y;
@@ -115,8 +96,8 @@ __device__ __forceinline__ void turn_unit(Half8<T>& lo, Half8<T>& hi, const floa
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 p = cs[i];
+    for (int i = 0; i < kN; ++i) {
+      const float2 p = cs[u.pair_lo + i];
       const float x = a[i], y = b[i];
       a[i] = x * p.x - y * p.y;
       b[i] = y * p.x + x * p.y;
@@ -126,121 +107,177 @@ __device__ __forceinline__ void turn_unit(Half8<T>& lo, Half8<T>& hi, const floa
   hi.set(b);
 }
 
-// Rows [blockIdx.x * per, + per): their cos and sin into LDS, then units in turn.
+// Turns the units of a workgroup's rows, kUnits of them to a thread at a time.  place(i) says
+// where unit i's data come from, dest(i) where they go to (null: nowhere); between() prepares what
+// dest and the rotation take, with the first units' loads under way.
+constexpr int kUnits = 2;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeFreq f, RopeCall c, int per) {
+struct Place {
+  const T* x;                   // null: no such unit
+  const float2* cs;
+  Unit u;
+};
+template <typename T, typename Where, typename To, typename Between>
+__device__ __forceinline__ void turn_rows(int total, bool interleaved, Where place, To dest, Between between) {
+  for (int i0 = 0; i0 == 0 || i0 < total; i0 += kUnits * kThreads) {
+    Place<T> p[kUnits];
+    Piece<T> lo[kUnits], hi[kUnits];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const int i = i0 + j * kThreads + (int)threadIdx.x;
+      p[j].x = nullptr;
+      if (i < total) p[j] = place(i);
+      if (p[j].x) {
+        lo[j].r = *reinterpret_cast<const u32x4*>(p[j].x + p[j].u.lo);
+        hi[j].r = *reinterpret_cast<const u32x4*>(p[j].x + p[j].u.hi);
+      }
+    }
+    if (i0 == 0) {
+      between();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      if (!p[j].x) continue;
+      if (p[j].u.pair_lo >= 0) turn_unit<T>(lo[j], hi[j], p[j].cs, p[j].u, interleaved);
+      T* y = dest(i0 + j * kThreads + (int)threadIdx.x);
+      if (!y) continue;
+      *reinterpret_cast<u32x4*>(y + p[j].u.lo) = lo[j].r;
+      *reinterpret_cast<u32x4*>(y + p[j].u.hi) = hi[j].r;
+    }
+  }
+}
+
+// Divisions of a unit's number in a workgroup into row, head and unit of the head; of a cache row
+// into pages.
+struct Units {
+  Divide row, head, page;
+};
+
+// Rows [blockIdx.x * per, + per).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeFreq f, RopeCall c, Units d, int per) {
   extern __shared__ float2 cs[];                    // [per][rot / 2]
   const int64_t row0 = (int64_t)blockIdx.x * per;
   const int rows = (int)(c.n - row0 < per ? c.n - row0 : per);
   const int pairs = f.rot / 2;
-  for (int i = threadIdx.x; i < rows * pairs; i += kThreads)
-    cs[i] = turn_of(f, i % pairs, c.pos[row0 + i / pairs], c.transpose ? -1.f : 1.f);
-  __syncthreads();
-  const int units = c.hd / 16, per_row = c.heads * units;
-  for (int i = threadIdx.x; i < rows * per_row; i += kThreads) {
-    const int r = i / per_row, w = i % per_row, h = w / units;
-    const Unit u = unit_of(f, w % units);
-    const T* x = static_cast<const T*>(c.x) + (row0 + r) * c.x_stride + h * c.hd;
-    T* y = static_cast<T*>(c.out) + (row0 + r) * c.out_stride + h * c.hd;
-    Half8<T> lo, hi;
-    lo.load(x + u.lo);
-    hi.load(x + u.hi);
-    if (u.pair >= 0) turn_unit(lo, hi, cs + r * pairs + u.pair, f.layout != RF_ROPE_HALF);
-    lo.store(y + u.lo);
-    hi.store(y + u.hi);
-  }
+  turn_rows<T>(
+      rows * (int)d.row.d, f.layout != RF_ROPE_HALF,
+      [&](int i) -> Place<T> {
+        const int r = (int)quotient((unsigned)i, d.row), w = i - r * (int)d.row.d, h = (int)quotient((unsigned)w, d.head);
+        return {static_cast<const T*>(c.x) + (row0 + r) * c.x_stride + h * c.hd, cs + r * pairs,
+                unit_of<T>(f, c.hd, w - h * (int)d.head.d)};
+      },
+      [&](int i) -> T* {
+        const int r = (int)quotient((unsigned)i, d.row), w = i - r * (int)d.row.d, h = (int)quotient((unsigned)w, d.head);
+        return static_cast<T*>(c.out) + (row0 + r) * c.out_stride + h * c.hd;
+      },
+      [&] {
+        for (int i = threadIdx.x; i < rows * pairs; i += kThreads)
+          cs[i] = turn_of(f, i % pairs, c.pos[row0 + i / pairs], c.transpose ? -1.f : 1.f);
+      });
 }
 
-// Pool slot of cache row `row` of sequence `seq`, or -1 if any of them is out of range.
-__device__ __forceinline__ int append_slot(const Batch& b, int seq, int row) {
-  if (seq >= b.batch || row < 0 || row >= b.max_len) return -1;
-  const int page = b.tables[(int64_t)seq * b.table_stride + row / b.page_size];
-  if (page < 0 || page >= b.num_pages) return -1;
-  return page * b.page_size + row % b.page_size;
+// Pool slot of cache row `row` of sequence `seq`, or -1 if any of them is out of range (then the
+// table's first entry is looked at instead: no branch keeps several lookups from running together).
+__device__ __forceinline__ int append_slot(const Batch& b, Divide by_page, int seq, int row) {
+  const bool in = seq < b.batch && row >= 0 && row < b.max_len;
+  const int pi = in ? (int)quotient((unsigned)row, by_page) : 0;
+  const int page = b.tables[(int64_t)(in ? seq : 0) * b.table_stride + pi];
+  return in && page >= 0 && page < b.num_pages ? page * b.page_size + (row - pi * b.page_size) : -1;
 }
 
 // The same for the append: heads 0 .. n_q-1 of a row are q, then k (rotated into the key
-// pages), then v (copied).  The last workgroup writes the status word: it alone looks all
+// pages), then v (copied).  The first workgroup writes the status word: it alone looks all
 // rows over, beside the others' work, so that the word needs no clearing launch.
 __global__ __launch_bounds__(kThreads) void append_kernel(RopeFreq f, Batch b, AppendCall c,
-                                                          int per) {
-  extern __shared__ float2 cs[];
-  if (blockIdx.x == gridDim.x - 1) {
+                                                          Units d, int per) {
+  extern __shared__ float2 cs[];                    // [per][rot / 2], then the rows' slots
+  if (blockIdx.x == 0) {
     int bad = 0;
-    for (int64_t i = threadIdx.x; i < c.n; i += kThreads) {
-      const int s = c.seq ? c.seq[i] : 0;
-      if (s >= 0 && append_slot(b, s, c.rows[i]) < 0) bad = 1;
+    for (int64_t i0 = threadIdx.x; i0 < c.n; i0 += 8 * kThreads) {   // eight lookups at a time
+      int slot[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = i0 + j * kThreads < c.n ? i0 + j * kThreads : i0;
+        const int s = c.seq ? c.seq[i] : 0;
+        const int at = append_slot(b, d.page, s < 0 ? 0 : s, c.rows[i]);
+        slot[j] = s < 0 ? 0 : at;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bad |= slot[j] < 0;
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *c.status = bad ? kStatusRowsBit : 0u;
     return;
   }
-  const int64_t row0 = (int64_t)blockIdx.x * per;
+  const int64_t row0 = (int64_t)(blockIdx.x - 1) * per;
   const int rows = (int)(c.n - row0 < per ? c.n - row0 : per);
   const int pairs = f.rot / 2;
+  int* slots = reinterpret_cast<int*>(cs + per * pairs);
   const int32_t* pos = c.pos ? c.pos : c.rows;
-  for (int i = threadIdx.x; i < rows * pairs; i += kThreads)
-    cs[i] = turn_of(f, i % pairs, pos[row0 + i / pairs], 1.f);
-  __syncthreads();
-  const int units = b.hd / 16, per_row = (c.n_q + 2 * b.n_kv) * units;
-  for (int i = threadIdx.x; i < rows * per_row; i += kThreads) {
-    const int r = i / per_row, w = i % per_row;
-    int h = w / units;
-    const int64_t row = row0 + r;
-    const int s = c.seq ? c.seq[row] : 0;
-    if (s < 0) continue;
-    Unit u = unit_of(f, w % units);
-    const uint16_t* x;
-    uint16_t* y;
-    if (h < c.n_q) {
-      x = c.q + row * c.q_stride + h * b.hd;
-      y = c.q_out + row * c.qo_stride + h * b.hd;
-    } else {
-      h -= c.n_q;
-      const bool val = h >= b.n_kv;
-      if (val) {
-        h -= b.n_kv;
-        u.pair = -1;
-      }
-      const int slot = append_slot(b, s, c.rows[row]);
-      if (slot < 0) continue;
-      x = (val ? c.v + row * c.v_stride : c.k + row * c.k_stride) + h * b.hd;
-      y = (val ? c.vp : c.kp) + ((int64_t)slot * b.n_kv + h) * b.hd;
-    }
-    Half8<uint16_t> lo, hi;
-    lo.load(x + u.lo);
-    hi.load(x + u.hi);
-    if (u.pair >= 0) turn_unit(lo, hi, cs + r * pairs + u.pair, f.layout != RF_ROPE_HALF);
-    lo.store(y + u.lo);
-    hi.store(y + u.hi);
-  }
+  turn_rows<uint16_t>(
+      rows * (int)d.row.d, f.layout != RF_ROPE_HALF,
+      [&](int i) -> Place<uint16_t> {
+        const int r = (int)quotient((unsigned)i, d.row), w = i - r * (int)d.row.d;
+        const int h = (int)quotient((unsigned)w, d.head);
+        const int64_t row = row0 + r;
+        Place<uint16_t> p = {c.v + row * c.v_stride + (h - c.n_q - b.n_kv) * b.hd, cs + r * pairs,
+                             unit_of<uint16_t>(f, b.hd, w - h * (int)d.head.d)};
+        if (h < c.n_q)
+          p.x = c.q + row * c.q_stride + h * b.hd;
+        else if (h < c.n_q + b.n_kv)
+          p.x = c.k + row * c.k_stride + (h - c.n_q) * b.hd;
+        else
+          p.u.pair_lo = -1;                             // v is copied
+        return p;
+      },
+      [&](int i) -> uint16_t* {
+        const int r = (int)quotient((unsigned)i, d.row), h = (int)quotient((unsigned)(i - r * (int)d.row.d), d.head);
+        const int slot = slots[r];
+        if (h < c.n_q) return slot == -2 ? nullptr : c.q_out + (row0 + r) * c.qo_stride + h * b.hd;
+        if (slot < 0) return nullptr;
+        const int kh = h - c.n_q;
+        return kh < b.n_kv ? c.kp + ((int64_t)slot * b.n_kv + kh) * b.hd : c.vp + ((int64_t)slot * b.n_kv + kh - b.n_kv) * b.hd;
+      },
+      [&] {
+        for (int r = threadIdx.x; r < rows; r += kThreads) {
+          const int s = c.seq ? c.seq[row0 + r] : 0;
+          const int at = append_slot(b, d.page, s < 0 ? 0 : s, c.rows[row0 + r]);
+          slots[r] = s < 0 ? -2 : at;                   // -2: a padding row
+        }
+        for (int i = threadIdx.x; i < rows * pairs; i += kThreads)
+          cs[i] = turn_of(f, i % pairs, pos[row0 + i / pairs], 1.f);
+      });
 }
 
-// Rows per workgroup: enough that its threads all have a unit, one for wide rows.
+// Rows per workgroup: enough that its threads all have two units, one for wide rows.
 int rows_per_block(int per_row) {
-  const int per = kThreads / per_row;
+  const int per = kUnits * kThreads / per_row;
   return per < 1 ? 1 : per > 32 ? 32 : per;
 }
 
 }  // namespace
 
 hipError_t launch_rope(const RopeFreq& f, const RopeCall& c, bool f32, hipStream_t stream) {
-  const int per = rows_per_block(c.heads * c.hd / 16);
+  const int units = c.hd / (f32 ? 8 : 16), per = rows_per_block(c.heads * units);
+  const Units d = {divide_by((unsigned)(c.heads * units)), divide_by((unsigned)units), divide_by(1u)};
   const dim3 grid((unsigned)((c.n + per - 1) / per));
   const size_t lds = (size_t)per * (f.rot / 2) * sizeof(float2);
   if (f32)
-    hipLaunchKernelGGL(rope_kernel<float>, grid, dim3(kThreads), lds, stream, f, c, per);
+    hipLaunchKernelGGL(rope_kernel<float>, grid, dim3(kThreads), lds, stream, f, c, d, per);
   else
-    hipLaunchKernelGGL(rope_kernel<uint16_t>, grid, dim3(kThreads), lds, stream, f, c, per);
+    hipLaunchKernelGGL(rope_kernel<uint16_t>, grid, dim3(kThreads), lds, stream, f, c, d, per);
   return hipGetLastError();
 }
 
 hipError_t launch_append(const RopeFreq& f, const Batch& b, const AppendCall& c,
                          hipStream_t stream) {
-  const int per = rows_per_block((c.n_q + 2 * b.n_kv) * b.hd / 16);
+  const int units = b.hd / 16, per_row = (c.n_q + 2 * b.n_kv) * units, per = rows_per_block(per_row);
+  const Units d = {divide_by((unsigned)per_row), divide_by((unsigned)units), divide_by((unsigned)b.page_size)};
   const dim3 grid((unsigned)((c.n + per - 1) / per) + 1);
-  const size_t lds = (size_t)per * (f.rot / 2) * sizeof(float2);
-  hipLaunchKernelGGL(append_kernel, grid, dim3(kThreads), lds, stream, f, b, c, per);
+  const size_t lds = (size_t)per * ((f.rot / 2) * sizeof(float2) + sizeof(int));
+  hipLaunchKernelGGL(append_kernel, grid, dim3(kThreads), lds, stream, f, b, c, d, per);
   return hipGetLastError();
 }
 
