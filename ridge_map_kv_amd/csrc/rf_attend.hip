@@ -215,8 +215,8 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   constexpr int kSteps = HD / 32, kFeat = HD / 16;
   __shared__ float sh_o[kWaves / 2][16 * MT][HD + 4];
   __shared__ float2 sh_ml[kWaves / 2][16 * MT];
-  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
-  int unit = blockIdx.x, mb = 0;
+  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
+  int unit = blockIdx.x - a.scan, mb = 0;
   place_block(a, &unit, &mb);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -553,8 +553,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   __shared__ __attribute__((aligned(256))) unsigned char sh_kv[kBufs * kBufBytes * (kOut ? 2 : 1)];
   __shared__ int sh_slot[kSlots];
   __shared__ unsigned long long sh_wild;      // drafts with a value that is not finite, a bit each
-  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
-  int unit = blockIdx.x, mb = 0;
+  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
+  int unit = blockIdx.x - a.scan, mb = 0;
   place_block(a, &unit, &mb);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;

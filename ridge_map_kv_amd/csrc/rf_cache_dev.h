@@ -54,29 +54,34 @@ __device__ __forceinline__ uint64_t seen64(uint64_t word, int d) {
   return d <= -64 ? ~0ull : word << -d | ((1ull << -d) - 1ull);
 }
 
-// The status word from one workgroup: every sequence and every page that it uses.
+// The status word from one workgroup: every sequence and every page that it uses, eight lookups
+// of a thread at a time.
 __device__ inline void scan_status(const Batch& b, const Queries& q, unsigned* status) {
+  const int each = (b.max_len - 1) / b.page_size + 1, total = b.batch * each;
   int bits = 0;
-  for (int s = 0; s < b.batch; ++s) {
-    int len, first, n;
-    bool bad;
-    if (sequence_of(b, q, s, &len, &first, &n, &bad)) {
-      const int pages = (len + b.page_size - 1) / b.page_size;
-      for (int i = threadIdx.x; i < pages; i += blockDim.x) {
-        const int page = b.tables[(int64_t)s * b.table_stride + i];
-        if (page < 0 || page >= b.num_pages) bits = 1;
-      }
+  for (int i0 = threadIdx.x; i0 < total; i0 += 8 * blockDim.x) {
+    bool wrong[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * (int)blockDim.x < total ? i0 + j * (int)blockDim.x : i0;
+      const int s = i / each, p = i - s * each;
+      int len, first, n;
+      bool bad;
+      const bool go = sequence_of(b, q, s, &len, &first, &n, &bad);
+      const int page = b.tables[(int64_t)s * b.table_stride + p];
+      wrong[j] = bad || (go && (int64_t)p * b.page_size < len && (page < 0 || page >= b.num_pages));
     }
-    if (bad) bits = 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bits |= wrong[j];
   }
   bits = __syncthreads_or(bits);
   if (threadIdx.x == 0) *status = bits ? kStatusRowsBit : 0u;
 }
 
 // The status word is written by a workgroup that scans the tables beside the others where that
-// takes no longer than they do (8,192 entries: a few microseconds); else cleared first.
+// takes no longer than they do (4,096 entries: two rounds of lookups); else it is cleared first.
 inline bool scans(const Batch& b) {
-  return (int64_t)b.batch * ((b.max_len + b.page_size - 1) / b.page_size) <= 8192;
+  return (int64_t)b.batch * ((b.max_len - 1) / b.page_size + 1) <= 4096;
 }
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {

@@ -25,6 +25,8 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 64;             // cache rows of one step of a wave
 constexpr int kBlock = 256;           // query rows in LDS
+constexpr int kHeadWaves = 8;         // waves that share them
+constexpr int kHeadThreads = 64 * kHeadWaves;
 
 struct WeightArgs {
   Batch b;
@@ -77,19 +79,25 @@ template <int HD>
 __device__ __forceinline__ void add_weights(const Keys<HD>& keys, const bf16x8 (&q)[HD / 32],
                                             float scale2, float lse2, bool some, uint64_t seen,
                                             int g, float (&w)[4][4]) {
+  f32x4 s[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < 4; ++t) s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int st = 0; st < HD / 32; ++st) s = mfma16(__builtin_bit_cast(bf16x8, keys.k[t][st]), q[st], s);
-    if (!some) {
+  for (int st = 0; st < HD / 32; ++st)                // four independent sums side by side
 #pragma unroll
-      for (int r = 0; r < 4; ++r) w[t][r] += __builtin_amdgcn_exp2f(fmaf(s[r], scale2, -lse2));
-    } else {
+    for (int t = 0; t < 4; ++t) s[t] = mfma16(__builtin_bit_cast(bf16x8, keys.k[t][st]), q[st], s[t]);
+  if (!some) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[t][r] += __builtin_amdgcn_exp2f(fmaf(s[t][r], scale2, -lse2));
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
       const uint32_t bits = (uint32_t)(seen >> (16 * t + 4 * g));
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        w[t][r] += bits >> r & 1 ? __builtin_amdgcn_exp2f(fmaf(s[r], scale2, -lse2)) : 0.f;
+        w[t][r] += bits >> r & 1 ? __builtin_amdgcn_exp2f(fmaf(s[t][r], scale2, -lse2)) : 0.f;
     }
   }
 }
@@ -113,8 +121,8 @@ template <int HD, int MT>
 __global__ __launch_bounds__(kThreads) void weight_rows_kernel(WeightArgs a) {
   constexpr int kSteps = HD / 32;
   __shared__ float sh[kWaves][kRows];
-  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
-  const int seq = blockIdx.x / a.splits, lane = threadIdx.x & 63;
+  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
+  const int id = blockIdx.x - a.scan, seq = id / a.splits, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int hw = a.b.n_kv >= 4 ? 4 : a.b.n_kv >= 2 ? 2 : 1;
@@ -122,8 +130,8 @@ __global__ __launch_bounds__(kThreads) void weight_rows_kernel(WeightArgs a) {
   bool bad;
   const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
   if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
-  const int base = (blockIdx.x % a.splits) * a.chunk + wave / hw * kRows;
-  if (!go || (blockIdx.x % a.splits) * a.chunk >= len) return;
+  const int base = (id % a.splits) * a.chunk + wave / hw * kRows;
+  if (!go || (id % a.splits) * a.chunk >= len) return;
   const int ctx = len - n, m_rows = n * a.group;
   const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
   bool err = false;
@@ -179,48 +187,30 @@ __global__ __launch_bounds__(kThreads) void weight_rows_kernel(WeightArgs a) {
 
 // M > 64: workgroup = one key head, a block of its query rows, a range of cache rows.
 template <int HD>
-__global__ __launch_bounds__(kThreads, 2) void weight_heads_kernel(WeightArgs a) {
+__global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArgs a) {
   constexpr int kSteps = HD / 32;
   __shared__ u32x4 sh_q[kBlock / 16][kSteps][64];   // as the lanes read them
-  __shared__ float sh_lse[kBlock];
+  __shared__ float sh_lse[kBlock];                  // in log2
   __shared__ uint64_t sh_word[kBlock];
-  if (a.scan && blockIdx.x == gridDim.x - 1) return scan_status(a.b, a.q, a.status);
-  const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
+  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
+  const int id = blockIdx.x - a.scan, split = id % a.splits, unit = id / a.splits;
   const int mb = unit % a.mblocks, kh = unit / a.mblocks % a.b.n_kv, seq = unit / a.mblocks / a.b.n_kv;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   int len, first, n;
   bool bad;
   const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
-  if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  if (bad && !a.scan && tid == 0) atomicOr(a.status, kStatusRowsBit);
   const int begin = split * a.chunk, m0 = mb * kBlock;
   const int m_rows = n * a.group - m0 < kBlock ? n * a.group - m0 : kBlock;
   if (!go || begin >= len || m_rows <= 0) return;
   const int end = len < begin + a.chunk ? len : begin + a.chunk;
   const int ctx = len - n, tiles = (m_rows + 15) / 16;
 
-  for (int x = threadIdx.x; x < tiles * 16 * (HD / 8); x += kThreads) {
-    const int m = x / (HD / 8), ch = x % (HD / 8);
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (m < m_rows) {
-      const int i = (m0 + m) / a.group, h = kh * a.group + (m0 + m) % a.group;
-      v = *reinterpret_cast<const u32x4*>(a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * ch);
-    }
-    sh_q[m / 16][ch / 4][ch % 4 * 16 + m % 16] = v;
-  }
-  for (int m = threadIdx.x; m < tiles * 16; m += kThreads) {
-    const int i = (m0 + m) / a.group, h = kh * a.group + (m0 + m) % a.group;
-    const bool in = m < m_rows;
-    sh_lse[m] = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] : -INFINITY;
-    sh_word[m] = in ? draft_word(a.q, first + i, i) : 0ull;
-  }
-  __syncthreads();
-
+  // the first rows on their way, then Q into LDS
   const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
   const uint16_t* kbase = a.kp + kh * HD;
   const int64_t row_size = (int64_t)a.b.n_kv * HD;
-  float* part = a.part + ((int64_t)(seq * a.b.n_kv + kh) * a.mblocks + mb) * a.b.max_len;
-  const float scale2 = a.q.scale * kLog2e;
   bool err = false;
   int base = begin + wave * kRows;
   Keys<HD> keys;
@@ -229,8 +219,31 @@ __global__ __launch_bounds__(kThreads, 2) void weight_heads_kernel(WeightArgs a)
     slot = key_slot(a, table, base + lane, len, &err);
     load_keys<HD>(keys, kbase, row_size, slot < 0 ? 0 : slot, c, g);
   }
-  for (; base < end; base += kWaves * kRows) {
-    const int ahead = base + kWaves * kRows;
+  constexpr int kPieces = kBlock * (HD / 8) / kHeadThreads;
+  u32x4 piece[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int x = tid + j * kHeadThreads, m = x / (HD / 8), ch = x % (HD / 8), mc = m < m_rows ? m : m_rows - 1;
+    const int i = (m0 + mc) / a.group, h = kh * a.group + (m0 + mc) % a.group;
+    piece[j] = *reinterpret_cast<const u32x4*>(a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * ch);
+  }
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int x = tid + j * kHeadThreads, m = x / (HD / 8), ch = x % (HD / 8);
+    sh_q[m / 16][ch / 4][ch % 4 * 16 + m % 16] = m < m_rows ? piece[j] : u32x4{0u, 0u, 0u, 0u};
+  }
+  for (int m = tid; m < kBlock; m += kHeadThreads) {
+    const bool in = m < m_rows;
+    const int i = in ? (m0 + m) / a.group : 0, h = kh * a.group + (in ? (m0 + m) % a.group : 0);
+    sh_lse[m] = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] * kLog2e : -INFINITY;
+    sh_word[m] = in ? draft_word(a.q, first + i, i) : 0ull;
+  }
+  __syncthreads();
+
+  float* part = a.part + ((int64_t)(seq * a.b.n_kv + kh) * a.mblocks + mb) * a.b.max_len;
+  const float scale2 = a.q.scale * kLog2e;
+  for (; base < end; base += kHeadWaves * kRows) {
+    const int ahead = base + kHeadWaves * kRows;
     int slot_next = -1;
     Keys<HD> next;
     if (ahead < end) {
@@ -244,15 +257,23 @@ __global__ __launch_bounds__(kThreads, 2) void weight_heads_kernel(WeightArgs a)
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) w[t][r] = 0.f;
+    bf16x8 q_next[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q_next[s] = __builtin_bit_cast(bf16x8, sh_q[0][s][lane]);
+    float l_next = sh_lse[c];
     for (int qt = 0; qt < tiles; ++qt) {
       bf16x8 q[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(bf16x8, sh_q[qt][s][lane]);
-      const float l = sh_lse[16 * qt + c];
+      for (int s = 0; s < kSteps; ++s) q[s] = q_next[s];
+      const float l = l_next;
+      const int nt = qt + 1 < tiles ? qt + 1 : qt;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q_next[s] = __builtin_bit_cast(bf16x8, sh_q[nt][s][lane]);
+      l_next = sh_lse[16 * nt + c];
       const bool live = l != -INFINITY;
       uint64_t seen = live ? there : 0ull;
       if (base + kRows > ctx) seen &= seen64(sh_word[16 * qt + c], base - ctx);
-      add_weights<HD>(keys, q, scale2, l * kLog2e, part_rows || __any(!live), seen, g, w);
+      add_weights<HD>(keys, q, scale2, l, part_rows || __any(!live), seen, g, w);
     }
     f32x4 mine = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -309,10 +330,10 @@ WeightPlan weight_plan(const Batch& b, int n_heads, int max_q) {
   }
   p.mt = 0;
   p.mblocks = (rows + kBlock - 1) / kBlock;
-  // two workgroups to a compute unit, each of at least one step of its waves
+  // one workgroup to a compute unit, each of at least one step of its waves
   const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
-  int64_t s = (512 + units - 1) / units;
-  const int step = kWaves * kRows, most = (b.max_len + step - 1) / step;
+  int64_t s = (256 + units - 1) / units;
+  const int step = kHeadWaves * kRows, most = (b.max_len + step - 1) / step;
   if (s > most) s = most;
   p.chunk = (int)((((int64_t)b.max_len + s - 1) / s + step - 1) / step * step);
   p.splits = (b.max_len + p.chunk - 1) / p.chunk;
@@ -331,7 +352,7 @@ void launch_weight_head(const WeightArgs& a, const WeightPlan& p, hipStream_t st
   } else if (p.mt == 4) {
     hipLaunchKernelGGL((weight_rows_kernel<HD, 4>), grid, block, 0, stream, a);
   } else {
-    hipLaunchKernelGGL((weight_heads_kernel<HD>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((weight_heads_kernel<HD>), grid, dim3(kHeadThreads), 0, stream, a);
     hipLaunchKernelGGL(weight_sum_kernel, dim3((a.b.max_len + kThreads - 1) / kThreads, a.b.batch),
                        block, 0, stream, a);
   }
