@@ -38,7 +38,7 @@ struct WeightArgs {
   unsigned* status;
   float* part;                  // [batch][n_kv mblocks][max_len]
   int64_t acc_stride;
-  Divide page;
+  Divide page, by_group;
   float decay;
   int chunk, splits;            // cache rows of a workgroup, workgroups along them
   int mblocks, group;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(kThreads) void weight_rows_kernel(WeightArgs a) {
         const int m = 16 * qt + c;
         if (16 * qt >= m_rows) break;
         const bool in = m < m_rows;
-        const int i = in ? m / a.group : 0, h = kh * a.group + (in ? m % a.group : 0);
+        const int i = in ? (int)quotient((unsigned)m, a.by_group) : 0, h = kh * a.group + (in ? m - i * a.group : 0);
         const uint16_t* p = a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * g;
         bf16x8 q[kSteps];
 #pragma unroll
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
 #pragma unroll
   for (int j = 0; j < kPieces; ++j) {
     const int x = tid + j * kHeadThreads, m = x / (HD / 8), ch = x % (HD / 8), mc = m < m_rows ? m : m_rows - 1;
-    const int i = (m0 + mc) / a.group, h = kh * a.group + (m0 + mc) % a.group;
+    const int i = (int)quotient((unsigned)(m0 + mc), a.by_group), h = kh * a.group + (m0 + mc - i * a.group);
     piece[j] = *reinterpret_cast<const u32x4*>(a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * ch);
   }
 #pragma unroll
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
   }
   for (int m = tid; m < kBlock; m += kHeadThreads) {
     const bool in = m < m_rows;
-    const int i = in ? (m0 + m) / a.group : 0, h = kh * a.group + (in ? (m0 + m) % a.group : 0);
+    const int i = in ? (int)quotient((unsigned)(m0 + m), a.by_group) : 0, h = kh * a.group + (in ? m0 + m - i * a.group : 0);
     sh_lse[m] = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] * kLog2e : -INFINITY;
     sh_word[m] = in ? draft_word(a.q, first + i, i) : 0ull;
   }
@@ -380,6 +380,7 @@ hipError_t launch_weight(const Batch& b, const uint16_t* kp, const Queries& q, c
   a.part = reinterpret_cast<float*>(w + p.part);
   a.acc_stride = acc_stride;
   a.page = divide_by((unsigned)b.page_size);
+  a.by_group = divide_by((unsigned)p.group);
   a.decay = decay;
   a.chunk = p.chunk;
   a.splits = p.splits;
