@@ -31,6 +31,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32;             // cache rows of one step of a wave
+// The running maximum follows a larger score only when that is more than 2^8 times as heavy: the
+// weights relative to it then stay below 2^8, which costs neither fp32 sums nor bf16 weights any
+// precision, and the outputs are rescaled a few times in all instead of in every other step.
+constexpr float kSlack = 8.f;
 
 struct AttendArgs {
   Batch b;
@@ -343,17 +347,17 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
       }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float m_new = fmaxf(m_run[t], top);
-      const float zero = m_new == -INFINITY ? 0.f : m_new;
-      if (__any(m_new > m_run[t])) {
-        const float shrink = __builtin_amdgcn_exp2f(m_run[t] - zero);
+      if (__any(top > m_run[t] + kSlack)) {
+        const float m_new = fmaxf(m_run[t], top);
+        const float shrink = __builtin_amdgcn_exp2f(m_run[t] - (m_new == -INFINITY ? 0.f : m_new));
         l_run[t] *= shrink;
         if constexpr (kOut) {
 #pragma unroll
           for (int f = 0; f < kFeat; ++f) o[t][f] *= shrink;
         }
+        m_run[t] = m_new;
       }
-      m_run[t] = m_new;
+      const float zero = m_run[t] == -INFINITY ? 0.f : m_run[t];
       float p[8], sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -693,17 +697,18 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, s[e][r]);
       top = fmaxf(top, other_half(top));
-      const float m_new = fmaxf(m_run, top * scale2);
-      const float zero = m_new == -INFINITY ? 0.f : m_new;
-      if (__any(m_new > m_run)) {
-        const float shrink = __builtin_amdgcn_exp2f(m_run - zero);
+      top *= scale2;
+      if (__any(top > m_run + kSlack)) {
+        const float m_new = fmaxf(m_run, top);
+        const float shrink = __builtin_amdgcn_exp2f(m_run - (m_new == -INFINITY ? 0.f : m_new));
         l_run *= shrink;
         if constexpr (kOut) {
 #pragma unroll
           for (int f = 0; f < kF; ++f) o[f] *= shrink;
         }
+        m_run = m_new;
       }
-      m_run = m_new;
+      const float zero = m_run == -INFINITY ? 0.f : m_run;
       // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, packed
       const auto pair = [&](int x, int i) -> uint32_t {
         const float p0 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i], scale2, -zero));
