@@ -51,7 +51,7 @@ struct AttendArgs {
   int parts, goal, least;       // parts of the grid; wanted of all sequences (0: one each), rows of one
   int mblocks;                  // blocks of query rows
   int group;                    // query heads of a key head
-  int scan;                     // 1: the workgroup past the grid looks all pages over for the status
+  int scan;                     // 1: the first workgroup looks all pages over for the status
 };
 
 __device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half) {
@@ -213,53 +213,41 @@ __device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, cons
   }
 }
 
-// MT tiles of 16 query rows.  kOut: with the product with V (else only the statistics).
-template <int HD, int MT, bool kOut>
-__global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(AttendArgs a) {
+// kOut: with the product with V (else only the statistics).
+// At most 16 query rows: bound by the read of K and V.  16 sequences of up to 16,384 rows, one token,
+// 8 key heads of 128 (805 MB): 145 us of the call's 155, 5.5 TB/s, as a large copy.
+template <int HD, bool kOut>
+__global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   constexpr int kSteps = HD / 32, kFeat = HD / 16;
-  __shared__ float sh_o[kWaves / 2][16 * MT][HD + 4];
-  __shared__ float2 sh_ml[kWaves / 2][16 * MT];
+  __shared__ float sh_o[kWaves / 2][16][HD + 4];
+  __shared__ float2 sh_ml[kWaves / 2][16];
   if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
-  int unit = blockIdx.x - a.scan, mb = 0;
-  place_block(a, &unit, &mb);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   Part pt;
-  if (!find_part(a, unit, &pt)) return;
+  if (!find_part(a, blockIdx.x - a.scan, &pt)) return;
   const int kh = pt.kh, seq = pt.seq, len = pt.len, first = pt.first, n = pt.n, begin = pt.begin, end = pt.end;
-  const int m_rows = n * a.group, m0 = mb * 16 * MT;
-  if (m0 >= m_rows) return;
-  const int ctx = len - n;
+  const int m_rows = n * a.group, ctx = len - n;
 
-  // Q^T fragments: query row m0 + 16 t + c of the block, zero past the last
-  bf16x8 qf[MT][kSteps];
-  uint64_t words[MT];
-  int qi[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + 16 * t + c;
-    const bool in = m < m_rows;
-    const int i = in ? m / a.group : 0, h = in ? kh * a.group + m % a.group : 0;
-    const uint16_t* p = a.q.q + (int64_t)(first + i) * a.q.q_stride + h * HD + 8 * g;
-    qi[t] = i;
-    words[t] = draft_word(a.q, first + i, i);
+  // Q^T fragments: query row c, zero past the last
+  const bool in = c < m_rows;
+  const int qi = in ? c / a.group : 0, head = kh * a.group + (in ? c % a.group : 0);
+  const uint64_t word = draft_word(a.q, first + qi, qi);
+  bf16x8 qf[kSteps];
+  {
+    const uint16_t* p = a.q.q + (int64_t)(first + qi) * a.q.q_stride + head * HD + 8 * g;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       u32x4 w = {0u, 0u, 0u, 0u};
       if (in) w = *reinterpret_cast<const u32x4*>(p + 32 * s);
-      qf[t][s] = __builtin_bit_cast(bf16x8, w);
+      qf[s] = __builtin_bit_cast(bf16x8, w);
     }
   }
 
-  f32x4 o[MT][kOut ? kFeat : 1];
-  float m_run[MT], l_run[MT];
+  f32x4 o[kOut ? kFeat : 1];
+  float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    m_run[t] = -INFINITY;
-    l_run[t] = 0.f;
-#pragma unroll
-    for (int f = 0; f < (kOut ? kFeat : 1); ++f) o[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int f = 0; f < (kOut ? kFeat : 1); ++f) o[f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
   const uint16_t* kbase = a.kp + kh * HD;
@@ -326,73 +314,70 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
       }
     }
 
+    f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st)
+      for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, cur.k[h][st]), qf[st], s[h]);
+    uint32_t seen = 0xffffffffu;                    // rows that this lane's query sees
+    if (masked) {
+      seen = there;
+      if (base + kRows > ctx) seen &= seen_rows(word, base - ctx);
+    }
+    float x[8], top = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, cur.k[h][st]), qf[t][st], s[h]);
-      uint32_t seen = 0xffffffffu;                    // rows that this lane's query sees
-      if (masked) {
-        seen = there;
-        if (base + kRows > ctx) seen &= seen_rows(words[t], base - ctx);
-      }
-      float x[8], top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = s[j / 4][j % 4] * scale2;
-        if (masked && !(seen >> (16 * (j / 4) + 4 * g + j % 4) & 1)) x[j] = -INFINITY;
-        top = fmaxf(top, x[j]);
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > m_run[t] + kSlack)) {
-        const float m_new = fmaxf(m_run[t], top);
-        const float shrink = __builtin_amdgcn_exp2f(m_run[t] - (m_new == -INFINITY ? 0.f : m_new));
-        l_run[t] *= shrink;
-        if constexpr (kOut) {
-#pragma unroll
-          for (int f = 0; f < kFeat; ++f) o[t][f] *= shrink;
-        }
-        m_run[t] = m_new;
-      }
-      const float zero = m_run[t] == -INFINITY ? 0.f : m_run[t];
-      float p[8], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(x[j] - zero);
-        sum += p[j];
-      }
-      l_run[t] += sum;
+    for (int j = 0; j < 8; ++j) {
+      x[j] = s[j / 4][j % 4] * scale2;
+      if (masked && !(seen >> (16 * (j / 4) + 4 * g + j % 4) & 1)) x[j] = -INFINITY;
+      top = fmaxf(top, x[j]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > m_run + kSlack)) {
+      const float m_new = fmaxf(m_run, top);
+      const float shrink = __builtin_amdgcn_exp2f(m_run - (m_new == -INFINITY ? 0.f : m_new));
+      l_run *= shrink;
       if constexpr (kOut) {
-        u32x4 pw;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pw[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
-        if (!wild) {
-          const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
+        for (int f = 0; f < kFeat; ++f) o[f] *= shrink;
+      }
+      m_run = m_new;
+    }
+    const float zero = m_run == -INFINITY ? 0.f : m_run;
+    float p[8], sum = 0.f;
 #pragma unroll
-          for (int f = 0; f < kFeat; ++f) o[t][f] = mfma16(vf[f], pf, o[t][f]);
-        } else {
-          // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
-          // for the queries that see the row.
-          for (int r = 0; r < kRows; ++r) {
-            const int rg = r % 16 / 4, j = r / 16 * 4 + r % 4;
-            const bool vis = __shfl(seen, 16 * rg + c) >> r & 1;
-            const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
-            u32x4 pr;
+    for (int j = 0; j < 8; ++j) {
+      p[j] = __builtin_amdgcn_exp2f(x[j] - zero);
+      sum += p[j];
+    }
+    l_run += sum;
+    if constexpr (kOut) {
+      u32x4 pw;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pr[i] = g == rg && i == j / 2 ? pw[i] & keep : 0u;
+      for (int i = 0; i < 4; ++i) pw[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+      if (!wild) {
+        const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
 #pragma unroll
-            for (int f = 0; f < kFeat; ++f) {
-              const u32x4 vw = __builtin_bit_cast(u32x4, vf[f]);
-              u32x4 vr;
+        for (int f = 0; f < kFeat; ++f) o[f] = mfma16(vf[f], pf, o[f]);
+      } else {
+        // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
+        // for the queries that see the row.
+        for (int r = 0; r < kRows; ++r) {
+          const int rg = r % 16 / 4, j = r / 16 * 4 + r % 4;
+          const bool vis = __shfl(seen, 16 * rg + c) >> r & 1;
+          const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
+          u32x4 pr;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) vr[i] = g == rg && i == j / 2 ? vw[i] & keep : 0u;
-              const f32x4 add = mfma16(__builtin_bit_cast(bf16x8, vr), __builtin_bit_cast(bf16x8, pr),
-                                       f32x4{0.f, 0.f, 0.f, 0.f});
-              if (vis) o[t][f] += add;
-            }
+          for (int i = 0; i < 4; ++i) pr[i] = g == rg && i == j / 2 ? pw[i] & keep : 0u;
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f) {
+            const u32x4 vw = __builtin_bit_cast(u32x4, vf[f]);
+            u32x4 vr;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[i] = g == rg && i == j / 2 ? vw[i] & keep : 0u;
+            const f32x4 add = mfma16(__builtin_bit_cast(bf16x8, vr), __builtin_bit_cast(bf16x8, pr),
+                                     f32x4{0.f, 0.f, 0.f, 0.f});
+            if (vis) o[f] += add;
           }
         }
       }
@@ -403,87 +388,70 @@ __global__ __launch_bounds__(kThreads, MT > 1 ? 1 : 2) void attend_kernel(Attend
   if (page_err && !a.scan && lane == 0) atomicOr(a.status, kStatusRowsBit);
 
   // sums over g, then the waves: 2 and 3 into 0 and 1, then 1 into 0
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    l_run[t] += __shfl_xor(l_run[t], 16);
-    l_run[t] += __shfl_xor(l_run[t], 32);
-  }
+  l_run += __shfl_xor(l_run, 16);
+  l_run += __shfl_xor(l_run, 32);
   for (int half = kWaves / 2; half; half /= 2) {
     if (wave >= half && wave < 2 * half) {
       const int w = wave - half;
+      if (g == 0) sh_ml[w][c] = make_float2(m_run, l_run);
+      if constexpr (kOut) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if (g == 0) sh_ml[w][16 * t + c] = make_float2(m_run[t], l_run[t]);
-        if constexpr (kOut) {
+        for (int f = 0; f < kFeat; ++f)
 #pragma unroll
-          for (int f = 0; f < kFeat; ++f)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sh_o[w][16 * t + c][kFeat * (4 * g + r) + f] = o[t][f][r];
-        }
+          for (int r = 0; r < 4; ++r) sh_o[w][c][kFeat * (4 * g + r) + f] = o[f][r];
       }
     }
     __syncthreads();
     if (wave < half) {
+      const float2 ml = sh_ml[wave][c];
+      const float m_new = fmaxf(m_run, ml.x), zero = m_new == -INFINITY ? 0.f : m_new;
+      const float mine = __builtin_amdgcn_exp2f(m_run - zero), theirs = __builtin_amdgcn_exp2f(ml.x - zero);
+      m_run = m_new;
+      l_run = l_run * mine + ml.y * theirs;
+      if constexpr (kOut) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const float2 ml = sh_ml[wave][16 * t + c];
-        const float m_new = fmaxf(m_run[t], ml.x), zero = m_new == -INFINITY ? 0.f : m_new;
-        const float mine = __builtin_amdgcn_exp2f(m_run[t] - zero), theirs = __builtin_amdgcn_exp2f(ml.x - zero);
-        m_run[t] = m_new;
-        l_run[t] = l_run[t] * mine + ml.y * theirs;
-        if constexpr (kOut) {
+        for (int f = 0; f < kFeat; ++f)
 #pragma unroll
-          for (int f = 0; f < kFeat; ++f)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              o[t][f][r] = o[t][f][r] * mine + sh_o[wave][16 * t + c][kFeat * (4 * g + r) + f] * theirs;
-        }
+          for (int r = 0; r < 4; ++r) o[f][r] = o[f][r] * mine + sh_o[wave][c][kFeat * (4 * g + r) + f] * theirs;
       }
     }
     __syncthreads();
   }
-  if (wave != 0) return;
-  const int64_t part = ((int64_t)pt.id * a.b.n_kv + kh) * (a.q.max_q * a.group);
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + 16 * t + c;
-    if (m >= m_rows) continue;
-    if (!pt.whole) {
-      if (g == 0) a.part_ml[part + m] = make_float2(m_run[t], l_run[t]);
-      if constexpr (kOut) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float* p = a.part_o + (part + m) * HD + kFeat * (4 * g + r);
-#pragma unroll
-          for (int f = 0; f < kFeat; f += 4)
-            *reinterpret_cast<f32x4*>(p + f) = f32x4{o[t][f][r], o[t][f + 1][r], o[t][f + 2][r], o[t][f + 3][r]};
-        }
-      }
-      continue;
-    }
-    const int h = kh * a.group + m % a.group;
-    const int64_t row = first + m / a.group;
-    const bool none = l_run[t] == 0.f;
-    if (a.lse && g == 0)
-      a.lse[row * a.q.n_heads + h] = none ? -INFINITY : m_run[t] * kLn2 + __logf(l_run[t]);
+  if (wave != 0 || !in) return;
+  if (!pt.whole) {
+    const int64_t part = ((int64_t)pt.id * a.b.n_kv + kh) * (a.q.max_q * a.group) + c;
+    if (g == 0) a.part_ml[part] = make_float2(m_run, l_run);
     if constexpr (kOut) {
-      const float inv = none ? 0.f : 1.f / l_run[t];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        uint16_t* p = a.out + row * a.out_stride + h * HD + kFeat * (4 * g + r);
+        float* p = a.part_o + part * HD + kFeat * (4 * g + r);
 #pragma unroll
-        for (int f = 0; f < kFeat; f += 4) {
-          u32x2 w;
-          w[0] = pack_bf16x2(o[t][f][r] * inv, o[t][f + 1][r] * inv);
-          w[1] = pack_bf16x2(o[t][f + 2][r] * inv, o[t][f + 3][r] * inv);
-          *reinterpret_cast<u32x2*>(p + f) = none ? u32x2{0u, 0u} : w;
-        }
+        for (int f = 0; f < kFeat; f += 4)
+          *reinterpret_cast<f32x4*>(p + f) = f32x4{o[f][r], o[f + 1][r], o[f + 2][r], o[f + 3][r]};
+      }
+    }
+    return;
+  }
+  const int64_t row = first + qi;
+  const bool none = l_run == 0.f;
+  if (a.lse && g == 0) a.lse[row * a.q.n_heads + head] = none ? -INFINITY : m_run * kLn2 + __logf(l_run);
+  if constexpr (kOut) {
+    const float inv = none ? 0.f : 1.f / l_run;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint16_t* p = a.out + row * a.out_stride + head * HD + kFeat * (4 * g + r);
+#pragma unroll
+      for (int f = 0; f < kFeat; f += 4) {
+        u32x2 w;
+        w[0] = pack_bf16x2(o[f][r] * inv, o[f + 1][r] * inv);
+        w[1] = pack_bf16x2(o[f + 2][r] * inv, o[f + 3][r] * inv);
+        *reinterpret_cast<u32x2*>(p + f) = none ? u32x2{0u, 0u} : w;
       }
     }
   }
 }
 
-// More than 64 query rows: bound by the matrix cores and the exponentials, so K and V go
+// More than 16 query rows: bound by the matrix cores and the exponentials, so K and V go
 // through LDS and are shared by the workgroup's eight waves, each of which keeps 32 query rows
 // (32x32x16 MFMAs, the same transposed products: lane (q, h) = (lane % 32, lane / 32) of S^T
 // holds cache rows 8 (r / 4) + 4 h + r % 4, r < 16).  WM of the waves lie along the query rows, with
@@ -874,14 +842,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   }
 }
 
-// Joins the splits of one output row per wave: sixteen lanes hold the row, four parts at a time
-// (and several of those in flight: one at a time, 128 parts took 80 us).
-template <int HD>
+// Joins the parts of one output row by kPer waves: sixteen lanes hold the row, four parts to a
+// wave at a time (and several of those in flight: one at a time, 128 parts took 80 us).
+template <int HD, int kPer>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
   constexpr int kE = HD / 16;
+  __shared__ float sh_o[kPer][HD + 1];
   const int rows = a.q.max_q * a.group;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int wave = threadIdx.x >> 6, g0 = 4 * (wave % kPer) + g;
+  const int64_t id = (int64_t)blockIdx.x * (kWaves / kPer) + wave / kPer;
   const int sh = (int)(id / rows), m = (int)(id % rows);
   if (sh >= a.b.batch * a.b.n_kv) return;
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
@@ -908,7 +878,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
   if (a.out) {
     const float* po = a.part_o + at * HD + c * kE;
 #pragma unroll 4
-    for (int s = g; s < parts; s += 4) {
+    for (int s = g0; s < parts; s += 4 * kPer) {
       const float2 v = ml[s * step];
       const float w = __builtin_amdgcn_exp2f(v.x - zero);
       sum += v.y * w;
@@ -925,13 +895,31 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
       o[e] += __shfl_xor(o[e], 32);
     }
   } else {
-    for (int s = g; s < parts; s += 4) {
+    for (int s = g0; s < parts; s += 4 * kPer) {
       const float2 v = ml[s * step];
       sum += v.y * __builtin_amdgcn_exp2f(v.x - zero);
     }
   }
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
+  if constexpr (kPer > 1) {                         // one row to a workgroup: all its waves are here
+    static_assert(kPer == kWaves, "a row is one workgroup's");
+    if (a.out && g == 0) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) sh_o[wave][c * kE + e] = o[e];
+    }
+    if (lane == 0) sh_o[wave][HD] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < kPer; ++w) {
+      sum += sh_o[w][HD];
+      if (a.out) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] += sh_o[w][c * kE + e];
+      }
+    }
+  }
   const int h = kh * a.group + m % a.group;
   const int64_t row = first + m / a.group;
   const bool none = sum == 0.f;
@@ -976,7 +964,7 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
 template <int HD, bool kOut>
 void launch_rows(const AttendArgs& a, int rows, unsigned grid, hipStream_t stream) {
   if (rows == 16)
-    hipLaunchKernelGGL((attend_kernel<HD, 1, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_kernel<HD, kOut>), dim3(grid), dim3(kThreads), 0, stream, a);
   else if (rows == 128)
     hipLaunchKernelGGL((attend_tile_kernel<HD, 4, kOut>), dim3(grid), dim3(512), 0, stream, a);
   else
@@ -991,8 +979,11 @@ void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStr
     launch_rows<HD, false>(a, p.rows, grid, stream);
   if (p.goal) {
     const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
-    hipLaunchKernelGGL((join_kernel<HD>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                       stream, a);
+    if (p.goal > 32)                // a sequence can have more parts than a wave has under way
+      hipLaunchKernelGGL((join_kernel<HD, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, stream, a);
+    else
+      hipLaunchKernelGGL((join_kernel<HD, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads),
+                         0, stream, a);
   }
 }
 
