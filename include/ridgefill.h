@@ -20,9 +20,10 @@
  *    even where the library produces them).  All matrices are row-major.
  *  - `stream` is a hipStream_t (NULL = the null stream).  Device work is enqueued
  *    on it and the call returns without waiting, except where stated.  ridgefill_fill
- *    with resident maps (plain or folded) enqueues kernels only (the status word is
- *    cleared by a kernel, not a memset), so it can be captured into a HIP graph and
- *    replayed; the workspace, index list and pools must then stay at their addresses.
+ *    with resident maps (plain or folded) and the cache calls (ridgefill_rope to
+ *    ridgefill_evict_rows) enqueue kernels only (the status word is cleared by a kernel,
+ *    not a memset), so they can be captured into a HIP graph and replayed; workspaces,
+ *    index lists and pools must then stay at their addresses.
  *  - Errors found on the host (null pointers, shapes, sizes, workspace too small,
  *    invalid parameters) return a non-zero rf_status before anything is enqueued;
  *    ridgefill_last_error() then gives a description.  A failed launch returns
@@ -460,7 +461,7 @@ typedef struct rf_paged_batch {
                                    (not read by ridgefill_append_rows, which takes NULL)    */
   int64_t table_stride;         /* >= ceil(max_len / page_size)                             */
   int32_t batch;                /* 1 .. 65535                                               */
-  int32_t max_len;              /* >= 1                                                     */
+  int32_t max_len;              /* 1 .. 2^30; batch * max_len <= 2^36                       */
   int32_t page_size, num_pages; /* >= 1; num_pages * page_size < 2^31                       */
   int32_t n_kv_heads;           /* 1 .. 256                                                 */
   int32_t head_dim;             /* 64 or 128; for ridgefill_append_rows a multiple of 16 up to 256 */
@@ -523,7 +524,8 @@ rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int
  * NULL) and written with v to cache row rows[i] of sequence seq[i]; q, if given, is rotated
  * into q_out.  Everything in one pass over the rows.
  *   q           device bf16 [n_rows][n_q_heads][head_dim] or NULL (then n_q_heads = 0)
- *   q_out       device bf16, the same shape; q_out = q rotates in place
+ *   q_out       device bf16, the same shape; q_out = q rotates in place (other overlaps of
+ *               the rows with one another or with the pages are not allowed)
  *   k, v        device bf16 [n_rows][n_kv_heads][head_dim]; the strides (elements between
  *               rows) are multiples of 8, all pointers 16-byte aligned
  *   seq         device int32 [n_rows] or NULL (all rows belong to sequence 0); a negative
@@ -560,13 +562,16 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
  *   max_q       1 .. 64: the host's bound on one sequence's queries
  *   tree_mask   device uint64 [n_q] or NULL
  *   out         device bf16 [n_q][n_q_heads][head_dim], rows out_stride elements apart
- *               (multiple of 8), 16-byte aligned; or NULL (only lse; v_pages may then be NULL)
+ *               (multiple of 8), 16-byte aligned, not overlapping q; or NULL (only lse; v_pages
+ *               may then be NULL)
  *   lse         device fp32 [n_q][n_q_heads] or NULL (one of out, lse is needed)
  *   ws          >= ridgefill_tree_attention_workspace_bytes(kv, n_q_heads, max_q), 256-byte
  *               aligned; its first 256 bytes hold the status
  * Scores, maxima, sums and outputs are held in fp32; exp(s - max) is rounded to bf16 as the
- * matrix cores' operand of the product with v, and out once at the end.
- * Neither call reads kv->lengths on the host.  Size query: 0 on invalid input.
+ * matrix cores' operand of the product with v, and out once at the end.  The same call on the
+ * same inputs gives the same bits; a row's bits may differ between calls whose sequences have
+ * other lengths, since long caches are split evenly over the batch.  Size query: 0 on invalid
+ * input.
  * ------------------------------------------------------------------------------ */
 size_t ridgefill_tree_attention_workspace_bytes(const rf_paged_batch* kv, int32_t n_q_heads,
                                                 int32_t max_q);
@@ -631,11 +636,11 @@ rf_status ridgefill_evict_rows(const rf_paged_batch* kv, const rf_layer* layers,
                                size_t ws_bytes, void* stream);
 
 /* Waits for `stream`, then returns the device status word of a fill, solve or selection
- * workspace (or of the cache calls' workspaces): RF_OK, RF_E_ROWS, RF_E_NOT_SPD, RF_E_WORKSPACE for a solve on a calibration
- * state whose header disagrees with the solve's sizes or that a calibrate call marked bad,
- * or RF_E_INVALID for a NaN score.  Each call
- * clears that word on the stream before its own kernels run, so the word reflects the
- * last call only. */
+ * workspace, or of a cache call's workspace or status word: RF_OK, RF_E_ROWS, RF_E_NOT_SPD,
+ * RF_E_WORKSPACE for a solve on a calibration state whose header disagrees with the solve's
+ * sizes or that a calibrate call marked bad, or RF_E_INVALID for a NaN score or weight.  Each
+ * call clears that word on the stream before its own kernels run (the cache calls write it
+ * whole), so the word reflects the last call only. */
 rf_status ridgefill_read_status(void* ws, void* stream);
 
 /* Waits for `stream`, then reports the conditioning of the last solve on this solve

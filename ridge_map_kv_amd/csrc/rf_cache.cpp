@@ -69,6 +69,8 @@ rf_status check_batch(const rf_paged_batch* kv, bool append, rf::Batch& b) {
   if (kv->batch < 1 || kv->batch > 65535) return fail(RF_E_SHAPE, "batch = %d must be in 1..65535", kv->batch);
   if (kv->max_len < 1 || kv->page_size < 1 || kv->num_pages < 1)
     return fail(RF_E_SHAPE, "max_len, page_size and num_pages must be >= 1");
+  if (kv->max_len > (1 << 30) || (int64_t)kv->batch * kv->max_len > (int64_t)1 << 36)
+    return fail(RF_E_SHAPE, "max_len = %d must be at most 2^30, batch * max_len at most 2^36", kv->max_len);
   if (kv->table_stride < ((int64_t)kv->max_len + kv->page_size - 1) / kv->page_size)
     return fail(RF_E_SHAPE, "table_stride = %lld holds fewer than max_len = %d rows",
                 (long long)kv->table_stride, kv->max_len);

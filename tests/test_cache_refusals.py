@@ -22,7 +22,8 @@ def _kv(**kw):
 
 
 BAD_KV = [dict(batch=0), dict(batch=65536), dict(max_len=0), dict(page_size=0), dict(num_pages=0),
-          dict(table_stride=6), dict(num_pages=1 << 28), dict(n_kv_heads=0), dict(n_kv_heads=257)]
+          dict(table_stride=6), dict(num_pages=1 << 28), dict(max_len=(1 << 30) + 1, table_stride=1 << 28),
+          dict(batch=60000, max_len=1 << 22, table_stride=1 << 20), dict(n_kv_heads=0), dict(n_kv_heads=257)]
 
 
 def _refused(status, want):

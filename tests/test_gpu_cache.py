@@ -682,6 +682,107 @@ def test_captured_step_replays_with_new_lengths():
     del graph
 
 
+def test_captured_eviction_of_a_long_cache():
+    # more keys than a launch's LDS unasked
+    n = 20000
+    cache = R.Cache([n], 1, 16, 100, seed=7)
+    acc0 = torch.rand(1, n, generator=torch.Generator().manual_seed(0))
+    pos0 = torch.randperm(n, generator=torch.Generator().manual_seed(1))[None].to(torch.int32)
+    acc, pos, kv = acc0.to(DEV), pos0.to(DEV), cache.batch(B)
+    pools, layers = (cache.k[0].clone(), cache.v[0].clone()), B.make_pools(cache.k, cache.v)
+    ws = torch.empty(B.ridgefill_evict_workspace_bytes(kv, 9000), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        B.ridgefill_evict_rows(kv, layers, acc, pos, 9000, acc, pos, cache.lengths, ws, n_sink=3, n_recent=10)
+    moves, holds = R.evict([n], acc0.numpy(), pos0.numpy(), 9000, 3, 10)
+    want = R.Cache.rows(cache, pools[0], 0)[holds[0]]
+    for _ in range(2):
+        acc.copy_(acc0)
+        pos.copy_(pos0)
+        cache.lengths.fill_(n)
+        cache.k[0].copy_(pools[0])
+        cache.v[0].copy_(pools[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert B.ridgefill_read_status(ws) == B.RF_OK and int(cache.lengths) == 9000
+        assert pos[0, :9000].tolist() == pos0[0, holds[0]].tolist()
+        assert torch.equal(cache.rows(cache.k[0], 0, 9000), want)
+    del graph
+
+
+@pytest.mark.parametrize("n", [32768, 33000, 70001])
+def test_evict_long(n):
+    # as many rows as LDS holds, and more: the order is kept in pieces
+    g = torch.Generator().manual_seed(n)
+    acc = torch.randint(0, 300, (1, n), generator=g).float()
+    pos = torch.arange(n, dtype=torch.int32)[None].contiguous()
+    _check_evict(R.Cache([n], 1, 16, 64, seed=1), acc, pos, n // 3, 4, 64)
+
+
+def test_nothing_to_do():
+    cache = R.Cache([40, 9], 2, 64, 16, seed=1)
+    kv = cache.batch(B)
+    q, lse = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV), torch.empty(0, 4, device=DEV)
+    start, acc = torch.zeros(3, dtype=torch.int32, device=DEV), torch.full((2, 40), 2.0, device=DEV)
+    ws = torch.empty(B.ridgefill_tree_attention_workspace_bytes(kv, 4, 8), dtype=torch.uint8, device=DEV)
+    B.ridgefill_tree_attention(kv, cache.k[0], cache.v[0], q, start, 8, 0.1, torch.empty_like(q), ws, lse=lse)
+    assert B.ridgefill_read_status(ws) == B.RF_OK
+    ws = torch.empty(B.ridgefill_attention_weight_workspace_bytes(kv, 4, 8), dtype=torch.uint8, device=DEV)
+    B.ridgefill_attention_weight(kv, cache.k[0], q, start, 8, 0.1, lse, acc, ws, acc=acc, decay=0.5)
+    assert B.ridgefill_read_status(ws) == B.RF_OK and (acc == 2).all()
+    status = torch.full((1,), -1, dtype=torch.int32, device=DEV)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    B.ridgefill_append_rows(B.make_rope(), kv, none, none, torch.empty(0, dtype=torch.int32, device=DEV), cache.k[0],
+                            cache.v[0], status)
+    assert B.ridgefill_read_status(status) == B.RF_OK
+
+
+def test_many_sequences_of_all_lengths():
+    # more sequences than lanes, split unevenly, some without queries
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 700, 150)]
+    counts = [min(n, (3 * b) % 4) for b, n in enumerate(lens)]
+    cache, q, starts, words, _ = _case(lens, counts, 2, 1, 64, 16, seed=15, tree=True, max_q=5)
+    for max_q in (5, 12):                                 # both kernels
+        out, lse, st = _attend(cache, q, starts, words, max_q, 0.1, n_pad=1)
+        assert st == B.RF_OK
+        want, wl, ot, lt = R.attention(cache, q, starts, words, 0.1)
+        n = q.shape[0]
+        _close(out[:n], want, ot, "out")
+        _close(lse[:n], wl, lt, "lse")
+        kv = cache.batch(B)
+        ws = torch.empty(B.ridgefill_attention_weight_workspace_bytes(kv, 2, max_q), dtype=torch.uint8, device=DEV)
+        acc = torch.full((150, cache.max_len), -7.0, device=DEV)
+        B.ridgefill_attention_weight(kv, cache.k[0], q, torch.tensor(starts, dtype=torch.int32, device=DEV), max_q, 0.1,
+                                     lse[:n].contiguous(), acc, ws, tree_mask=_mask(words))
+        assert B.ridgefill_read_status(ws) == B.RF_OK
+        want, tol = R.weight(cache, q, starts, words, 0.1, lse[:n], 1.0, None, torch.full_like(acc, -7.0))
+        _close(acc, want, tol, "weight")
+
+
+def test_two_calls_on_two_streams():
+    a, b = (_case([2000, 300], [4, 9], 8, 2, 128, 16, seed=s, tree=True) for s in (21, 22))
+    want = [_attend(*c[:4], c[4], 0.1)[0] for c in (a, b)]
+    got, keep = [], []
+    torch.cuda.synchronize()
+    for c in (a, b):
+        s = torch.cuda.Stream()
+        kv = c[0].batch(B)
+        ws = torch.empty(B.ridgefill_tree_attention_workspace_bytes(kv, 8, c[4]), dtype=torch.uint8, device=DEV)
+        start, mask, out = torch.tensor(c[2], dtype=torch.int32, device=DEV), _mask(c[3]), torch.empty_like(c[1])
+        torch.cuda.synchronize()
+        keep.append((s, kv, ws, start, mask))
+        got.append(out)
+    for _ in range(5):
+        for c, out, (s, kv, ws, start, mask) in zip((a, b), got, keep):
+            B.ridgefill_tree_attention(kv, c[0].k[0], c[0].v[0], c[1], start, c[4], 0.1, out, ws, tree_mask=mask, stream=s)
+    torch.cuda.synchronize()
+    for out, w in zip(got, want):
+        assert torch.equal(out, w)
+
+
 def test_another_stream():
     cache, q, starts, words, max_q = _case([3000], [5], 8, 2, 128, 16, seed=6, tree=True)
     ref, ref_lse, _ = _attend(cache, q, starts, words, max_q, 0.1)
