@@ -514,7 +514,7 @@ typedef struct rf_rope {
  *   x, out      device, of x_type (RF_TYPE_BF16 or RF_TYPE_F32), 16-byte aligned; strides
  *               >= n_heads * head_dim and multiples of 8 (bf16) or 4 (fp32) elements
  *   positions   device int32 [n_rows]; any value, negative ones too
- * head_dim: a multiple of 16 up to 256. */
+ * head_dim: a multiple of 16 up to 256; n_rows: 0 .. 2^23. */
 rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int64_t n_rows,
                          int32_t n_heads, int32_t head_dim, int64_t x_stride,
                          const int32_t* positions, void* out, int64_t out_stride,
@@ -535,7 +535,7 @@ rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int
  *   status      device uint32 (4-byte aligned): receives the device status word of the
  *               call.  A sequence, row or page out of range sets RF_E_ROWS there and that
  *               row's k and v are not written (its q is rotated all the same).
- * The (seq, rows) pairs of one call must differ from one another. */
+ * The (seq, rows) pairs of one call must differ from one another.  n_rows: 0 .. 2^23. */
 rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, const uint16_t* q,
                                 int32_t n_q_heads, int64_t q_stride, uint16_t* q_out,
                                 int64_t q_out_stride, const uint16_t* k, int64_t k_stride,
@@ -559,7 +559,8 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
  *   q_start     device int32 [batch + 1], ascending; sequences may have no queries.  One
  *               with more than max_q queries, more queries than rows, or outside [0, n_q)
  *               sets RF_E_ROWS and is skipped.  Queries of no sequence are left as they were.
- *   max_q       1 .. 64: the host's bound on one sequence's queries
+ *   max_q       1 .. 64: the host's bound on one sequence's queries;
+ *               batch * n_q_heads * max_q <= 2^26
  *   tree_mask   device uint64 [n_q] or NULL
  *   out         device bf16 [n_q][n_q_heads][head_dim], rows out_stride elements apart
  *               (multiple of 8), 16-byte aligned, not overlapping q; or NULL (only lse; v_pages
@@ -592,7 +593,7 @@ rf_status ridgefill_tree_attention(const rf_paged_batch* kv, const uint16_t* k_p
  *   acc         device fp32 [batch][acc_stride] or NULL (nothing accumulated so far)
  *   acc_out     device fp32 [batch][acc_stride]; acc_out = acc accumulates in place.  Entries
  *               from lengths[b] on, and sequences without queries, are left as they were.
- *   acc_stride  >= max_len
+ *   acc_stride  >= max_len; batch * max_len <= 2^29
  *   ws          >= ridgefill_attention_weight_workspace_bytes(kv, n_q_heads, max_q)
  * Sums are held in fp32 and added in a fixed order: results do not vary between runs.
  * ------------------------------------------------------------------------------ */

@@ -100,7 +100,8 @@ __device__ int grains_of_part(const AttendArgs& a, const Seq& mine, bool* bad) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
   *bad = __any(some);
-  int each = (int)((total + a.goal - 1) / a.goal);
+  constexpr int64_t kMost = (1 << 30) / kGrain;         // of the longest sequence
+  int each = (int)min((total + a.goal - 1) / a.goal, (long long)kMost);
   if (each < a.least / kGrain) each = a.least / kGrain;
   for (int tries = 0; tries < 4; ++tries) {
     int parts = (mine.grains + each - 1) / each;
@@ -108,7 +109,7 @@ __device__ int grains_of_part(const AttendArgs& a, const Seq& mine, bool* bad) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) parts += __shfl_xor(parts, d);
     if (parts <= a.goal) break;
-    each += (each * (parts - a.goal) + a.goal - 1) / a.goal;
+    each = (int)min(each + ((int64_t)each * (parts - a.goal) + a.goal - 1) / a.goal, kMost);
   }
   return each;
 }
@@ -154,8 +155,8 @@ __device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
       p->len = of(s.len);
       p->first = of(s.first);
       p->n = of(s.n);
-      p->begin = __builtin_amdgcn_readfirstlane(split * each * kGrain);
-      p->end = p->len < p->begin + each * kGrain ? p->len : p->begin + each * kGrain;
+      p->begin = __builtin_amdgcn_readfirstlane((int)((int64_t)split * each * kGrain));
+      p->end = p->len - p->begin < each * kGrain ? p->len : p->begin + each * kGrain;
       p->whole = parts == 1;
       return true;
     }
@@ -457,11 +458,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // holds cache rows 8 (r / 4) + 4 h + r % 4, r < 16).  WM of the waves lie along the query rows, with
 // WM = 4 the other four take the second half of a step's cache rows and are added at the end.
 // The rows of a step (64) are copied into LDS as they are, by direct loads that hold no
-// registers, two steps ahead of the products: four buffers, one barrier a step.  K^T's fragments are 16-byte reads, V^T's are transposing reads (four rows of one
-// feature a lane).  The 16-byte pieces of a row lie in the order piece ^ (row % 8) for K, piece ^
-// 4 (row % 2) for V, which spreads both kinds of read over all banks.  The pool slots of the
-// workgroup's rows are looked up beforehand: a table load between the direct loads would wait
-// for those.
+// registers, two steps ahead of the products: four buffers, one barrier a step.  K^T's fragments
+// are 16-byte reads, V^T's are transposing reads (four rows of one feature a lane).  The 16-byte
+// pieces of a row lie in the order piece ^ (row % 8) for K, piece ^ 4 (row % 2) for V, which
+// spreads both kinds of read over all banks.  The pool slots of the workgroup's rows are looked
+// up beforehand: a table load between the direct loads would wait for those.
 constexpr int kTileRows = 64;
 constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;

@@ -1,6 +1,6 @@
 // C entry points of the cache calls (rotary positions, append, attention, attention weight,
 // eviction): argument checks and the host side of the rotation's frequencies.  Device work is
-// in rf_rope.hip, rf_attend.hip and rf_evict.hip.
+// in rf_rope.hip, rf_attend.hip, rf_weight.hip and rf_evict.hip.
 #include "rf_cache.h"
 
 #include <cmath>
@@ -14,6 +14,11 @@ using rf::hip_fail;
 using rf::ok;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Bounds that keep every grid below 2^32 threads.
+constexpr int64_t kMaxRows = 1 << 23;         // of a rotation or an append: up to a workgroup of 256 each
+constexpr int64_t kMaxQueries = 1 << 26;      // batch * query heads * max_q
+constexpr int64_t kMaxWeights = 1 << 29;      // batch * max_len of the attention weight
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
@@ -103,6 +108,14 @@ rf_status check_heads(const rf::Batch& b, int n_q_heads, int max_q) {
     return fail(RF_E_SHAPE, "n_q_heads = %d must be a multiple of n_kv_heads = %d, at most 4096",
                 n_q_heads, b.n_kv);
   if (max_q < 1 || max_q > 64) return fail(RF_E_SHAPE, "max_q = %d must be in 1..64", max_q);
+  if ((int64_t)b.batch * n_q_heads * max_q > kMaxQueries)
+    return fail(RF_E_SHAPE, "batch * n_q_heads * max_q must be at most 2^26");
+  return RF_OK;
+}
+
+rf_status check_weights(const rf::Batch& b) {
+  if ((int64_t)b.batch * b.max_len > kMaxWeights)
+    return fail(RF_E_SHAPE, "batch * max_len must be at most 2^29 for the attention weight");
   return RF_OK;
 }
 
@@ -134,7 +147,8 @@ rf_status ridgefill_rope(const rf_rope* rope, const void* x, int32_t x_type, int
   if (head_dim < 16 || head_dim > 256 || head_dim % 16)
     return fail(RF_E_SHAPE, "head_dim = %d must be a multiple of 16 up to 256", head_dim);
   if (n_heads < 1 || n_heads > 4096) return fail(RF_E_SHAPE, "n_heads = %d must be in 1..4096", n_heads);
-  if (n_rows < 0 || n_rows > INT32_MAX) return fail(RF_E_SHAPE, "n_rows out of range");
+  if (n_rows < 0 || n_rows > kMaxRows)
+    return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23", (long long)n_rows);
   if (transpose != 0 && transpose != 1) return fail(RF_E_INVALID, "transpose must be 0 or 1");
   rf::RopeFreq f;
   rf_status s = make_freq(rope, head_dim, f);
@@ -167,7 +181,8 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
   if (s != RF_OK) return s;
   if (!status || !aligned(status, 4))
     return fail(RF_E_INVALID, "status must be a 4-byte aligned device pointer");
-  if (n_rows < 0 || n_rows > INT32_MAX) return fail(RF_E_SHAPE, "n_rows out of range");
+  if (n_rows < 0 || n_rows > kMaxRows)
+    return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23", (long long)n_rows);
   rf::RopeFreq f = {};
   f.layout = RF_ROPE_HALF;
   if (rope) {
@@ -238,7 +253,9 @@ rf_status ridgefill_tree_attention(const rf_paged_batch* kv, const uint16_t* k_p
 size_t ridgefill_attention_weight_workspace_bytes(const rf_paged_batch* kv, int32_t n_q_heads,
                                                   int32_t max_q) {
   rf::Batch b;
-  if (check_batch(kv, false, b) != RF_OK || check_heads(b, n_q_heads, max_q) != RF_OK) return 0;
+  if (check_batch(kv, false, b) != RF_OK || check_heads(b, n_q_heads, max_q) != RF_OK ||
+      check_weights(b) != RF_OK)
+    return 0;
   return rf::weight_workspace(b, n_q_heads, max_q);
 }
 
@@ -252,6 +269,7 @@ rf_status ridgefill_attention_weight(const rf_paged_batch* kv, const uint16_t* k
   rf_status s = check_batch(kv, false, b);
   if (s == RF_OK)
     s = check_queries(b, q, n_q_heads, q_stride, q_start, n_q, max_q, tree_mask, scale);
+  if (s == RF_OK) s = check_weights(b);
   if (s == RF_OK) s = check_memory(b, ws, ws_bytes, rf::weight_workspace(b, n_q_heads, max_q));
   if (s != RF_OK) return s;
   if (!k_pages || !acc_out || (n_q > 0 && !lse))

@@ -6,7 +6,8 @@
 // found by a radix select of 8 bits a pass; of the rows at that key the lowest are kept.  The
 // keys stay in LDS (up to 32,768 rows; in registers they, and the votes that the compiler kept
 // with them, spilled), and there are sixteen histograms side by side: weights share most of
-// their leading bits, so in one all lanes would count in the same few words, one after another.  //
+// their leading bits, so in one all lanes would count in the same few words, one after another.
+//
 // A kept row below n_keep stays where it is and a kept row above moves into a free row below:
 // the sources (>= n_keep) and the destinations (< n_keep) are disjoint, so rows move in place
 // and in parallel, and only k (1 - k/n) of the k kept rows move (of n, evenly spread), 64 of
@@ -375,7 +376,8 @@ hipError_t launch_evict(const Batch& b, const EvictCall& c, uint16_t* const* poo
                      lds, stream, b, c, head, moves, reinterpret_cast<MoveRow*>(p + w.rows), w.most,
                      divide_by((unsigned)b.page_size));
   const int row16 = b.n_kv * b.hd / 8;
-  const int per = row16 < 1024 ? 1024 / row16 : 1;
+  int per = row16 < 1024 ? 1024 / row16 : 1;
+  if (w.most / per > 1 << 22) per = (int)(w.most >> 22) + 1;    // within a grid's threads
   const unsigned blocks = w.most > 0 ? (unsigned)((w.most + per - 1) / per) : 1u;
   for (int first = 0; first == 0 || first < n_pools; first += kEvictPools) {
     EvictPools e = {};

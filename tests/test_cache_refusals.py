@@ -38,7 +38,7 @@ def _rope(x=FAKE, kind=0, n=4, heads=2, hd=64, xs=128, pos=FAKE, out=FAKE + 6553
 
 def test_rope_refusals():
     for kw in (dict(rotary_dim=8), dict(rotary_dim=80), dict(rotary_dim=-16), dict(rotary_dim=24), dict(hd=40),
-               dict(hd=272), dict(hd=0), dict(heads=0), dict(heads=5000), dict(n=-1), dict(xs=120), dict(os_=127),
+               dict(hd=272), dict(hd=0), dict(heads=0), dict(heads=5000), dict(n=-1), dict(n=(1 << 23) + 1), dict(xs=120), dict(os_=127),
                dict(xs=132), dict(kind=1, xs=130), dict(x=FAKE + 8), dict(out=FAKE + 2), dict(pos=FAKE + 1)):
         _refused(_rope(**kw), B.RF_E_SHAPE)
     for kw in (dict(layout=2), dict(layout=-1), dict(scaling=5), dict(scaling=-1), dict(theta=1.0), dict(theta=float("nan")),
@@ -61,7 +61,7 @@ def _append(kv=None, q=FAKE, heads=4, qs=256, qo=FAKE + 65536, qos=256, k=FAKE, 
 def test_append_refusals():
     for kw in BAD_KV + [dict(head_dim=8), dict(head_dim=72), dict(head_dim=512)]:
         _refused(_append(kv=_kv(**kw)), B.RF_E_SHAPE)
-    for kw in (dict(ks=120), dict(vs=129), dict(qs=248), dict(qos=260), dict(n=-1), dict(heads=-1), dict(heads=5000),
+    for kw in (dict(ks=120), dict(vs=129), dict(qs=248), dict(qos=260), dict(n=-1), dict(n=(1 << 23) + 1), dict(heads=-1), dict(heads=5000),
                dict(q=FAKE + 8), dict(k=FAKE + 2), dict(vp=FAKE + 4), dict(rows=FAKE + 2), dict(seq=FAKE + 1),
                dict(pos=FAKE + 2), dict(rotary_dim=128)):
         _refused(_append(**kw), B.RF_E_SHAPE)
@@ -91,7 +91,9 @@ def test_query_refusals(call):
         _refused(call(kv=_kv(**kw)), B.RF_E_SHAPE)
     for kw in (dict(heads=0), dict(heads=3), dict(heads=4098), dict(max_q=0), dict(max_q=65), dict(n=-1), dict(qs=248),
                dict(qs=260), dict(q=FAKE + 8), dict(start=FAKE + 2), dict(mask=FAKE + 4), dict(kp=FAKE + 8),
-               dict(lse=FAKE + 2), dict(kv=_kv(lengths=FAKE + 2))):
+               dict(lse=FAKE + 2), dict(kv=_kv(lengths=FAKE + 2)),
+               dict(kv=_kv(batch=1 << 14), heads=4096, qs=1 << 18, os_=1 << 18) if call is _attend
+               else dict(kv=_kv(batch=1 << 14), heads=4096, qs=1 << 18)):
         _refused(call(**kw), B.RF_E_SHAPE)
     for kw in (dict(q=None), dict(start=None), dict(kp=None), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(ws=None), dict(kv=_kv(lengths=None)), dict(kv=_kv(block_tables=None))):
@@ -110,7 +112,9 @@ def test_attention_refusals():
 def test_weight_refusals():
     for kw in (dict(lse=None), dict(out=None), dict(decay=float("nan"))):
         _refused(_weight(**kw), B.RF_E_INVALID)
-    for kw in (dict(stride=99), dict(acc=FAKE + 1), dict(out=FAKE + 2)):
+    many = dict(batch=1 << 15, max_len=(1 << 14) + 1, table_stride=1 << 14)
+    assert B.ridgefill_attention_weight_workspace_bytes(_kv(**many), 4, 2) == 0
+    for kw in (dict(stride=99), dict(acc=FAKE + 1), dict(out=FAKE + 2), dict(kv=_kv(**many), stride=1 << 15)):
         _refused(_weight(**kw), B.RF_E_SHAPE)
 
 

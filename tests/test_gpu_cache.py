@@ -783,6 +783,48 @@ def test_two_calls_on_two_streams():
         assert torch.equal(out, w)
 
 
+@pytest.mark.parametrize("heads,runs", [(2, 2 ** 17), (32, 2 ** 20)])
+def test_longest_cache(heads, runs):
+    # 2^30 rows: one page of 2^16, over and over.  runs: how many additions follow one another in one
+    # lane (2^30 rows over 1,024 parts of 16 lanes; over 256 parts of two waves, a lane half of each).
+    page, times = 2 ** 16, 2 ** 14
+    cache = R.Cache([page], 1, 64, page, spare=0, seed=3)
+    cache.v[0].add_(1.0)
+    q = _randn(2, 1, heads, 64)
+    table = torch.zeros(1, times, dtype=torch.int32, device=DEV)
+    table.fill_(int(cache.table_np[0, 0]))
+    length = torch.tensor([page * times], dtype=torch.int32, device=DEV)
+    kv = B.make_batch(table, length, page, 1, 1, 64)
+    start = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(1, heads, device=DEV)
+    ws = torch.empty(B.ridgefill_tree_attention_workspace_bytes(kv, heads, 1), dtype=torch.uint8, device=DEV)
+    B.ridgefill_tree_attention(kv, cache.k[0], cache.v[0], q, start, 1, 0.1, out, ws, lse=lse)
+    assert B.ridgefill_read_status(ws) == B.RF_OK
+    want, wl, ot, lt = R.attention(cache, q, [0, 1], None, 0.1)
+    # the oracle counts one addition a row of the page
+    more = 2 * (runs - page) * R.U_FP32 if runs > page else 0.0
+    _close(out, want, ot + more * (1 + want.abs()) * 2, "out")
+    _close(lse, wl + np.log(times), lt + more + 8 * R.U_FP32 * np.log(times), "lse")
+
+
+def test_longest_weight():
+    page, times = 2 ** 16, 2 ** 13
+    cache = R.Cache([page], 1, 64, page, spare=0, seed=4)
+    q, lse = _randn(2, 1, 2, 64), torch.full((1, 2), 3.0, device=DEV)
+    table = torch.zeros(1, times, dtype=torch.int32, device=DEV)
+    table.fill_(int(cache.table_np[0, 0]))
+    length = torch.tensor([page * times], dtype=torch.int32, device=DEV)
+    kv = B.make_batch(table, length, page, 1, 1, 64)
+    acc = torch.full((1, page * times), -1.0, device=DEV)
+    ws = torch.empty(B.ridgefill_attention_weight_workspace_bytes(kv, 2, 1), dtype=torch.uint8, device=DEV)
+    B.ridgefill_attention_weight(kv, cache.k[0], q, torch.tensor([0, 1], dtype=torch.int32, device=DEV), 1, 0.1, lse, acc, ws)
+    assert B.ridgefill_read_status(ws) == B.RF_OK
+    acc = acc.view(times, page)
+    want, tol = R.weight(cache, q, [0, 1], None, 0.1, lse, 1.0, None, acc[:1].clone())
+    _close(acc[:1], want, tol, "weight")
+    assert bool((acc == acc[:1]).all())
+
+
 def test_another_stream():
     cache, q, starts, words, max_q = _case([3000], [5], 8, 2, 128, 16, seed=6, tree=True)
     ref, ref_lse, _ = _attend(cache, q, starts, words, max_q, 0.1)
