@@ -13,6 +13,11 @@
 // and in parallel, and only k (1 - k/n) of the k kept rows move (of n, evenly spread), 64 of
 // 4096 where 64 new rows have been appended, while closing the gaps in order would move nearly
 // all of them.
+// What the first launch is bound by is one compute unit's instructions, so it leaves the second,
+// which has the whole chip, the looking up of pages and the moved rows' weights and positions.
+// 8 sequences of 4,160 rows cut to 4,096, 4 layers: 15 + 6 us (with the lookups in the first
+// launch 19 + 6); one of 32,768 cut to 16,384: 36 + 61 us (57 + 65), the moving of 8,192 rows at
+// 4.4 TB/s.
 #include "rf_cache_dev.h"
 
 namespace rf {
@@ -22,10 +27,18 @@ namespace {
 constexpr int kSel = 1024;      // threads of the selecting workgroup
 constexpr int kWaves = kSel / 64;
 
-// Workspace: status; per sequence {moves, error bits}; per sequence the list of moves as pool
-// slots {from, to} and, before that, the moving rows' {from, to, weight, position}.
+struct MoveRow {
+  int from, to;
+  float weight;
+  int pos;
+};
+struct EvictHead {              // of a sequence
+  int moves, err, old_len;      // old_len: 0 where nothing is cut
+};
+
+// Workspace: status; per sequence its head; per sequence the moving rows.
 struct EvictWs {
-  size_t head, moves, rows, total;
+  size_t head, rows, total;
   int64_t most;                 // moves of one sequence at most
 };
 EvictWs evict_ws(const Batch& b, int n_keep) {
@@ -33,9 +46,8 @@ EvictWs evict_ws(const Batch& b, int n_keep) {
   const int64_t over = b.max_len > n_keep ? b.max_len - n_keep : 0;
   w.most = over < n_keep ? over : n_keep;
   w.head = kStatusBytes;
-  w.moves = w.head + align256((size_t)b.batch * 8);
-  w.rows = w.moves + align256((size_t)b.batch * w.most * 8);
-  w.total = w.rows + align256((size_t)b.batch * w.most * 16);
+  w.rows = w.head + align256((size_t)b.batch * sizeof(EvictHead));
+  w.total = w.rows + align256((size_t)b.batch * w.most * sizeof(MoveRow));
   return w;
 }
 
@@ -46,14 +58,9 @@ __device__ __forceinline__ uint32_t weight_order(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct MoveRow {
-  int from, to;
-  float weight;
-  int pos;
-};
-
 constexpr int kCopies = 16;     // histograms, one to two banks
 constexpr int kRun = 33;        // most rows in a row that a thread takes where their order counts
+constexpr int kMostPer = 512;   // moves of a copying workgroup: 1,024 pieces of rows of two or more
 constexpr int kHeldRows = (kRun - 1) * kSel;    // rows that LDS holds at a time
 
 // Inclusive prefix sum over the wave, by row shifts and broadcasts in registers.
@@ -89,17 +96,18 @@ __device__ __forceinline__ int block_before(int v, int* part, int* all) {
 // kHold: the keys of all rows lie in LDS (max_len <= kHeldRows); else they are formed anew in each
 // pass, and LDS holds those of 32,768 rows at a time where their order counts.
 template <bool kHold>
-__global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c, int2* head,
-                                                            int2* moves, MoveRow* mrows,
-                                                            int64_t most, Divide by_page) {
-  extern __shared__ uint32_t held[];            // keys, then what becomes of the rows: [whole runs]
-  __shared__ unsigned hist[256 * kCopies];
+__global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c, EvictHead* head,
+                                                            MoveRow* rows, int64_t most,
+                                                            unsigned* status) {
+  extern __shared__ uint32_t held[];            // keys, then the lists of free and of moving rows
+  __shared__ unsigned hist[256 * kCopies], digits[256];
   __shared__ int red[kWaves];
   __shared__ unsigned sh_digit, sh_need;
   const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int len = b.lengths[seq];
+  if (seq == 0 && tid == 0) *status = 0u;       // the second launch adds the errors
   if (len < 0 || len > b.max_len) {
-    if (tid == 0) head[seq] = make_int2(0, (int)kStatusRowsBit);
+    if (tid == 0) head[seq] = {0, (int)kStatusRowsBit, 0};
     return;
   }
   const float* acc = c.acc + seq * c.stride;
@@ -110,15 +118,17 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   int err = 0;
 
   // Thread tid looks after rows tid, tid + 1024, ..: chunk i's is 1024 i + tid.  Values are fetched
-  // eight chunks at a time, or each chunk would wait for its own.
+  // sixteen chunks at a time, or each chunk would wait for its own.
   const int chunks = (len + kSel - 1) / kSel;
-  const auto batches = [&](int from, int to, auto fetch, auto body) {   // body(i, fetch(i))
-    for (int i0 = from; i0 < to; i0 += 8) {
-      decltype(fetch(0)) v[8];
+  constexpr int kFetch = 16;
+  const auto batches = [&](int to, auto fetch, auto body) {             // body(i, fetch(i))
+    for (int i0 = 0; i0 < to; i0 += kFetch) {
+      decltype(fetch(0)) v[kFetch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fetch(i0 + j);
+      for (int j = 0; j < kFetch; ++j)
+        if (i0 + (j & ~3) < to) v[j] = fetch(i0 + j);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kFetch; ++j)
         if (i0 + j < to) body(i0 + j, v[j]);
     }
   };
@@ -126,16 +136,26 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
     float w;
     int p;
   };
-  const auto row_at = [&](int i) -> Row {             // past the end: the last row (len > 0)
-    const int t = i * kSel + tid < len ? i * kSel + tid : len - 1;
-    return {acc[t], pos[t]};
+  const auto at = [&](int i) { return i * kSel + tid < len ? i * kSel + tid : len - 1; };   // len > 0
+  const auto row_at = [&](int i) -> Row { return {acc[at(i)], pos[at(i)]}; };
+  const auto copy_rows = [&](int n) {           // rows that stay, unless they are there already
+    if (acc_out == acc && pos_out == pos) return;
+    batches((n + kSel - 1) / kSel, row_at, [&](int i, const Row& r) {
+      if (i * kSel + tid >= n) return;
+      acc_out[i * kSel + tid] = r.w;
+      pos_out[i * kSel + tid] = r.p;
+    });
   };
   int top = INT32_MIN;
-  batches(0, chunks, row_at, [&](int i, const Row& r) {
+  batches(chunks, row_at, [&](int i, const Row& r) {
     top = max(top, r.p);
     if (r.w != r.w) err = 1;
     if constexpr (kHold) held[i * kSel + tid] = i * kSel + tid < len ? weight_order(r.w) : 0u;
   });
+  // whole eights of chunks: keys of 0, the lowest, after the last row change nothing below
+  if constexpr (kHold)
+    for (int i = chunks; i & 7; ++i) held[i * kSel + tid] = 0u;
+  for (int x = tid; x < 256 * kCopies; x += kSel) hist[x] = 0u;
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, __shfl_xor(top, d));
   if (lane == 0) red[wave] = top;
@@ -143,16 +163,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   for (int w = 0; w < kWaves; ++w) top = max(top, red[w]);
 
   if (len <= keep) {                                // nothing to cut
-    batches(0, chunks, row_at, [&](int i, const Row& r) {
-      const int t = i * kSel + tid;
-      if (t < len) {
-        acc_out[t] = r.w;
-        pos_out[t] = r.p;
-      }
-    });
+    copy_rows(len);
     if (tid == 0) {
       c.len_out[seq] = len;
-      head[seq] = make_int2(0, err);
+      head[seq] = {0, err, 0};
     }
     return;
   }
@@ -160,39 +174,47 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   const int64_t newest = (int64_t)top - c.n_recent;   // protected above this position
   const auto safe = [&](int p) { return p < c.n_sink || p > newest; };
   if constexpr (kHold)
-    batches(0, chunks, [&](int i) { return pos[i * kSel + tid < len ? i * kSel + tid : len - 1]; },
+    batches(chunks, [&](int i) { return pos[at(i)]; },
             [&](int i, int p) {
               if (i * kSel + tid < len && safe(p)) held[i * kSel + tid] = 0xffffffffu;
             });
-  const auto key_at = [&](int i) -> uint32_t {        // a thread reads its own entries only
-    if constexpr (kHold) return held[(i < chunks ? i : chunks - 1) * kSel + tid];
-    const Row r = row_at(i);
-    return safe(r.p) ? 0xffffffffu : weight_order(r.w);
-  };
+  const auto key_of = [&](const Row& r) { return safe(r.p) ? 0xffffffffu : weight_order(r.w); };
   // the keep-th largest key, digit by digit; `need` of the rows at it are kept
   uint32_t prefix = 0u, mask = 0u;
   unsigned need = (unsigned)keep;
   for (int shift = 24; keep > 0 && shift >= 0; shift -= 8) {
-    for (int x = tid; x < 256 * kCopies; x += kSel) hist[x] = 0u;
+    const auto count = [&](uint32_t k) {
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift & 0xffu) * kCopies + lane % kCopies], 1u);
+    };
+    if constexpr (kHold) {                          // a thread reads its own entries
+      for (int i0 = 0; i0 < chunks; i0 += 8) {
+        uint32_t k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) k[j] = held[(i0 + j) * kSel + tid];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) count(k[j]);
+      }
+    } else {
+      batches(chunks, row_at, [&](int i, const Row& r) {
+        if (i * kSel + tid < len) count(key_of(r));
+      });
+    }
     __syncthreads();
-    batches(0, chunks, key_at, [&](int i, uint32_t k) {
-      if (i * kSel + tid < len && (k & mask) == prefix)
-        atomicAdd(&hist[(k >> shift & 0xffu) * kCopies + lane % kCopies], 1u);
-    });
-    __syncthreads();
-    // four lanes a digit add up its copies, each starting at another bank
+    // four lanes a digit add up its copies, each starting at another bank, and clear them
     unsigned part = 0u;
 #pragma unroll
-    for (int x = 0; x < kCopies / 4; ++x)
-      part += hist[(tid >> 2) * kCopies + (tid & 3) * (kCopies / 4) + ((x + (tid >> 3)) & (kCopies / 4 - 1))];
+    for (int x = 0; x < kCopies / 4; ++x) {
+      unsigned* h = hist + (tid >> 2) * kCopies + (tid & 3) * (kCopies / 4) + ((x + (tid >> 3)) & (kCopies / 4 - 1));
+      part += *h;
+      *h = 0u;
+    }
     part += __shfl_xor(part, 1);
     part += __shfl_xor(part, 2);
-    __syncthreads();
-    if ((tid & 3) == 0) hist[tid >> 2] = part;
+    if ((tid & 3) == 0) digits[tid >> 2] = part;
     __syncthreads();
     if (wave == 0) {                                // lane l: digits 255-4l down to 252-4l
       unsigned v[4], s = 0u;
-      for (int i = 0; i < 4; ++i) s += v[i] = hist[255 - 4 * lane - i];
+      for (int i = 0; i < 4; ++i) s += v[i] = digits[255 - 4 * lane - i];
       const unsigned run = (unsigned)wave_scan((int)s);
       unsigned above = run - s;                     // keys with a larger digit
       for (int i = 0; i < 4; ++i) {
@@ -211,16 +233,21 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
 
   // In order: which rows are kept, the free rows below keep, the kept rows from keep on.  A thread
   // takes up to 33 rows in a row (an odd number: no two of 64 runs begin at one bank), a bit each, so
-  // that counts of bits and scans over the threads rank them; what becomes of a row replaces its
-  // key, and is done with the rows dealt out as before.
-  constexpr uint32_t kStays = 0u, kFree = 1u, kMoves = 2u, kCut = 3u;   // in the top two bits; the rank below
-  MoveRow* list = mrows + seq * most;
+  // that counts of bits and scans over the threads rank them; the free rows replace the keys from
+  // the first on, the moving ones from the last on back, and go from there to the list side by side.
+  MoveRow* list = rows + seq * most;
   int ties = 0, holes = 0, movers = 0;                // of the rows before these
   for (int t0 = 0; t0 < len; t0 += kHeldRows) {
     const int here = len - t0 < kHeldRows ? len - t0 : kHeldRows, deal = (here + kSel - 1) / kSel;
-    const int c0 = t0 / kSel, size = deal | 1;
+    const int size = deal | 1;
     if constexpr (!kHold)
-      batches(c0, c0 + deal, key_at, [&](int i, uint32_t k) { held[(i - c0) * kSel + tid] = k; });
+      for (int i0 = 0; i0 < deal; i0 += 8) {
+        Row r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = row_at(t0 / kSel + i0 + j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) held[(i0 + j) * kSel + tid] = key_of(r[j]);
+      }
     __syncthreads();
     const int run0 = tid * size, n = here - run0 < 0 ? 0 : here - run0 < size ? here - run0 : size;
     const uint32_t* run = held + (n ? run0 : 0);
@@ -248,88 +275,85 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
     const uint64_t kept = (larger & valid) | equal;
     const int under = keep - (t0 + run0);             // of the run, the rows below keep
     const uint64_t low = under >= n ? valid : under <= 0 ? 0ull : (1ull << under) - 1;
-    int hole = holes + block_before(__popcll(low & ~kept), red, &all);
-    holes += all;
-    int mover = movers + block_before(__popcll(kept & ~low), red, &all);
-    movers += all;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const bool is = kept >> j & 1, lo = low >> j & 1;
-      held[run0 + j] = is ? lo ? kStays << 30 : kMoves << 30 | (uint32_t)mover : lo ? kFree << 30 | (uint32_t)hole : kCut << 30;
-      hole += lo && !is;
-      mover += !lo && is;
-    }
+    uint64_t open = low & ~kept, moving = kept & ~low;
+    int new_holes, new_movers;
+    uint32_t* hole = held + block_before(__popcll(open), red, &new_holes);
+    uint32_t* mover = held + here - 1 - block_before(__popcll(moving), red, &new_movers);
+    for (; open; open &= open - 1) *hole++ = (uint32_t)(t0 + run0 + __ffsll((unsigned long long)open) - 1);
+    for (; moving; moving &= moving - 1) *mover-- = (uint32_t)(t0 + run0 + __ffsll((unsigned long long)moving) - 1);
     __syncthreads();
-    batches(c0, c0 + deal, row_at, [&](int i, const Row& r) {
-      const int t = i * kSel + tid;
-      if (t >= len) return;
-      const uint32_t x = held[t - t0], what = x >> 30, at = x & 0x3fffffffu;
-      if (what == kFree) list[at].to = t;
-      if (what == kMoves) {
-        list[at].from = t;
-        list[at].weight = r.w;
-        list[at].pos = r.p;
-      }
-      if (what == kStays) {
-        acc_out[t] = r.w;
-        pos_out[t] = r.p;
-      }
-      if (t >= keep) acc_out[t] = 0.f;
-    });
-    __syncthreads();                                  // LDS is written again; the list is whole
-  }
-  const auto slot_of = [&](int t) -> int {
-    const int pi = (int)quotient((unsigned)t, by_page), page = b.tables[(int64_t)seq * b.table_stride + pi];
-    return page < 0 || page >= b.num_pages ? -1 : page * b.page_size + (t - pi * b.page_size);
-  };
-  int bad = 0;
-#pragma unroll 1
-  for (int i0 = tid; i0 < movers; i0 += 8 * kSel) {   // eight at a time
-    MoveRow r[8];
-    int2 m[8];
+    for (int x = tid; x < new_holes; x += kSel) list[holes + x].to = (int)held[x];
+    for (int x0 = tid; x0 < new_movers; x0 += 8 * kSel) {   // eight at a time
+      MoveRow r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = list[i0 + j * kSel < movers ? i0 + j * kSel : i0];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = make_int2(slot_of(r[j].from), slot_of(r[j].to));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * kSel;
-      if (i >= movers) continue;
-      acc_out[r[j].to] = r[j].weight;
-      pos_out[r[j].to] = r[j].pos;
-      if (m[j].x < 0 || m[j].y < 0) {
-        bad = 1;
-        m[j] = make_int2(-1, -1);
+      for (int j = 0; j < 8; ++j) {
+        r[j].from = (int)held[here - 1 - (x0 + j * kSel < new_movers ? x0 + j * kSel : x0)];
+        r[j].weight = acc[r[j].from];
+        r[j].pos = pos[r[j].from];
       }
-      moves[seq * most + i] = m[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (x0 + j * kSel < new_movers) {
+          MoveRow* m = list + movers + x0 + j * kSel;
+          m->from = r[j].from;
+          m->weight = r[j].weight;
+          m->pos = r[j].pos;
+        }
     }
+    holes += new_holes;
+    movers += new_movers;
+    __syncthreads();                                  // LDS is written again
   }
-  bad = __syncthreads_or(bad);
+  copy_rows(keep);
   if (tid == 0) {
     c.len_out[seq] = keep;
-    head[seq] = make_int2(movers, err | (bad ? (int)kStatusRowsBit : 0));
+    head[seq] = {movers, err, len};
   }
 }
 
 // blockIdx.x: `per` of a sequence's moves, y: pool, z: sequence.  A row is n_kv * hd bf16
 // values in one piece, row16 pieces of 16 bytes; a thread has up to four of them under way.
-__global__ __launch_bounds__(256) void evict_move_kernel(EvictPools pools, const int2* head,
-                                                         const int2* moves, int64_t most, int per,
-                                                         int row16, Divide by_row, int batch,
+// With `status` the first y is none of the pools but the rows' weights and positions (weights of
+// 0 from keep on) and, of its first workgroup, the errors.
+__global__ __launch_bounds__(256) void evict_move_kernel(EvictPools pools, Batch b, EvictCall c,
+                                                         const EvictHead* head, const MoveRow* rows,
+                                                         int64_t most, int per, int row16,
+                                                         Divide by_row, Divide by_page,
                                                          unsigned* status) {
-  if (status && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-    int bits = 0;
-    for (int s = threadIdx.x; s < batch; s += 256) bits |= head[s].y;
-    const int rows = __syncthreads_or(bits & (int)kStatusRowsBit);
-    const int nan = __syncthreads_or(bits & (int)kStatusScoreBit);
-    if (threadIdx.x == 0) *status = (rows ? kStatusRowsBit : 0u) | (nan ? kStatusScoreBit : 0u);
+  __shared__ int2 sh_move[kMostPer];
+  const int seq = blockIdx.z;
+  const MoveRow* list = rows + seq * most;
+  const auto slot_of = [&](int t) -> int {
+    const int pi = (int)quotient((unsigned)t, by_page), page = b.tables[(int64_t)seq * b.table_stride + pi];
+    return page < 0 || page >= b.num_pages ? -1 : page * b.page_size + (t - pi * b.page_size);
+  };
+  const EvictHead h = head[seq];
+  if (status && blockIdx.y == 0) {
+    float* acc_out = c.acc_out + seq * c.stride;
+    int32_t* pos_out = c.pos_out + seq * c.stride;
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    bool bad = false;
+    for (int64_t i = first; i < h.moves; i += step) {
+      const MoveRow r = list[i];
+      acc_out[r.to] = r.weight;
+      pos_out[r.to] = r.pos;
+      bad |= slot_of(r.from) < 0 || slot_of(r.to) < 0;
+    }
+    for (int64_t t = c.n_keep + first; t < h.old_len; t += step) acc_out[t] = 0.f;
+    const unsigned bits = (blockIdx.x == 0 ? (unsigned)h.err : 0u) | (__any(bad) ? kStatusRowsBit : 0u);
+    if (bits && (threadIdx.x & 63) == 0) atomicOr(status, bits);
+    return;
   }
-  const int64_t first = (int64_t)blockIdx.x * per;
-  const int64_t left = head[blockIdx.z].x - first;
+  const int64_t first = (int64_t)blockIdx.x * per, left = h.moves - first;
   if (left <= 0) return;
-  const int total = (int)(left < per ? left : per) * row16;
-  const int2* mv = moves + blockIdx.z * most + first;
-  u32x4* p = reinterpret_cast<u32x4*>(pools.p[blockIdx.y]);
+  const int n = (int)(left < per ? left : per), total = n * row16;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const MoveRow r = list[first + i];
+    const int2 m = make_int2(slot_of(r.from), slot_of(r.to));
+    sh_move[i] = m.x < 0 || m.y < 0 ? make_int2(-1, -1) : m;
+  }
+  __syncthreads();
+  u32x4* p = reinterpret_cast<u32x4*>(pools.p[blockIdx.y - (status ? 1 : 0)]);
   for (int i0 = threadIdx.x; i0 < total; i0 += 1024) {
     u32x4 v[4];
     int64_t to[4];
@@ -339,7 +363,7 @@ __global__ __launch_bounds__(256) void evict_move_kernel(EvictPools pools, const
       to[j] = -1;
       if (i < total) {
         const int m = (int)quotient((unsigned)i, by_row), e = i - m * row16;
-        const int2 w = mv[m];
+        const int2 w = sh_move[m];
         if (w.x >= 0) {
           v[j] = p[(int64_t)w.x * row16 + e];
           to[j] = (int64_t)w.y * row16 + e;
@@ -361,10 +385,10 @@ hipError_t launch_evict(const Batch& b, const EvictCall& c, uint16_t* const* poo
   const EvictWs w = evict_ws(b, c.n_keep);
   unsigned char* p = static_cast<unsigned char*>(ws);
   unsigned* status = reinterpret_cast<unsigned*>(p);
-  int2* head = reinterpret_cast<int2*>(p + w.head);
-  int2* moves = reinterpret_cast<int2*>(p + w.moves);
+  EvictHead* head = reinterpret_cast<EvictHead*>(p + w.head);
+  MoveRow* rows = reinterpret_cast<MoveRow*>(p + w.rows);
   const bool hold = b.max_len <= kHeldRows;
-  const int deal = hold ? (b.max_len + kSel - 1) / kSel : kRun - 1;
+  const int deal = hold ? (b.max_len + 8 * kSel - 1) / (8 * kSel) * 8 : kHeldRows / kSel;
   const size_t lds = ((size_t)deal * kSel + kRun + 7) * 4;   // runs are read eight words at a time
   if (lds > 32768) {                                  // beyond what a launch gets unasked
     const hipError_t e = hipFuncSetAttribute(
@@ -373,8 +397,7 @@ hipError_t launch_evict(const Batch& b, const EvictCall& c, uint16_t* const* poo
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(hold ? evict_select_kernel<true> : evict_select_kernel<false>, dim3(b.batch), dim3(kSel),
-                     lds, stream, b, c, head, moves, reinterpret_cast<MoveRow*>(p + w.rows), w.most,
-                     divide_by((unsigned)b.page_size));
+                     lds, stream, b, c, head, rows, w.most, status);
   const int row16 = b.n_kv * b.hd / 8;
   int per = row16 < 1024 ? 1024 / row16 : 1;
   if (w.most / per > 1 << 22) per = (int)(w.most >> 22) + 1;    // within a grid's threads
@@ -383,9 +406,9 @@ hipError_t launch_evict(const Batch& b, const EvictCall& c, uint16_t* const* poo
     EvictPools e = {};
     const int n = n_pools - first < kEvictPools ? n_pools - first : kEvictPools;
     for (int i = 0; i < n; ++i) e.p[i] = pools[first + i];
-    hipLaunchKernelGGL(evict_move_kernel, n ? dim3(blocks, n, b.batch) : dim3(1), dim3(256), 0, stream, e,
-                       head, moves, w.most, per, n ? row16 : 0, divide_by((unsigned)row16), b.batch,
-                       first == 0 ? status : nullptr);
+    hipLaunchKernelGGL(evict_move_kernel, dim3(blocks, n + (first == 0 ? 1 : 0), b.batch), dim3(256), 0, stream,
+                       e, b, c, head, rows, w.most, per, row16, divide_by((unsigned)row16),
+                       divide_by((unsigned)b.page_size), first == 0 ? status : nullptr);
   }
   return hipGetLastError();
 }
