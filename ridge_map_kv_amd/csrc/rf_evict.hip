@@ -15,9 +15,9 @@
 // all of them.
 // What the first launch is bound by is one compute unit's instructions, so it leaves the second,
 // which has the whole chip, the looking up of pages and the moved rows' weights and positions.
-// 8 sequences of 4,160 rows cut to 4,096, 4 layers: 15 + 6 us (with the lookups in the first
-// launch 19 + 6); one of 32,768 cut to 16,384: 36 + 61 us (57 + 65), the moving of 8,192 rows at
-// 4.4 TB/s.
+// 8 sequences of 4,160 rows cut to 4,096, 4 layers: 14 + 6 us (with the lookups in the first
+// launch 19 + 6); one of 32,768 cut to 16,384: 32 + 61 us (57 + 65), the moving of 8,192 rows at
+// 4.4 TB/s.  Of the 32 us 6 go to reading weights and positions, 10 to the radix select.
 #include "rf_cache_dev.h"
 
 namespace rf {
@@ -27,7 +27,7 @@ namespace {
 constexpr int kSel = 1024;      // threads of the selecting workgroup
 constexpr int kWaves = kSel / 64;
 
-struct MoveRow {
+struct __attribute__((aligned(16))) MoveRow {
   int from, to;
   float weight;
   int pos;
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   extern __shared__ uint32_t held[];            // keys, then the lists of free and of moving rows
   __shared__ unsigned hist[256 * kCopies], digits[256];
   __shared__ int red[kWaves];
-  __shared__ unsigned sh_digit, sh_need;
+  __shared__ unsigned sh_digit, sh_need, sh_all;
   const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int len = b.lengths[seq];
   if (seq == 0 && tid == 0) *status = 0u;       // the second launch adds the errors
@@ -118,9 +118,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   int err = 0;
 
   // Thread tid looks after rows tid, tid + 1024, ..: chunk i's is 1024 i + tid.  Values are fetched
-  // sixteen chunks at a time, or each chunk would wait for its own.
+  // eight chunks at a time, or each chunk would wait for its own (sixteen: longer code, which is fetched
+  // once for each launch: 15.4 instead of 14.4 us for 4,160 rows, no gain for 32,768).
   const int chunks = (len + kSel - 1) / kSel;
-  constexpr int kFetch = 16;
+  constexpr int kFetch = 8;
   const auto batches = [&](int to, auto fetch, auto body) {             // body(i, fetch(i))
     for (int i0 = 0; i0 < to; i0 += kFetch) {
       decltype(fetch(0)) v[kFetch];
@@ -146,9 +147,10 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
       pos_out[i * kSel + tid] = r.p;
     });
   };
-  int top = INT32_MIN;
+  int top = INT32_MIN, bottom = INT32_MAX;
   batches(chunks, row_at, [&](int i, const Row& r) {
     top = max(top, r.p);
+    bottom = min(bottom, r.p);
     if (r.w != r.w) err = 1;
     if constexpr (kHold) held[i * kSel + tid] = i * kSel + tid < len ? weight_order(r.w) : 0u;
   });
@@ -158,6 +160,9 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   for (int x = tid; x < 256 * kCopies; x += kSel) hist[x] = 0u;
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, __shfl_xor(top, d));
+#pragma unroll
+  for (int d = 32; d; d >>= 1) bottom = min(bottom, __shfl_xor(bottom, d));
+  const int wave_top = top;
   if (lane == 0) red[wave] = top;
   err = __syncthreads_or(err) ? (int)kStatusScoreBit : 0;
   for (int w = 0; w < kWaves; ++w) top = max(top, red[w]);
@@ -174,12 +179,14 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
   const int64_t newest = (int64_t)top - c.n_recent;   // protected above this position
   const auto safe = [&](int p) { return p < c.n_sink || p > newest; };
   if constexpr (kHold)
-    batches(chunks, [&](int i) { return pos[at(i)]; },
-            [&](int i, int p) {
-              if (i * kSel + tid < len && safe(p)) held[i * kSel + tid] = 0xffffffffu;
-            });
+    if (safe(bottom) || safe(wave_top))             // few waves have a protected row
+      batches(chunks, [&](int i) { return pos[at(i)]; },
+              [&](int i, int p) {
+                if (i * kSel + tid < len && safe(p)) held[i * kSel + tid] = 0xffffffffu;
+              });
   const auto key_of = [&](const Row& r) { return safe(r.p) ? 0xffffffffu : weight_order(r.w); };
-  // the keep-th largest key, digit by digit; `need` of the rows at it are kept
+  // the keep-th largest key, digit by digit; `need` of the rows at it are kept.  Where all rows of a
+  // digit are needed the digits after it are not (after three of them that is nearly always so).
   uint32_t prefix = 0u, mask = 0u;
   unsigned need = (unsigned)keep;
   for (int shift = 24; keep > 0 && shift >= 0; shift -= 8) {
@@ -221,6 +228,7 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
         if (above < need && need <= above + v[i]) {
           sh_digit = 255u - 4u * lane - i;
           sh_need = need - above;
+          sh_all = need - above == v[i];
         }
         above += v[i];
       }
@@ -229,6 +237,11 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
     prefix |= sh_digit << shift;
     mask |= 0xffu << shift;
     need = sh_need;
+    if (sh_all) {                                   // all from `prefix` on: those above prefix - 1, which
+      --prefix;                                     // is not below 0, or all rows would be kept
+      need = 0u;
+      break;
+    }
   }
 
   // In order: which rows are kept, the free rows below keep, the kept rows from keep on.  A thread
@@ -282,12 +295,15 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
     for (; open; open &= open - 1) *hole++ = (uint32_t)(t0 + run0 + __ffsll((unsigned long long)open) - 1);
     for (; moving; moving &= moving - 1) *mover-- = (uint32_t)(t0 + run0 + __ffsll((unsigned long long)moving) - 1);
     __syncthreads();
-    for (int x = tid; x < new_holes; x += kSel) list[holes + x].to = (int)held[x];
+    if constexpr (!kHold)                             // else as many as rows that move: with those
+      for (int x = tid; x < new_holes; x += kSel) list[holes + x].to = (int)held[x];
     for (int x0 = tid; x0 < new_movers; x0 += 8 * kSel) {   // eight at a time
       MoveRow r[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        r[j].from = (int)held[here - 1 - (x0 + j * kSel < new_movers ? x0 + j * kSel : x0)];
+        const int x = x0 + j * kSel < new_movers ? x0 + j * kSel : x0;
+        r[j].from = (int)held[here - 1 - x];
+        if constexpr (kHold) r[j].to = (int)held[x];
         r[j].weight = acc[r[j].from];
         r[j].pos = pos[r[j].from];
       }
@@ -295,9 +311,13 @@ __global__ __launch_bounds__(kSel) void evict_select_kernel(Batch b, EvictCall c
       for (int j = 0; j < 8; ++j)
         if (x0 + j * kSel < new_movers) {
           MoveRow* m = list + movers + x0 + j * kSel;
-          m->from = r[j].from;
-          m->weight = r[j].weight;
-          m->pos = r[j].pos;
+          if constexpr (kHold) {
+            *m = r[j];
+          } else {
+            m->from = r[j].from;
+            m->weight = r[j].weight;
+            m->pos = r[j].pos;
+          }
         }
     }
     holes += new_holes;
