@@ -216,7 +216,9 @@ __device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, cons
 
 // kOut: with the product with V (else only the statistics).
 // At most 16 query rows: bound by the read of K and V.  16 sequences of up to 16,384 rows, one token,
-// 8 key heads of 128 (805 MB): 145 us of the call's 155, 5.5 TB/s, as a large copy.
+// 8 key heads of 128 (805 MB): 147 us of the call's 154, 5.5 TB/s, as a large copy.  (The tile kernel
+// below takes 187 us there; this one, with four tiles of 16 queries, takes 120 us for 64 query rows
+// over 65,536 where that takes 70.)
 template <int HD, bool kOut>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   constexpr int kSteps = HD / 32, kFeat = HD / 16;
@@ -463,6 +465,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // pieces of a row lie in the order piece ^ (row % 8) for K, piece ^ 4 (row % 2) for V, which
 // spreads both kinds of read over all banks.  The pool slots of the workgroup's rows are looked
 // up beforehand: a table load between the direct loads would wait for those.
+// Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 147 us
+// with the join's 9, 395 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 147 us, 587 TFLOP/s.
+// What bounds it are the vector instructions, 1,700 cycles a wave and step of 64 rows, with two
+// waves to a SIMD (exponentials 512 of them), at a clock that 256 busy query rows pull down to
+// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  Blocks of 128 rows took 248, two workgroups
+// for each compute unit 203 us.
 constexpr int kTileRows = 64;
 constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;
@@ -844,7 +852,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 }
 
 // Joins the parts of one output row by kPer waves: sixteen lanes hold the row, four parts to a
-// wave at a time (and several of those in flight: one at a time, 128 parts took 80 us).
+// wave at a time (and several of those in flight: one at a time, 128 parts took 80 us).  One token
+// over 65,536 rows, 8 key heads: 64 us by four waves a row, 72 by one; one key head 26 and 40.
 template <int HD, int kPer>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
   constexpr int kE = HD / 16;

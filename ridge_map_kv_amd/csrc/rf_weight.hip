@@ -11,10 +11,12 @@
 //
 // M <= 64 (decoding, small trees): bound by the read of K.  A workgroup takes 64 or more cache
 // rows and all key heads (its waves share them out), joins the heads in LDS and writes the
-// accumulated weight: one launch.
+// accumulated weight: one launch.  16 sequences of up to 16,384 rows, one token, 8 key heads of
+// 128: 73 us, 5.5 TB/s, as a large copy.
 // M > 64: bound by the exponentials (16 cycles a wave of 64) and the matrix cores.  Q of one key
 // head (256 rows a block) lies in LDS and a workgroup walks a long range of cache rows with it;
-// the heads' sums meet in a second launch.
+// the heads' sums meet in a second launch.  The last 64 tokens of 32,768 rows, 32 query heads: 38 + 5
+// us, 431 TFLOP/s; the exponentials alone are 12 us (24 cycles with their addition), staging Q 7.
 #include "rf_cache_dev.h"
 
 namespace rf {
@@ -232,13 +234,15 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
     const int x = tid + j * kHeadThreads, m = x / (HD / 8), ch = x % (HD / 8);
     sh_q[m / 16][ch / 4][ch % 4 * 16 + m % 16] = m < m_rows ? piece[j] : u32x4{0u, 0u, 0u, 0u};
   }
+  bool off = false;                                 // some query of the tiles gives nothing
   for (int m = tid; m < kBlock; m += kHeadThreads) {
     const bool in = m < m_rows;
     const int i = in ? (int)quotient((unsigned)(m0 + m), a.by_group) : 0, h = kh * a.group + (in ? m0 + m - i * a.group : 0);
     sh_lse[m] = in ? a.lse[(int64_t)(first + i) * a.q.n_heads + h] * kLog2e : -INFINITY;
     sh_word[m] = in ? draft_word(a.q, first + i, i) : 0ull;
+    if (m < 16 * tiles && sh_lse[m] == -INFINITY) off = true;
   }
-  __syncthreads();
+  const bool some_off = __syncthreads_or(off);
 
   float* part = a.part + ((int64_t)(seq * a.b.n_kv + kh) * a.mblocks + mb) * a.b.max_len;
   const float scale2 = a.q.scale * kLog2e;
@@ -257,24 +261,33 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) w[t][r] = 0.f;
-    bf16x8 q_next[kSteps];
+    // Two tiles of queries in turn, the fragments of one on their way while the other is used.
+    const auto fetch = [&](int qt, bf16x8 (&q)[kSteps], float& l) {
+      const int at = qt < tiles ? qt : tiles - 1;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) q_next[s] = __builtin_bit_cast(bf16x8, sh_q[0][s][lane]);
-    float l_next = sh_lse[c];
-    for (int qt = 0; qt < tiles; ++qt) {
-      bf16x8 q[kSteps];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) q[s] = q_next[s];
-      const float l = l_next;
-      const int nt = qt + 1 < tiles ? qt + 1 : qt;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) q_next[s] = __builtin_bit_cast(bf16x8, sh_q[nt][s][lane]);
-      l_next = sh_lse[16 * nt + c];
-      const bool live = l != -INFINITY;
-      uint64_t seen = live ? there : 0ull;
-      if (base + kRows > ctx) seen &= seen64(sh_word[16 * qt + c], base - ctx);
-      add_weights<HD>(keys, q, scale2, l, part_rows || __any(!live), seen, g, w);
-    }
+      for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(bf16x8, sh_q[at][s][lane]);
+      l = sh_lse[16 * at + c];
+    };
+    const auto all_tiles = [&](auto add) {
+      bf16x8 q0[kSteps], q1[kSteps];
+      float l0, l1;
+      fetch(0, q0, l0);
+      for (int qt = 0; qt < tiles; qt += 2) {
+        fetch(qt + 1, q1, l1);
+        add(qt, q0, l0);
+        if (qt + 1 >= tiles) break;
+        fetch(qt + 2, q0, l0);
+        add(qt + 1, q1, l1);
+      }
+    };
+    if (!part_rows && !some_off)
+      all_tiles([&](int, const bf16x8 (&q)[kSteps], float l) { add_weights<HD>(keys, q, scale2, l, false, 0ull, g, w); });
+    else
+      all_tiles([&](int qt, const bf16x8 (&q)[kSteps], float l) {
+        uint64_t seen = l != -INFINITY ? there : 0ull;
+        if (base + kRows > ctx) seen &= seen64(sh_word[16 * qt + c], base - ctx);
+        add_weights<HD>(keys, q, scale2, l, true, seen, g, w);
+      });
     f32x4 mine = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 4; ++t)
