@@ -52,6 +52,8 @@ struct AttendArgs {
   int mblocks;                  // blocks of query rows
   int group;                    // query heads of a key head
   int scan;                     // 1: the first workgroup looks all pages over for the status
+  int report;                   // 1: the workgroups report bad pages and sequences
+  int scan_parts;               // of a sequence, in the join
 };
 
 __device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half) {
@@ -79,27 +81,21 @@ constexpr int kGrain = 64;              // parts are multiples of this many rows
 // One sequence of a batch as a lane looks it up; grains 0: it is skipped.
 struct Seq {
   int len, first, n, grains;
-  bool bad;
 };
 __device__ __forceinline__ Seq look_up(const AttendArgs& a, int b) {
   Seq s = {};
-  if (b < a.b.batch && sequence_of(a.b, a.q, b, &s.len, &s.first, &s.n, &s.bad)) s.grains = (s.len + kGrain - 1) / kGrain;
+  bool bad;
+  if (b < a.b.batch && sequence_of(a.b, a.q, b, &s.len, &s.first, &s.n, &bad)) s.grains = (s.len + kGrain - 1) / kGrain;
   return s;
 }
 
-// Grains of one part, and whether some sequence is in error; `mine`: sequence lane.
-__device__ int grains_of_part(const AttendArgs& a, const Seq& mine, bool* bad) {
+// Grains of one part; `mine`: sequence lane.
+__device__ int grains_of_part(const AttendArgs& a, const Seq& mine) {
   const int lane = threadIdx.x & 63;
   long long total = mine.grains;
-  bool some = mine.bad;
-  for (int b = 64 + lane; b < a.b.batch; b += 64) {
-    const Seq s = look_up(a, b);
-    total += s.grains;
-    some |= s.bad;
-  }
+  for (int b = 64 + lane; b < a.b.batch; b += 64) total += look_up(a, b).grains;
 #pragma unroll
   for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-  *bad = __any(some);
   constexpr int64_t kMost = (1 << 30) / kGrain;         // of the longest sequence
   int each = (int)min((total + a.goal - 1) / a.goal, (long long)kMost);
   if (each < a.least / kGrain) each = a.least / kGrain;
@@ -121,21 +117,21 @@ struct Part {
 };
 __device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
   const int lane = threadIdx.x & 63;
-  bool bad;
   p->kh = unit % a.b.n_kv;
   p->id = unit / a.b.n_kv;
   if (!a.goal) {
     p->seq = p->id;
+    bool bad;
     const bool go = sequence_of(a.b, a.q, p->seq, &p->len, &p->first, &p->n, &bad);
-    if (bad && !a.scan && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+    if (bad && a.report && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
     p->begin = 0;
     p->end = p->len;
     p->whole = true;
     return go;
   }
   Seq s = look_up(a, lane);
-  const int each = grains_of_part(a, s, &bad);
-  if (bad && !a.scan && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRowsBit);
+  const int each = grains_of_part(a, s);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;      // the join adds what is wrong
   int before = 0;                       // parts of the sequences before these 64
   for (int b0 = 0; b0 < a.b.batch; b0 += 64) {
     if (b0) s = look_up(a, b0 + lane);
@@ -216,7 +212,7 @@ __device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, cons
 
 // kOut: with the product with V (else only the statistics).
 // At most 16 query rows: bound by the read of K and V.  16 sequences of up to 16,384 rows, one token,
-// 8 key heads of 128 (805 MB): 147 us of the call's 154, 5.5 TB/s, as a large copy.  (The tile kernel
+// 8 key heads of 128 (805 MB): 146 us of the call's 153, 5.5 TB/s, as a large copy.  (The tile kernel
 // below takes 187 us there; this one, with four tiles of 16 queries, takes 120 us for 64 query rows
 // over 65,536 where that takes 70.)
 template <int HD, bool kOut>
@@ -388,7 +384,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     cur = next;
     slot = slot_next;
   }
-  if (page_err && !a.scan && lane == 0) atomicOr(a.status, kStatusRowsBit);
+  if (page_err && a.report && lane == 0) atomicOr(a.status, kStatusRowsBit);
 
   // sums over g, then the waves: 2 and 3 into 0 and 1, then 1 into 0
   l_run += __shfl_xor(l_run, 16);
@@ -610,7 +606,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
       if (x < steps * kTileRows)                          // -1: not there
         sh_slot[x] = is ? page[i] * a.b.page_size + (part + x - (int)quotient((unsigned)(part + x), a.page) * a.b.page_size) : -1;
     }
-    if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
+    if (a.report && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
     if (tid == 0 && part == begin) sh_wild = 0ull;
     __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): only direct loads from here on
     __syncthreads();
@@ -854,22 +850,26 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 // Joins the parts of one output row by kPer waves: sixteen lanes hold the row, four parts to a
 // wave at a time (and several of those in flight: one at a time, 128 parts took 80 us).  One token
 // over 65,536 rows, 8 key heads: 64 us by four waves a row, 72 by one; one key head 26 and 40.
+// Eight workgroups fit a compute unit (with more registers for the scan: five, 12.6 instead of 9.4
+// us for the trees above).
 template <int HD, int kPer>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
   constexpr int kE = HD / 16;
   __shared__ float sh_o[kPer][HD + 1];
   const int rows = a.q.max_q * a.group;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = threadIdx.x >> 6, g0 = 4 * (wave % kPer) + g;
-  const int64_t id = (int64_t)blockIdx.x * (kWaves / kPer) + wave / kPer;
+  const int scans = a.b.batch * a.scan_parts;
+  if ((int)blockIdx.x < scans)
+    return scan_sequence(a.b, a.q, blockIdx.x / a.scan_parts, blockIdx.x % a.scan_parts, a.scan_parts, a.status);
+  const int64_t id = (int64_t)(blockIdx.x - scans) * (kWaves / kPer) + wave / kPer;
   const int sh = (int)(id / rows), m = (int)(id % rows);
   if (sh >= a.b.batch * a.b.n_kv) return;
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
-  bool bad;
   const Seq mine = look_up(a, lane), self = look_up(a, seq);
   const int n = self.n, first = self.first;
   if (!self.grains || m >= n * a.group) return;
-  const int each = grains_of_part(a, mine, &bad), parts = (self.grains + each - 1) / each;
+  const int each = grains_of_part(a, mine), parts = (self.grains + each - 1) / each;
   if (parts == 1) return;                           // written by its workgroup
   int before = lane < seq ? (mine.grains + each - 1) / each : 0;
   for (int b = 64 + lane; b < seq; b += 64) before += (look_up(a, b).grains + each - 1) / each;
@@ -988,12 +988,12 @@ void launch_head(const AttendArgs& a, const AttendPlan& p, unsigned grid, hipStr
   else
     launch_rows<HD, false>(a, p.rows, grid, stream);
   if (p.goal) {
-    const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
+    const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group, scans = (int64_t)a.b.batch * a.scan_parts;
     if (p.goal > 32)                // a sequence can have more parts than a wave has under way
-      hipLaunchKernelGGL((join_kernel<HD, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((join_kernel<HD, kWaves>), dim3((unsigned)(rows + scans)), dim3(kThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((join_kernel<HD, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads),
-                         0, stream, a);
+      hipLaunchKernelGGL((join_kernel<HD, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves + scans)),
+                         dim3(kThreads), 0, stream, a);
   }
 }
 
@@ -1025,8 +1025,10 @@ hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp,
   a.least = p.least;
   a.mblocks = p.mblocks;
   a.group = p.group;
-  a.scan = scans(b) ? 1 : 0;
-  if (!a.scan) {
+  a.scan = !p.goal && scans(b) ? 1 : 0;
+  a.report = !p.goal && !a.scan ? 1 : 0;
+  a.scan_parts = scan_parts(b);
+  if (a.report) {
     const hipError_t e = launch_clear_status(a.status, stream);
     if (e != hipSuccess) return e;
   }

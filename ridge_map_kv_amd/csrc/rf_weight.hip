@@ -15,8 +15,9 @@
 // 128: 73 us, 5.5 TB/s, as a large copy.
 // M > 64: bound by the exponentials (16 cycles a wave of 64) and the matrix cores.  Q of one key
 // head (256 rows a block) lies in LDS and a workgroup walks a long range of cache rows with it;
-// the heads' sums meet in a second launch.  The last 64 tokens of 32,768 rows, 32 query heads: 38 + 5
-// us, 431 TFLOP/s; the exponentials alone are 12 us (24 cycles with their addition), staging Q 7.
+// the heads' sums meet in a second launch.  The last 64 tokens of 32,768 rows, 32 query heads: 33 + 5
+// us, 35 in one call after another, 485 TFLOP/s; the exponentials alone are 12 us (24 cycles with
+// their addition), staging Q 7.
 #include "rf_cache_dev.h"
 
 namespace rf {
@@ -44,7 +45,8 @@ struct WeightArgs {
   float decay;
   int chunk, splits;            // cache rows of a workgroup, workgroups along them
   int mblocks, group;
-  int scan;
+  int scan;                     // 1: the first workgroup of the only launch looks all pages over
+  int scan_parts;               // of a sequence, in the second launch
 };
 
 // Sum over the 16 lanes of a row of the wave, in every one of them.
@@ -194,15 +196,14 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
   __shared__ u32x4 sh_q[kBlock / 16][kSteps][64];   // as the lanes read them
   __shared__ float sh_lse[kBlock];                  // in log2
   __shared__ uint64_t sh_word[kBlock];
-  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
-  const int id = blockIdx.x - a.scan, split = id % a.splits, unit = id / a.splits;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;      // the sum's launch adds what is wrong
+  const int id = blockIdx.x, split = id % a.splits, unit = id / a.splits;
   const int mb = unit % a.mblocks, kh = unit / a.mblocks % a.b.n_kv, seq = unit / a.mblocks / a.b.n_kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   int len, first, n;
   bool bad;
   const bool go = sequence_of(a.b, a.q, seq, &len, &first, &n, &bad);
-  if (bad && !a.scan && tid == 0) atomicOr(a.status, kStatusRowsBit);
   const int begin = split * a.chunk, m0 = mb * kBlock;
   const int m_rows = n * a.group - m0 < kBlock ? n * a.group - m0 : kBlock;
   if (!go || begin >= len || m_rows <= 0) return;
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
   const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
   const uint16_t* kbase = a.kp + kh * HD;
   const int64_t row_size = (int64_t)a.b.n_kv * HD;
-  bool err = false;
+  bool err = false;                                 // reported by the sum's launch
   int base = begin + wave * kRows;
   Keys<HD> keys;
   int slot = -1;
@@ -306,14 +307,15 @@ __global__ __launch_bounds__(kHeadThreads, 2) void weight_heads_kernel(WeightArg
     keys = next;
     slot = slot_next;
   }
-  if (!a.scan && __any(err) && lane == 0) atomicOr(a.status, kStatusRowsBit);
 }
 
-// The heads' sums, in order.
+// The heads' sums, in order; the last a.scan_parts of a sequence's workgroups look its pages over.
 __global__ __launch_bounds__(kThreads) void weight_sum_kernel(WeightArgs a) {
   const int seq = blockIdx.y, row = blockIdx.x * kThreads + threadIdx.x;
   int len, first, n;
   bool bad;
+  const int scan = (int)blockIdx.x - (int)(gridDim.x - a.scan_parts);
+  if (scan >= 0) return scan_sequence(a.b, a.q, seq, scan, a.scan_parts, a.status);
   if (!sequence_of(a.b, a.q, seq, &len, &first, &n, &bad) || row >= len) return;
   const int live = (n * a.group + kBlock - 1) / kBlock;    // blocks of query rows
   const float* p = a.part + (int64_t)seq * a.b.n_kv * a.mblocks * a.b.max_len + row;
@@ -366,7 +368,7 @@ void launch_weight_head(const WeightArgs& a, const WeightPlan& p, hipStream_t st
     hipLaunchKernelGGL((weight_rows_kernel<HD, 4>), grid, block, 0, stream, a);
   } else {
     hipLaunchKernelGGL((weight_heads_kernel<HD>), grid, dim3(kHeadThreads), 0, stream, a);
-    hipLaunchKernelGGL(weight_sum_kernel, dim3((a.b.max_len + kThreads - 1) / kThreads, a.b.batch),
+    hipLaunchKernelGGL(weight_sum_kernel, dim3((a.b.max_len + kThreads - 1) / kThreads + a.scan_parts, a.b.batch),
                        block, 0, stream, a);
   }
 }
@@ -399,8 +401,9 @@ hipError_t launch_weight(const Batch& b, const uint16_t* kp, const Queries& q, c
   a.splits = p.splits;
   a.mblocks = p.mblocks;
   a.group = p.group;
-  a.scan = scans(b) ? 1 : 0;
-  if (!a.scan) {
+  a.scan = p.mt && scans(b) ? 1 : 0;
+  a.scan_parts = scan_parts(b);
+  if (p.mt && !a.scan) {
     const hipError_t e = launch_clear_status(a.status, stream);
     if (e != hipSuccess) return e;
   }
