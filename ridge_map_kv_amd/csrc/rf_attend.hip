@@ -457,10 +457,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // WM = 4 the other four take the second half of a step's cache rows and are added at the end.
 // The rows of a step (64) are copied into LDS as they are, by direct loads that hold no
 // registers, two steps ahead of the products: four buffers, one barrier a step.  K^T's fragments
-// are 16-byte reads, V^T's are transposing reads (four rows of one feature a lane).  The 16-byte
-// pieces of a row lie in the order piece ^ (row % 8) for K, piece ^ 4 (row % 2) for V, which
-// spreads both kinds of read over all banks.  The pool slots of the workgroup's rows are looked
-// up beforehand: a table load between the direct loads would wait for those.
+// are 16-byte reads, V^T's are transposing reads (four rows of one feature a lane).  The pieces of
+// a row lie in another order in each of the rows that are read at a time (16 of K's 16 bytes, four
+// of V's 64), so that these come from all 64 banks: no conflicts, where turns of eight and two
+// rows gave as many cycles of them as of reads and 153 instead of 150 us for 65,536 rows.  The pool
+// slots of the workgroup's rows are looked up beforehand: a table load between the direct loads
+// would wait for those.
 // Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 147 us
 // with the join's 9, 395 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 147 us, 587 TFLOP/s.
 // What bounds it are the vector instructions, 1,700 cycles a wave and step of 64 rows, with two
@@ -514,6 +516,16 @@ __device__ __forceinline__ bf16x8 read_transposed(const unsigned char* p, int ap
   } pr = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)p),
           __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_byte*)(p + apart))};
   return __builtin_bit_cast(bf16x8, pr);
+}
+
+// How the pieces of an LDS row are turned: of K in 16 bytes, of V in 64.
+template <int HD>
+__device__ __forceinline__ int k_turn(int row) {
+  return HD == 128 ? row & 15 : row >> 1 & 7;
+}
+template <int HD>
+__device__ __forceinline__ int v_turn(int row) {
+  return HD == 128 ? row & 3 : row >> 1 & 1;
 }
 
 template <int HD, int WM, bool kOut>
@@ -582,8 +594,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
       const int block = wave * kLoads + i, row = block * kLoadRows + ln / kPieces;
       const int slot = sh_slot[step * kTileRows + row];
       const int64_t off = (int64_t)(slot < 0 ? 0 : slot) * row_size;
-      dma_row(kbase + off + (at ^ (row & 7)) * 8, lds_address(k_at(step)) + block * 1024);
-      if constexpr (kOut) dma_row(vbase + off + (at ^ (row & 1) << 2) * 8, lds_address(v_at(step)) + block * 1024);
+      dma_row(kbase + off + (at ^ k_turn<HD>(row)) * 8, lds_address(k_at(step)) + block * 1024);
+      if constexpr (kOut) dma_row(vbase + off + (at ^ v_turn<HD>(row) << 2) * 8, lds_address(v_at(step)) + block * 1024);
     }
   };
 
@@ -620,7 +632,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
       const int ln = fresh(lane);
       const unsigned char* row = k_at(step) + (32 * e0 + (ln & 31)) * kRowBytes;
       const auto fragment = [&](int i) {
-        return *reinterpret_cast<const bf16x8*>(row + i % kE * 32 * kRowBytes + (((2 * (i / kE) + (ln >> 5)) ^ (ln & 7)) << 4));
+        return *reinterpret_cast<const bf16x8*>(row + i % kE * 32 * kRowBytes + (((2 * (i / kE) + (ln >> 5)) ^ k_turn<HD>(ln & 31)) << 4));
       };
 #pragma unroll
       for (int e = 0; e < kE; ++e)
@@ -652,11 +664,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         }
       }
       // lane i of 16 reads row i / 4, features 4 (i % 4) .. and gets feature i of the four rows
-      const int i16 = ln & 15, odd = i16 >> 2 & 1;
+      const int i16 = ln & 15, turn = v_turn<HD>(i16 >> 2);
       const unsigned char* vs = v_at(step) + 32 * e0 * kRowBytes;
       const unsigned char* v = vs + (4 * (ln >> 5) + (i16 >> 2)) * kRowBytes + ((ln >> 4 & 1) * 2 + (i16 >> 1 & 1)) * 16 + 8 * (i16 & 1);
       const auto fragment = [&](int i) {
-        return read_transposed(v + i / kF * 16 * kRowBytes + 64 * (i % kF ^ odd), 8 * kRowBytes);
+        return read_transposed(v + i / kF * 16 * kRowBytes + 64 * (i % kF ^ turn), 8 * kRowBytes);
       };
       bf16x8 vf[4];
       if constexpr (kOut) {
