@@ -474,9 +474,10 @@ constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;
 constexpr int kSlots = 4096;          // cache rows whose slots are looked up at a time
 
-// 16 bytes per lane from p to the LDS address lds + 16 lane (lds: the same in the wave).  The
+// 16 bytes per lane from base + off (bytes) to the LDS address lds + 16 lane (lds: the same in the wave).  The
 // compiler does not see the load: dma_wait before the barrier that hands the data on.
-__device__ __forceinline__ void dma_row(const uint16_t* p, uint32_t lds) {
+__device__ __forceinline__ void dma_row(const uint16_t* base, uint64_t off, uint32_t lds) {
+  const unsigned char* p = reinterpret_cast<const unsigned char*>(base) + off;
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
@@ -520,11 +521,11 @@ __device__ __forceinline__ bf16x8 read_transposed(const unsigned char* p, int ap
 
 // How the pieces of an LDS row are turned: of K in 16 bytes, of V in 64.
 template <int HD>
-__device__ __forceinline__ int k_turn(int row) {
+__device__ __forceinline__ unsigned k_turn(unsigned row) {
   return HD == 128 ? row & 15 : row >> 1 & 7;
 }
 template <int HD>
-__device__ __forceinline__ int v_turn(int row) {
+__device__ __forceinline__ unsigned v_turn(unsigned row) {
   return HD == 128 ? row & 3 : row >> 1 & 1;
 }
 
@@ -586,19 +587,23 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 
   const int32_t* table = a.b.tables + (int64_t)seq * a.b.table_stride;
   const int64_t row_size = (int64_t)a.b.n_kv * HD;
+  const unsigned row_bytes = 2u * a.b.n_kv * HD;
   const uint16_t* kbase = a.kp + kh * HD;
   const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
   const auto k_at = [&](int step) { return sh_kv + step % kBufs * kBufBytes; };
   const auto v_at = [&](int step) { return sh_kv + (kBufs + step % kBufs) * kBufBytes; };
   const auto load = [&](int step) {
-    const int ln = fresh(lane), at = ln % kPieces;        // where the lane's piece goes
+    const unsigned ln = fresh(lane), at = ln % kPieces;   // where the lane's piece goes
+    int slot[kLoads];                                     // together: no load waits between two of them
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      slot[i] = sh_slot[step * kTileRows + (wave * kLoads + i) * kLoadRows + ln / kPieces];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int block = wave * kLoads + i, row = block * kLoadRows + ln / kPieces;
-      const int slot = sh_slot[step * kTileRows + row];
-      const int64_t off = (int64_t)(slot < 0 ? 0 : slot) * row_size;
-      dma_row(kbase + off + (at ^ k_turn<HD>(row)) * 8, lds_address(k_at(step)) + block * 1024);
-      if constexpr (kOut) dma_row(vbase + off + (at ^ v_turn<HD>(row) << 2) * 8, lds_address(v_at(step)) + block * 1024);
+      const unsigned block = wave * kLoads + i, row = block * kLoadRows + ln / kPieces;
+      const uint64_t off = (uint64_t)(unsigned)(slot[i] < 0 ? 0 : slot[i]) * row_bytes;
+      dma_row(kbase + (at ^ k_turn<HD>(row)) * 8, off, lds_address(k_at(step)) + block * 1024);
+      if constexpr (kOut) dma_row(vbase + (at ^ v_turn<HD>(row) << 2) * 8, off, lds_address(v_at(step)) + block * 1024);
     }
   };
 
@@ -667,7 +672,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         }
       }
       // lane i of 16 reads row i / 4, features 4 (i % 4) .. and gets feature i of the four rows
-      const int i16 = ln & 15, turn = v_turn<HD>(i16 >> 2);
+      const int i16 = ln & 15, turn = (int)v_turn<HD>(i16 >> 2);
       const unsigned char* vs = v_at(step) + 32 * e0 * kRowBytes;
       const unsigned char* v = vs + (4 * (ln >> 5) + (i16 >> 2)) * kRowBytes + ((ln >> 4 & 1) * 2 + (i16 >> 1 & 1)) * 16 + 8 * (i16 & 1);
       const auto fragment = [&](int i) {
