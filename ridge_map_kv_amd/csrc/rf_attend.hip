@@ -463,12 +463,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // rows gave as many cycles of them as of reads and 153 instead of 150 us for 65,536 rows.  The pool
 // slots of the workgroup's rows are looked up beforehand: a table load between the direct loads
 // would wait for those.
-// Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 147 us
-// with the join's 9, 395 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 147 us, 587 TFLOP/s.
-// What bounds it are the vector instructions, 1,700 cycles a wave and step of 64 rows, with two
+// Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 139 us
+// with the join's 9, 416 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 140 us, 614 TFLOP/s.
+// What bounds it are the vector instructions, 1,600 cycles a wave and step of 64 rows, with two
 // waves to a SIMD (exponentials 512 of them), at a clock that 256 busy query rows pull down to
-// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  Blocks of 128 rows took 248, two workgroups
-// for each compute unit 203 us.
+// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  When it took 147 us,  blocks of 128 rows
+// (another way of loading) took 248 and two workgroups for each compute unit 203.
 constexpr int kTileRows = 64;
 constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;
