@@ -467,8 +467,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // with the join's 9, 416 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 140 us, 614 TFLOP/s.
 // What bounds it are the vector instructions, 1,600 cycles a wave and step of 64 rows, with two
 // waves to a SIMD (exponentials 512 of them), at a clock that 256 busy query rows pull down to
-// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  When it took 147 us,  blocks of 128 rows
-// (another way of loading) took 248 and two workgroups for each compute unit 203.
+// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  Blocks of 128
+// query rows that loaded through registers took 248 us, two workgroups for each compute unit 203.
 constexpr int kTileRows = 64;
 constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;
