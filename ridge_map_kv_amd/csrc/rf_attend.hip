@@ -60,6 +60,25 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t lo, uint32_t hi, int half
   return __builtin_amdgcn_perm(hi, lo, half ? 0x07060302u : 0x05040100u);
 }
 
+// Two weights, e^(s - max), as operands of the product with V: the leading eight bits of each, cut
+// off, and what these leave, in bf16 too, so that the products add up to weights within 2^-15.  One
+// bf16 a weight put the outputs as far off (0.0011 of them) as their own rounding does (0.0017), and
+// more than the scores and sums in fp32 do.  The second products cost nothing where the read of the
+// cache is the bound (16 sequences of up to 16,384 rows, one token: 200 us before and after, caches
+// cold), 11 and 26% where the matrix cores are (162 -> 180 us for trees of 48 on 4 sequences of up to
+// 32,768 rows, 143 -> 180 for one of 64 over 65,536).
+// The rest is taken from the weight times 1 + 2^-23: it is above 0 wherever the weight is, so that an
+// infinite value, which both products take, stays what it is (0 or a rest below 0 would make it NaN).
+struct Weights {
+  uint32_t lead, rest;
+};
+__device__ __forceinline__ Weights split_weights(float a, float b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  constexpr float kUp = 1.f + 0x1p-23f;
+  return {half_pair(x, y, 1), pack_bf16x2(fmaf(a, kUp, -__uint_as_float(x & 0xffff0000u)),
+                                          fmaf(b, kUp, -__uint_as_float(y & 0xffff0000u)))};
+}
+
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -351,13 +370,18 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     }
     l_run += sum;
     if constexpr (kOut) {
-      u32x4 pw;
+      u32x4 pw[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pw[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        const Weights w = split_weights(p[2 * i], p[2 * i + 1]);
+        pw[0][i] = w.lead;
+        pw[1][i] = w.rest;
+      }
       if (!wild) {
-        const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
 #pragma unroll
-        for (int f = 0; f < kFeat; ++f) o[f] = mfma16(vf[f], pf, o[f]);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int f = 0; f < kFeat; ++f) o[f] = mfma16(vf[f], __builtin_bit_cast(bf16x8, pw[k]), o[f]);
       } else {
         // Some value is infinite or NaN, and 0 times it is not 0: row by row, added only
         // for the queries that see the row.
@@ -365,17 +389,20 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
           const int rg = r % 16 / 4, j = r / 16 * 4 + r % 4;
           const bool vis = __shfl(seen, 16 * rg + c) >> r & 1;
           const uint32_t keep = j & 1 ? 0xffff0000u : 0x0000ffffu;
-          u32x4 pr;
+          u32x4 pr[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pr[i] = g == rg && i == j / 2 ? pw[i] & keep : 0u;
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pr[k][i] = g == rg && i == j / 2 ? pw[k][i] & keep : 0u;
 #pragma unroll
           for (int f = 0; f < kFeat; ++f) {
             const u32x4 vw = __builtin_bit_cast(u32x4, vf[f]);
             u32x4 vr;
 #pragma unroll
             for (int i = 0; i < 4; ++i) vr[i] = g == rg && i == j / 2 ? vw[i] & keep : 0u;
-            const f32x4 add = mfma16(__builtin_bit_cast(bf16x8, vr), __builtin_bit_cast(bf16x8, pr),
-                                     f32x4{0.f, 0.f, 0.f, 0.f});
+            f32x4 add = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) add = mfma16(__builtin_bit_cast(bf16x8, vr), __builtin_bit_cast(bf16x8, pr[k]), add);
             if (vis) o[f] += add;
           }
         }
@@ -702,12 +729,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         m_run = m_new;
       }
       const float zero = m_run == -INFINITY ? 0.f : m_run;
-      // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, packed
-      const auto pair = [&](int x, int i) -> uint32_t {
+      // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, as operands
+      const auto pair = [&](int x, int i) -> Weights {
         const float p0 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i], scale2, -zero));
         const float p1 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i + 1], scale2, -zero));
         l_run += p0 + p1;
-        return pack_bf16x2(p0, p1);
+        return split_weights(p0, p1);
       };
       if constexpr (!kOut) {
 #pragma unroll
@@ -715,23 +742,26 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 #pragma unroll
           for (int i = 0; i < 4; ++i) pair(x, i);
       } else {
-        u32x4 now, next = {0u, 0u, 0u, 0u};
+        u32x4 now[2], next[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+        const auto weigh = [&](int x, int i, u32x4 (&to)[2]) {
+          const Weights w = pair(x, i);
+          to[0][i] = w.lead;
+          to[1][i] = w.rest;
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) now[i] = pair(0, i);
+        for (int i = 0; i < 4; ++i) weigh(0, i, now);
 #pragma unroll
         for (int x = 0; x < 2 * kE; ++x) {
 #pragma unroll
-          for (int f = 0; f < kF; ++f) {
-            const int i = x * kF + f;
+          for (int u = 0; u < 2 * kF; ++u) {                // all features with the leading bits, then the rest
+            const int f = u % kF, i = x * kF + f;
             __builtin_amdgcn_sched_barrier(0);
-            o[f] = mfma32(vf[i % 4], __builtin_bit_cast(bf16x8, now), o[f]);
-            if (i + 4 < 2 * kE * kF) vf[i % 4] = fragment(i + 4);
-            if (x + 1 < 2 * kE) {
-#pragma unroll
-              for (int j = f * (4 / kF); j < (f + 1) * (4 / kF); ++j) next[j] = pair(x + 1, j);
-            }
+            o[f] = mfma32(vf[i % 4], __builtin_bit_cast(bf16x8, now[u / kF]), o[f]);
+            if (u >= kF && i + 4 < 2 * kE * kF) vf[i % 4] = fragment(i + 4);
+            if (x + 1 < 2 * kE && u % (kF / 2) == 0) weigh(x + 1, u / (kF / 2), next);
           }
-          now = next;
+          now[0] = next[0];
+          now[1] = next[1];
         }
         __builtin_amdgcn_sched_barrier(0);
       }

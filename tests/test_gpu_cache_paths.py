@@ -1,0 +1,60 @@
+"""GPU tests of the cache calls by kernel: each of the attention's forms (up to 16, up to 128, up
+to 256 query rows of a key head, whole or split caches) and of the weight's, at what they could
+get wrong."""
+
+import copy
+
+import pytest
+import torch
+
+import cachecase as R
+from test_gpu_cache import _attend, _case, _close
+
+from ridge_map_kv_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+# lens, counts, heads, n_kv, hd, page, tree: query rows of a key head, and whether the cache is split
+FORMS = {
+    "16 rows, whole": ([40, 21, 1], [1, 4, 1], 8, 2, 128, 16, False),
+    "16 rows, split": ([700, 90], [8, 3], 4, 2, 64, 5, True),
+    "128 rows, whole": ([45, 80], [20, 7], 4, 1, 64, 4, True),
+    "128 rows, split": ([150, 129], [30, 64], 4, 2, 128, 16, True),
+    "256 rows, whole": ([64, 70, 100], [64, 11, 40], 16, 4, 128, 16, True),
+    "256 rows, split": ([300, 6], [64, 6], 3, 1, 64, 100, False),
+    "320 rows, split": ([200], [64], 10, 2, 128, 12, True),
+}
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_weights_of_the_values_keep_15_bits(form):
+    # the product with V takes each weight as two bf16 operands: an eighth bit cut off leaves less than
+    # 2^-7 of it, which loses at most half a step of bf16, 2^-8 of itself
+    lens, counts, heads, n_kv, hd, page, tree = FORMS[form]
+    cache, q, starts, words, max_q = _case(lens, counts, heads, n_kv, hd, page, seed=31, tree=tree)
+    out, _, st = _attend(cache, q, starts, words, max_q, hd ** -0.5)
+    assert st == B.RF_OK
+    want, _, tol, _ = R.attention(cache, q, starts, words, hd ** -0.5)
+    size = copy.copy(cache)                               # sums of the weights times |v|
+    size.v = [cache.v[0].abs()]
+    size = R.attention(size, q, starts, words, hd ** -0.5)[0]
+    _close(out, want, tol - size * (R.U_BF16 - 2.0 ** -15), form)
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.1])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_value_that_all_see(form, scale):
+    # with a scale of 0 all weights are 1, which one bf16 operand holds whole
+    lens, counts, heads, n_kv, hd, page, tree = FORMS[form]
+    lens = [n + 64 for n in lens]                         # its step has no drafts
+    cache, q, starts, words, max_q = _case(lens, counts, heads, n_kv, hd, page, seed=32, tree=tree)
+    for b in range(len(lens)):
+        cache.v[0][int(cache.table_np[b, 3 // page]), 3 % page, :, 5] = float("inf")
+        cache.v[0][int(cache.table_np[b, 1 // page]), 1 % page, :, 9] = -float("inf")
+    out, _, st = _attend(cache, q, starts, words, max_q, scale)
+    assert st == B.RF_OK
+    assert (out[..., 5] == float("inf")).all() and (out[..., 9] == -float("inf")).all()
+    rest = torch.ones(hd, dtype=torch.bool)
+    rest[[5, 9]] = False
+    assert torch.isfinite(out[..., rest.to(DEV)]).all()
