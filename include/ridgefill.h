@@ -625,7 +625,8 @@ rf_status ridgefill_attention_weight(const rf_paged_batch* kv, const uint16_t* k
  *   stride        >= max_len
  *   n_keep, n_sink, n_recent >= 0
  *   ws            >= ridgefill_evict_workspace_bytes(kv, n_keep), 256-byte aligned; its first
- *                 256 bytes hold the status.  A moving row on a bad page is not moved.
+ *                 256 bytes hold the status.  A row that would move from or to a bad page is
+ *                 lost: the place it would take keeps its own row, weight and position.
  * The cut off pages stay in the block table; their rows are free for new ones.  Sequences of
  * one call must not share pages that the cut writes.
  * ------------------------------------------------------------------------------ */

@@ -355,9 +355,12 @@ __global__ __launch_bounds__(256) void evict_move_kernel(EvictPools pools, Batch
     bool bad = false;
     for (int64_t i = first; i < h.moves; i += step) {
       const MoveRow r = list[i];
+      if (slot_of(r.from) < 0 || slot_of(r.to) < 0) {     // no pool moves it: the place keeps its own
+        bad = true;
+        continue;
+      }
       acc_out[r.to] = r.weight;
       pos_out[r.to] = r.pos;
-      bad |= slot_of(r.from) < 0 || slot_of(r.to) < 0;
     }
     for (int64_t t = c.n_keep + first; t < h.old_len; t += step) acc_out[t] = 0.f;
     const unsigned bits = (blockIdx.x == 0 ? (unsigned)h.err : 0u) | (__any(bad) ? kStatusRowsBit : 0u);

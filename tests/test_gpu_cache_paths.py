@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import cachecase as R
-from test_gpu_cache import _attend, _case, _close
+from test_gpu_cache import _attend, _case, _close, _evict
 
 from ridge_map_kv_amd import binding as B
 
@@ -58,3 +58,31 @@ def test_infinite_value_that_all_see(form, scale):
     rest = torch.ones(hd, dtype=torch.bool)
     rest[[5, 9]] = False
     assert torch.isfinite(out[..., rest.to(DEV)]).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("page", [4, 0])
+def test_evict_rows_on_bad_pages_keep_their_places(in_place, page):
+    # page 4 of 5 holds sources of moves (rows 32 .. 39), page 0 destinations (rows 0 .. 7)
+    lens, keep = [40, 40], 20
+    cache = R.Cache(lens, 1, 64, 8, seed=4)
+    acc = torch.rand(2, 40, generator=torch.Generator().manual_seed(0))
+    pos = torch.stack([torch.randperm(40, generator=torch.Generator().manual_seed(b)) for b in (1, 2)]).to(torch.int32)
+    old = [p.clone() for p in (cache.k[0], cache.v[0])]
+    cache.table[0, page] = cache.num_pages
+    ao, po, lo, st = _evict(cache, acc, pos, keep, 0, 0, in_place)
+    assert st == B.RF_E_ROWS and lo.tolist() == [keep, keep]
+    moves, _ = R.evict(lens, acc.numpy(), pos.numpy(), keep, 0, 0)
+    lost = [m for m in moves[0] if page in (m[0] // 8, m[1] // 8)]
+    assert lost and len(lost) < len(moves[0])
+    for b in range(2):
+        holds = list(range(keep))
+        for f, t in moves[b]:
+            if b or (f, t) not in lost:
+                holds[t] = f
+        assert torch.equal(ao[b, :keep], acc[b, holds]) and torch.equal(po[b, :keep], pos[b, holds])
+        assert (ao[b, keep:] == 0).all()
+        for pool, was in zip((cache.k[0], cache.v[0]), old):     # what every place holds is what it says
+            was = cache.rows(was, b)[holds]
+            there = [t for t in range(keep) if b or t // 8 != page]
+            assert torch.equal(cache.rows(pool, b, keep)[there], was[there])
