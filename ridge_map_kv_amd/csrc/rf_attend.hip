@@ -23,6 +23,7 @@
 // ahead.  A workgroup's four waves take the 32-row tiles of its row range in turn and are joined
 // in LDS; long caches are split over workgroups, whose partial results (fp32) a second kernel joins.
 #include "rf_cache_dev.h"
+#include "rf_split.h"
 
 namespace rf {
 
@@ -44,6 +45,7 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   unsigned* status;
+  unsigned* each;               // grains of a part, from the first launch to the join
   float* part_o;                // [parts][n_kv][max_q G][hd]
   float2* part_ml;              // [parts][n_kv][max_q G]: running maximum (log2), sum
   int64_t out_stride;
@@ -93,8 +95,10 @@ __device__ __forceinline__ int fresh(int v) {
 
 // Long caches are split into parts of about equal length over all sequences, `goal` of them at
 // most: with one workgroup to a compute unit one part too many costs a second round (trees on 4
-// sequences, 35 parts of 8 heads instead of 32: 239 instead of 149 us).  The lengths are known only
-// here, so each wave works the split out for itself.
+// sequences, 35 parts of 8 heads instead of 32: 239 instead of 149 us; one of 64 tokens over 32,768
+// rows, 5 key heads, 52 parts instead of 51: 74 instead of 62).  The lengths are known only here, so
+// each wave works the split out for itself, and the join takes it from the workspace (worked out for
+// each row there too: 290 instead of 273 us for trees on 24 sequences).
 constexpr int kGrain = 64;              // parts are multiples of this many rows
 
 // One sequence of a batch as a lane looks it up; grains 0: it is skipped.
@@ -111,22 +115,18 @@ __device__ __forceinline__ Seq look_up(const AttendArgs& a, int b) {
 // Grains of one part; `mine`: sequence lane.
 __device__ int grains_of_part(const AttendArgs& a, const Seq& mine) {
   const int lane = threadIdx.x & 63;
+  const auto sum = [](auto v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+  };
   long long total = mine.grains;
   for (int b = 64 + lane; b < a.b.batch; b += 64) total += look_up(a, b).grains;
-#pragma unroll
-  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-  constexpr int64_t kMost = (1 << 30) / kGrain;         // of the longest sequence
-  int each = (int)min((total + a.goal - 1) / a.goal, (long long)kMost);
-  if (each < a.least / kGrain) each = a.least / kGrain;
-  for (int tries = 0; tries < 4; ++tries) {
+  return part_grains(sum(total), a.b.batch, a.goal, a.least / kGrain, [&](int each) {
     int parts = (mine.grains + each - 1) / each;
     for (int b = 64 + lane; b < a.b.batch; b += 64) parts += (look_up(a, b).grains + each - 1) / each;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) parts += __shfl_xor(parts, d);
-    if (parts <= a.goal) break;
-    each = (int)min(each + ((int64_t)each * (parts - a.goal) + a.goal - 1) / a.goal, kMost);
-  }
-  return each;
+    return sum(parts);
+  });
 }
 
 // What a workgroup computes: rows [begin, end) of a sequence, for one key head.
@@ -150,7 +150,10 @@ __device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
   }
   Seq s = look_up(a, lane);
   const int each = grains_of_part(a, s);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;      // the join adds what is wrong
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.status = 0u;                     // the join adds what is wrong
+    *a.each = each;
+  }
   int before = 0;                       // parts of the sequences before these 64
   for (int b0 = 0; b0 < a.b.batch; b0 += 64) {
     if (b0) s = look_up(a, b0 + lane);
@@ -919,7 +922,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
   const Seq mine = look_up(a, lane), self = look_up(a, seq);
   const int n = self.n, first = self.first;
   if (!self.grains || m >= n * a.group) return;
-  const int each = grains_of_part(a, mine), parts = (self.grains + each - 1) / each;
+  const int each = (int)*a.each, parts = (self.grains + each - 1) / each;
   if (parts == 1) return;                           // written by its workgroup
   int before = lane < seq ? (mine.grains + each - 1) / each : 0;
   for (int b = 64 + lane; b < seq; b += 64) before += (look_up(a, b).grains + each - 1) / each;
@@ -1010,10 +1013,10 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q) {
   // enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS
   const int per_part = b.n_kv * p.mblocks, want = p.rows == 16 ? 1024 : 256;
   p.least = p.rows == 16 ? 256 : 128;
-  p.goal = (want + per_part - 1) / per_part;
+  p.goal = parts_goal(want, per_part);
   if (p.goal <= b.batch || b.max_len <= p.least) p.goal = 0;
   const int64_t most = (int64_t)b.batch * ((b.max_len + p.least - 1) / p.least);
-  p.parts = p.goal == 0 ? b.batch : most < p.goal + b.batch ? (int)most : p.goal + b.batch;
+  p.parts = p.goal == 0 ? b.batch : most < p.goal ? (int)most : p.goal;
   const size_t held = p.goal ? (size_t)p.parts * b.n_kv * rows : 0;
   p.ml = kStatusBytes;
   p.o = p.ml + align256(held * sizeof(float2));
@@ -1066,6 +1069,7 @@ hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp,
   a.out = out;
   a.lse = lse;
   a.status = reinterpret_cast<unsigned*>(w);
+  a.each = a.status + 1;
   a.part_ml = reinterpret_cast<float2*>(w + p.ml);
   a.part_o = reinterpret_cast<float*>(w + p.o);
   a.out_stride = out_stride;
