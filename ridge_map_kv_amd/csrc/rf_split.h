@@ -36,4 +36,20 @@ constexpr int part_grains(int64_t total, int batch, int goal, int least, Count p
   return hi;
 }
 
+// Rows of a workgroup where `units` axes of `rows` rows are split over workgroups that each want a
+// compute unit (of kUnitsOfChip), in multiples of `step` rows: as many as fit into one round or, if those of
+// a second round are so much shorter that both are over sooner, as many as leave no compute unit out.
+constexpr int kUnitsOfChip = 256;
+constexpr int chunk_rows(int64_t units, int rows, int step) {
+  const auto chunk = [&](int64_t splits) {
+    const int64_t each = splits > 1 ? (rows + splits - 1) / splits : rows;
+    return (each + step - 1) / step * step;
+  };
+  const auto time = [&](int64_t each) {
+    return (units * ((rows + each - 1) / each) + kUnitsOfChip - 1) / kUnitsOfChip * each;
+  };
+  const int64_t few = chunk(kUnitsOfChip / units), many = chunk((kUnitsOfChip + units - 1) / units);
+  return (int)(time(many) < time(few) ? many : few);
+}
+
 }  // namespace rf

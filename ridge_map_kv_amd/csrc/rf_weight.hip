@@ -19,6 +19,7 @@
 // us, 35 in one call after another, 485 TFLOP/s; the exponentials alone are 12 us (24 cycles with
 // their addition), staging Q 7.
 #include "rf_cache_dev.h"
+#include "rf_split.h"
 
 namespace rf {
 
@@ -345,12 +346,10 @@ WeightPlan weight_plan(const Batch& b, int n_heads, int max_q) {
   }
   p.mt = 0;
   p.mblocks = (rows + kBlock - 1) / kBlock;
-  // one workgroup to a compute unit, each of at least one step of its waves
+  // one workgroup to a compute unit, each of at least one step of its waves (rounded up whatever the
+  // rounds, 64 queries of 3 sequences of 32,768 rows took 133 us in 264 workgroups, 97 in 240; 6: 219, 155)
   const int64_t units = (int64_t)b.batch * b.n_kv * p.mblocks;
-  int64_t s = (256 + units - 1) / units;
-  const int step = kHeadWaves * kRows, most = (b.max_len + step - 1) / step;
-  if (s > most) s = most;
-  p.chunk = (int)((((int64_t)b.max_len + s - 1) / s + step - 1) / step * step);
+  p.chunk = chunk_rows(units, b.max_len, kHeadWaves * kRows);
   p.splits = (b.max_len + p.chunk - 1) / p.chunk;
   p.total = p.part + align256((size_t)units * b.max_len * sizeof(float));
   return p;

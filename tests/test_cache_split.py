@@ -52,6 +52,31 @@ int main() {
 }
 """
 
+# the chunk of every number of axes, and of random lengths: covers the rows in whole steps, and no more
+# rounds of workgroups times rows than the two numbers of parts that it chooses from
+CHUNKS = r"""
+#include "rf_split.h"
+#include <initializer_list>
+#include <stdio.h>
+
+int main() {
+  const int step = 512;
+  for (int units = 1; units < 1000; ++units)
+    for (int rows = 1; rows < 70000; rows = rows * 5 / 4 + 1) {
+      const int64_t each = rf::chunk_rows(units, rows, step);
+      if (each < 1 || each % step) return 1;
+      const auto rounds = [&](int64_t chunk) { return (units * ((rows + chunk - 1) / chunk) + 255) / 256; };
+      for (int64_t s : {256 / units, (256 + units - 1) / units}) {
+        if (s < 1) s = 1;
+        const int64_t other = ((rows + s - 1) / s + step - 1) / step * step;
+        if (rounds(each) * each > rounds(other) * other) return 2;
+      }
+    }
+  for (int batch : {3, 5, 6, 9, 12}) printf("%d ", rf::chunk_rows(8 * batch, 32768, step));
+  return 0;
+}
+"""
+
 
 def _run(tmp_path, source):
     gxx = shutil.which("g++")
@@ -78,3 +103,10 @@ def test_attention_fits_one_round_of_workgroups(heads, n_kv, max_q):
     parts = (size - 256) // (n_kv * rows * (8 + 4 * hd))
     want, block = (1024, 16) if rows <= 16 else (256, 128) if rows <= 128 else (256, 256)
     assert want * 3 // 4 < parts * n_kv * -(-rows // block) <= want
+
+
+def test_weight_chunks_leave_no_stragglers(tmp_path):
+    # 8 key heads, 32,768 rows: workgroups of all batches fit 256 compute units
+    chunks = [int(x) for x in _run(tmp_path, CHUNKS)]
+    for batch, chunk in zip((3, 5, 6, 9, 12), chunks):
+        assert 8 * batch * -(-32768 // chunk) <= 256
