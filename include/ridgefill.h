@@ -569,7 +569,8 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
  *   ws          >= ridgefill_tree_attention_workspace_bytes(kv, n_q_heads, max_q), 256-byte
  *               aligned; its first 256 bytes hold the status
  * Scores, maxima, sums and outputs are held in fp32; for the product with v exp(s - max) is two
- * bf16 operands of the matrix cores, which hold it to 2^-15; out is rounded once at the end.  The same call on the
+ * bf16 operands of the matrix cores, which hold it to 2^-15; out is rounded once at the end
+ * (a workgroup's sums of equal weights are exact up to 2^28 rows).  The same call on the
  * same inputs gives the same bits; a row's bits may differ between calls whose sequences have
  * other lengths, since long caches are split evenly over the batch.  Size query: 0 on invalid
  * input.

@@ -732,11 +732,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         m_run = m_new;
       }
       const float zero = m_run == -INFINITY ? 0.f : m_run;
-      // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, as operands
+      // exponentials of values 2 i and 2 i + 1 of the sixteen rows x, as operands; their sum is added once
+      // a step (equal scores, added by twos, stood still at 2^25 in a lane: 2^26 rows of one workgroup)
+      float sum = 0.f;
       const auto pair = [&](int x, int i) -> Weights {
         const float p0 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i], scale2, -zero));
         const float p1 = __builtin_amdgcn_exp2f(fmaf(s[x / 2][x % 2 * 8 + 2 * i + 1], scale2, -zero));
-        l_run += p0 + p1;
+        sum += p0 + p1;
         return split_weights(p0, p1);
       };
       if constexpr (!kOut) {
@@ -768,6 +770,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      l_run += sum;
     };
 
 #pragma unroll

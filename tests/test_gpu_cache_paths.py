@@ -3,6 +3,7 @@ to 256 query rows of a key head, whole or split caches) and of the weight's, at 
 get wrong."""
 
 import copy
+import math
 
 import pytest
 import torch
@@ -86,3 +87,25 @@ def test_evict_rows_on_bad_pages_keep_their_places(in_place, page):
             was = cache.rows(was, b)[holds]
             there = [t for t in range(keep) if b or t // 8 != page]
             assert torch.equal(cache.rows(pool, b, keep)[there], was[there])
+
+
+def test_sums_of_a_long_cache_in_one_workgroup():
+    # as many sequences as parts are wanted: each is one workgroup's for each key head.  Equal scores have
+    # weights of 1, 48 million for each of a query's two lanes, and values of 1 have means of 1
+    page, times, n_kv, batch = 2 ** 16, 3 * 2 ** 9, 8, 32
+    rows = page * times
+    pool = torch.ones(1, page, n_kv, 64, dtype=torch.bfloat16, device=DEV)
+    lengths = torch.zeros(batch, dtype=torch.int32, device=DEV)
+    lengths[0] = rows
+    kv = B.make_batch(torch.zeros(batch, times, dtype=torch.int32, device=DEV), lengths, page, 1, n_kv, 64)
+    q = torch.ones(34, 4 * n_kv, 64, dtype=torch.bfloat16, device=DEV)
+    start = torch.tensor([0] + [34] * batch, dtype=torch.int32, device=DEV)
+    ws = torch.empty(B.ridgefill_tree_attention_workspace_bytes(kv, 4 * n_kv, 34), dtype=torch.uint8, device=DEV)
+    assert ws.numel() == 256                              # no parts to join
+    out, lse = torch.empty_like(q), torch.empty(34, 4 * n_kv, device=DEV)
+    B.ridgefill_tree_attention(kv, pool, pool, q, start, 34, 0.0, out, ws, lse=lse)
+    assert B.ridgefill_read_status(ws) == B.RF_OK
+    # chains of a step's sums of 32 and of products of 16 rows are whole numbers below 2^29: exact
+    want = torch.tensor([math.log(rows - 33 + i) for i in range(34)], dtype=torch.float64)[:, None]
+    assert float((lse.cpu().double() - want).abs().max()) <= 8 * R.U_FP32 * math.log(rows)
+    assert float((out.float() - 1).abs().max()) <= R.U_BF16
