@@ -368,6 +368,20 @@ def _flat(name: str, t, dtype, device, ndim: int, shape: tuple | None = None) ->
                      f", not {tuple(t.shape)} with strides {t.stride()}")
 
 
+def _fits(*values: int) -> bool:
+    """Whether integers are what the C side will get: ctypes cuts off what is past 32 bits."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            return False
+    return True
+
+
+def _ints(**values: int) -> None:
+    for name, v in values.items():
+        if not _fits(v):
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def _rows_of(name: str, t, dtype, device, width: int, n: int | None = None) -> int:
     """Elements between the rows of [rows][heads][head_dim]; each row lies in one piece."""
     shape, stride = t.shape, t.stride()
@@ -402,6 +416,7 @@ def _go(f, device, stream, *args) -> None:
 def make_rope(theta: float = 500000.0, rotary_dim: int = 0, layout: int = RF_ROPE_HALF,
               scaling: int = RF_ROPE_PLAIN, factor: float = 1.0, orig_len: int = 0,
               low: float = 0.0, high: float = 0.0, mscale: float = 0.0) -> rf_rope:
+    _ints(rotary_dim=rotary_dim, layout=layout, scaling=scaling, orig_len=orig_len)
     return rf_rope(theta, rotary_dim, layout, scaling, orig_len, factor, low, high, mscale)
 
 
@@ -418,10 +433,13 @@ def make_batch(block_tables, lengths, page_size: int, num_pages: int, n_kv_heads
         raise ValueError("the entries of a block table must lie in one piece")
     if lengths is not None:
         _flat("lengths", lengths, torch.int32, dev, 1, (batch,))
+    if max_len is None:
+        max_len = per * page_size
+    _ints(max_len=max_len, page_size=page_size, num_pages=num_pages, n_kv_heads=n_kv_heads,
+          head_dim=head_dim)
     kv = rf_paged_batch(block_tables.data_ptr(), _ptr(lengths),
-                        block_tables.stride(0) if batch > 1 else per, batch,
-                        per * page_size if max_len is None else max_len, page_size, num_pages,
-                        n_kv_heads, head_dim)
+                        block_tables.stride(0) if batch > 1 else per, batch, max_len, page_size,
+                        num_pages, n_kv_heads, head_dim)
     if per * page_size < kv.max_len:
         raise ValueError(f"a block table of {per} pages holds fewer than max_len = {kv.max_len} rows")
     kv._keep = (block_tables, lengths)
@@ -493,13 +511,15 @@ def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, 
 
 
 def ridgefill_tree_attention_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int) -> int:
-    return int(lib().ridgefill_tree_attention_workspace_bytes(C.byref(kv), n_q_heads, max_q))
+    return int(lib().ridgefill_tree_attention_workspace_bytes(C.byref(kv), n_q_heads, max_q)) if _fits(n_q_heads, max_q) else 0
 
 
-def _queries(kv: rf_paged_batch, k_pages, q, q_start, tree_mask, lse, ws) -> int:
+def _queries(kv: rf_paged_batch, k_pages, q, q_start, max_q, tree_mask, lse, ws) -> int:
     """Checks shared by the attention and the weight accumulation; q's row stride."""
     import torch
     dev = kv._device
+    if not _fits(max_q):
+        raise ValueError(f"max_q = {max_q} does not fit 32 bits")
     if kv._keep[1] is None:
         raise ValueError("the batch was made without lengths")
     stride = _rows_of("q", q, torch.bfloat16, dev, kv.head_dim)
@@ -521,7 +541,7 @@ def ridgefill_tree_attention(kv: rf_paged_batch, k_pages, v_pages, q, q_start, m
     cache.  q_start int32 [batch + 1]; tree_mask int64 [n] (bit j: sees draft j) or None (a
     chain); out bf16 like q or None; lse fp32 [n][heads] or None."""
     import torch
-    qs = _queries(kv, k_pages, q, q_start, tree_mask, lse, ws)
+    qs = _queries(kv, k_pages, q, q_start, max_q, tree_mask, lse, ws)
     os_ = 0
     if out is not None:
         _flat("v_pages", v_pages, torch.bfloat16, kv._device, 4, kv._pool)
@@ -534,7 +554,7 @@ def ridgefill_tree_attention(kv: rf_paged_batch, k_pages, v_pages, q, q_start, m
 
 
 def ridgefill_attention_weight_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int) -> int:
-    return int(lib().ridgefill_attention_weight_workspace_bytes(C.byref(kv), n_q_heads, max_q))
+    return int(lib().ridgefill_attention_weight_workspace_bytes(C.byref(kv), n_q_heads, max_q)) if _fits(n_q_heads, max_q) else 0
 
 
 def ridgefill_attention_weight(kv: rf_paged_batch, k_pages, q, q_start, max_q: int, scale: float,
@@ -543,7 +563,7 @@ def ridgefill_attention_weight(kv: rf_paged_batch, k_pages, q, q_start, max_q: i
     """acc_out (fp32 [batch][>= max_len]) = decay * acc + the weight that q's queries, with
     their lse, give to each cached row; acc=None where nothing is accumulated yet."""
     import torch
-    qs = _queries(kv, k_pages, q, q_start, tree_mask, lse, ws)
+    qs = _queries(kv, k_pages, q, q_start, max_q, tree_mask, lse, ws)
     dev = kv._device
     _flat("acc_out", acc_out, torch.float32, dev, 2)
     if acc_out.shape[0] != kv.batch:
@@ -557,7 +577,7 @@ def ridgefill_attention_weight(kv: rf_paged_batch, k_pages, q, q_start, max_q: i
 
 
 def ridgefill_evict_workspace_bytes(kv: rf_paged_batch, n_keep: int) -> int:
-    return int(lib().ridgefill_evict_workspace_bytes(C.byref(kv), n_keep))
+    return int(lib().ridgefill_evict_workspace_bytes(C.byref(kv), n_keep)) if _fits(n_keep) else 0
 
 
 def ridgefill_evict_rows(kv: rf_paged_batch, layers, acc, positions, n_keep: int, acc_out,
@@ -570,6 +590,8 @@ def ridgefill_evict_rows(kv: rf_paged_batch, layers, acc, positions, n_keep: int
     dev = kv._device
     if kv._keep[1] is None:
         raise ValueError("the batch was made without lengths")
+    if not _fits(n_keep, n_sink, n_recent):
+        raise ValueError(f"n_keep = {n_keep}, n_sink = {n_sink}, n_recent = {n_recent}: more than 32 bits")
     if isinstance(layers, (list, tuple)):
         layers = make_pools([l["k_pages"] for l in layers], [l["v_pages"] for l in layers])
     for pool in layers._keep[0] + layers._keep[1]:
