@@ -497,6 +497,8 @@ def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, 
         raise ValueError("status must be a 4-byte integer tensor on the cache's device")
     heads = qs = qos = 0
     if q is not None:
+        if q_out is None:
+            raise ValueError("q without q_out")
         qs = _rows_of("q", q, torch.bfloat16, dev, hd, n)
         qos = _rows_of("q_out", q_out, torch.bfloat16, dev, hd, n)
         heads = q.shape[1]
@@ -544,6 +546,8 @@ def ridgefill_tree_attention(kv: rf_paged_batch, k_pages, v_pages, q, q_start, m
     qs = _queries(kv, k_pages, q, q_start, max_q, tree_mask, lse, ws)
     os_ = 0
     if out is not None:
+        if v_pages is None:
+            raise ValueError("out without v_pages")
         _flat("v_pages", v_pages, torch.bfloat16, kv._device, 4, kv._pool)
         os_ = _rows_of("out", out, torch.bfloat16, kv._device, kv.head_dim, q.shape[0])
         if out.shape[1] != q.shape[1]:
@@ -565,6 +569,8 @@ def ridgefill_attention_weight(kv: rf_paged_batch, k_pages, q, q_start, max_q: i
     import torch
     qs = _queries(kv, k_pages, q, q_start, max_q, tree_mask, lse, ws)
     dev = kv._device
+    if lse is None:
+        raise ValueError("the weights need the queries' lse")
     _flat("acc_out", acc_out, torch.float32, dev, 2)
     if acc_out.shape[0] != kv.batch:
         raise ValueError(f"acc_out has {acc_out.shape[0]} rows for {kv.batch} sequences")

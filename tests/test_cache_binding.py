@@ -43,3 +43,12 @@ def test_integers_past_32_bits_are_refused(kv, n):
     assert B.ridgefill_evict_workspace_bytes(kv, n) == 0
     for size in (B.ridgefill_tree_attention_workspace_bytes, B.ridgefill_attention_weight_workspace_bytes):
         assert size(kv, 2, 1) > 0 and size(kv, 2, n) == 0 and size(kv, n, 1) == 0
+
+
+def test_missing_tensors_are_refused(kv):
+    pool, k, ws = _bf(20, 16, 2, 64), _bf(3, 2, 64), torch.zeros(512, dtype=torch.uint8)
+    for call, text in ((lambda: B.ridgefill_append_rows(None, kv, k, k, _i32(3), pool, pool, _i32(1), q=k), "q_out"),
+                       (lambda: B.ridgefill_tree_attention(kv, pool, None, k, _i32(3), 2, 0.1, k, ws), "v_pages"),
+                       (lambda: B.ridgefill_attention_weight(kv, pool, k, _i32(3), 2, 0.1, None, torch.zeros(2, 100), ws), "lse")):
+        with pytest.raises(ValueError, match=text):
+            call()
