@@ -383,12 +383,13 @@ def _ints(**values: int) -> None:
 
 
 def _rows_of(name: str, t, dtype, device, width: int, n: int | None = None) -> int:
-    """Elements between the rows of [rows][heads][head_dim]; each row lies in one piece."""
+    """Elements between the rows of [rows][heads][head_dim]; each row lies in one piece.  A single
+    row's stride means nothing and is taken as the row's own size."""
     shape, stride = t.shape, t.stride()
     if (t.dtype is dtype and t.device == device and len(shape) == 3 and shape[2] == width
             and stride[2] == 1 and (stride[1] == width or shape[1] == 1) and shape[1] > 0
             and (n is None or shape[0] == n)):
-        return stride[0] if shape[0] > 1 else max(shape[1] * width, stride[0])
+        return stride[0] if shape[0] > 1 else shape[1] * width
     _need(name, t, dtype, device, 3)
     raise ValueError(f"{name} must be [{'rows' if n is None else n}][heads][{width}] with each "
                      f"row in one piece, not {tuple(shape)} with strides {stride}")

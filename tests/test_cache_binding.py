@@ -52,3 +52,10 @@ def test_missing_tensors_are_refused(kv):
                        (lambda: B.ridgefill_attention_weight(kv, pool, k, _i32(3), 2, 0.1, None, torch.zeros(2, 100), ws), "lse")):
         with pytest.raises(ValueError, match=text):
             call()
+
+
+def test_a_single_row_has_no_stride():
+    for base in (_bf(4, 387), _bf(4, 1000)):
+        row = base.as_strided((1, 3, 128), (base.shape[1], 128, 1))
+        assert B._rows_of("x", row, torch.bfloat16, base.device, 128) == 384
+        assert B._rows_of("x", base[:, :384].unflatten(1, (3, 128)), torch.bfloat16, base.device, 128) == base.shape[1]

@@ -109,3 +109,16 @@ def test_sums_of_a_long_cache_in_one_workgroup():
     want = torch.tensor([math.log(rows - 33 + i) for i in range(34)], dtype=torch.float64)[:, None]
     assert float((lse.cpu().double() - want).abs().max()) <= 8 * R.U_FP32 * math.log(rows)
     assert float((out.float() - 1).abs().max()) <= R.U_BF16
+
+
+def test_a_single_row_of_any_stride():
+    # one token taken out of rows of an odd length, rotated in place and elsewhere
+    base = torch.randn(4, 387, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    row = lambda t: t.as_strided((1, 3, 128), (387, 128, 1))  # noqa: E731
+    x, pos = row(base), torch.tensor([77], dtype=torch.int32, device=DEV)
+    want, out, rest = torch.empty(1, 3, 128, dtype=torch.bfloat16, device=DEV), torch.zeros_like(base), base.clone()
+    B.ridgefill_rope(B.make_rope(), x.contiguous(), pos, want)
+    B.ridgefill_rope(B.make_rope(), x, pos, row(out))
+    B.ridgefill_rope(B.make_rope(), x, pos, x)
+    rest[0, :384] = want.view(-1)
+    assert torch.equal(out[0, :384], want.view(-1)) and not out[0, 384:].any() and torch.equal(base, rest)
