@@ -552,8 +552,14 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
  * n rows those j whose bit is set in its word of tree_mask (without tree_mask: j <= i).
  *     s = scale q . k,   lse = ln sum exp s,   out = sum exp(s - lse) v
  * over the visible rows.  Query head h reads key head h / (n_q_heads / n_kv_heads).  A query
- * that sees no row, or only scores of -inf, gives out = 0 and lse = -inf.  A row that a query
- * does not see has no influence on it, whatever the row holds (NaN included).
+ * that sees no row, or only scores of -inf, gives out = 0 and lse = -inf; one that sees a score
+ * of +inf or NaN gives NaN in both.  A row that a query does not see has no influence on it,
+ * whatever the row holds (NaN included).  Sums of the values are fp32: magnitudes of v above
+ * 2^88 may overflow.
+ * Rows that are not the last of a sequence, or more than 64 of them, are sequences of their own
+ * in the batch with a copy of the same block-table row, each ending with its own queries: the
+ * last 150 rows of 300 as lengths 172, 236, 300 with 22, 64 and 64 queries.  Each such sequence
+ * reads the cache once more.
  *   q           device bf16 [n_q][n_q_heads][head_dim], rows q_stride elements apart
  *               (multiple of 8), 16-byte aligned; n_q_heads a multiple of n_kv_heads
  *   q_start     device int32 [batch + 1], ascending; sequences may have no queries.  One
