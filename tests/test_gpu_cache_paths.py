@@ -5,6 +5,7 @@ get wrong."""
 import copy
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -450,3 +451,39 @@ def test_weight_of_bad_sequences(form):
         _close(acc, want, tol, form)
     _, st = _weigh(cache, q, starts, words, max_q, 0.1, lse)
     assert st == B.RF_OK
+
+
+# ------------------------------------------------------------------------------------ append of many rows
+
+@pytest.mark.parametrize("n,n_kv,hd,heads", [(4096, 1, 64, 0), (4097, 1, 64, 0), (9001, 2, 64, 3), (5000, 8, 128, 32)])
+def test_append_many_rows(n, n_kv, hd, heads):
+    # looked over by one workgroup or reported by all: the same rows, the same status
+    page, g = 16, np.random.default_rng(n)
+    per = -(-n // page)
+    table = torch.from_numpy(g.permutation(2 * per)[:per].astype(np.int32))[None].to(DEV)
+    kv = B.make_batch(table, None, page, 2 * per, n_kv, hd, n)
+    qkv = torch.randn(n, heads + 2 * n_kv, hd, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).to(DEV)
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + n_kv], qkv[:, heads + n_kv:]
+    rows_np = g.permutation(n).astype(np.int32)
+    status = torch.full((1,), -1, dtype=torch.int32, device=DEV)
+    for bad in ([], [n - 1], [0, n // 2]):
+        rows_bad = rows_np.copy()
+        rows_bad[bad] = n
+        seq_np = np.zeros(n, np.int32)
+        seq_np[3] = -1                                    # padding is no error
+        kp, vp = (torch.zeros(2 * per, page, n_kv, hd, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        q_out = torch.zeros(n, heads, hd, dtype=torch.bfloat16, device=DEV) if heads else None
+        B.ridgefill_append_rows(None, kv, k, v, torch.from_numpy(rows_bad).to(DEV), kp, vp, status,
+                                seq=torch.from_numpy(seq_np).to(DEV), q=q if heads else None, q_out=q_out)
+        assert B.ridgefill_read_status(status) == (B.RF_E_ROWS if bad else B.RF_OK)
+        real = np.setdiff1d(np.arange(n), bad + [3])
+        at = table[0].long()[torch.from_numpy(rows_np[real] // page).to(DEV).long()], torch.from_numpy(rows_np[real] % page).to(DEV).long()
+        real = torch.from_numpy(real).to(DEV)
+        for pool, x in ((kp, k), (vp, v)):
+            assert torch.equal(pool[at], x[real])
+            pool[at] = 0
+            assert not pool.any()
+        if heads:
+            assert not q_out[3].any()
+            q_out[3] = q[3]
+            assert torch.equal(q_out, q)
