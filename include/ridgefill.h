@@ -444,7 +444,8 @@ rf_status ridgefill_solve_ex(const void* state, size_t state_bytes, int32_t d_in
  * The cache beyond the fill.  Exact rows, the tail and the generated tokens run the upper
  * layers themselves (section "Two numbers set the skip range"): their keys and values go
  * into the same paged cache, and their queries attend over it.  The calls below rotate and
- * append such rows, attend over the cache, accumulate the attention weight that its rows
+ * append such rows, attend over the cache (up to 64 queries a sequence, its last rows; more
+ * and others as sequences of their own), accumulate the attention weight that its rows
  * receive (the scores of section "Which rows to compute exactly"), and shorten it.  They
  * work on one layer's pools (the eviction on all of them) and on a batch of sequences.
  *

@@ -234,9 +234,9 @@ __device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, cons
 
 // kOut: with the product with V (else only the statistics).
 // At most 16 query rows: bound by the read of K and V.  16 sequences of up to 16,384 rows, one token,
-// 8 key heads of 128 (805 MB): 146 us of the call's 153, 5.5 TB/s, as a large copy.  (The tile kernel
-// below takes 187 us there; this one, with four tiles of 16 queries, takes 120 us for 64 query rows
-// over 65,536 where that takes 70.)
+// 8 key heads of 128 (760 MB): 148 us of the call's 153, 5.1 TB/s, as a large copy.  (The tile kernel
+// below took 187 us there; this one, with four tiles of 16 queries, 120 us for 64 query rows over 65,536
+// where that took 70; both with one operand a weight.)
 template <int HD, bool kOut>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   constexpr int kSteps = HD / 32, kFeat = HD / 16;
@@ -493,12 +493,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 // rows gave as many cycles of them as of reads and 153 instead of 150 us for 65,536 rows.  The pool
 // slots of the workgroup's rows are looked up beforehand: a table load between the direct loads
 // would wait for those.
-// Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 139 us
-// with the join's 9, 416 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 140 us, 614 TFLOP/s.
-// What bounds it are the vector instructions, 1,600 cycles a wave and step of 64 rows, with two
-// waves to a SIMD (exponentials 512 of them), at a clock that 256 busy query rows pull down to
-// 1.5 GHz (64: 2.2 GHz); 17 us are the start and the end.  Blocks of 128
-// query rows that loaded through registers took 248 us, two workgroups for each compute unit 203.
+// Trees of up to 48 tokens on 4 sequences of up to 32,768 rows, 32 query and 8 key heads of 128: 173 us
+// with the join's 9, 429 TFLOP/s; one of 64 tokens over 65,536 rows, 40 query heads: 175 us, 490 TFLOP/s;
+// 32 query heads there: 112 and 9 us, 615 TFLOP/s.
+// What bounds it are the matrix products (36 to 39% of the cycles) beside the vector instructions (50%,
+// exponentials included) of two waves to a SIMD, at 1.6 to 1.9 GHz; and waves with no query rows: a step
+// takes nearly as long with five busy (132 to 192 query rows, the trees) as with eight, and of 320 query
+// rows the block of 64 keeps two of eight busy for as many parts of the cache as the block of 256.
+// Blocks of 128 query rows that loaded through registers took 248 us, two workgroups for each compute
+// unit 203 (139 with the present ones, all with one operand a weight).
 constexpr int kTileRows = 64;
 constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;

@@ -1,5 +1,5 @@
 // Internal interface between the C entry points of the cache calls (rf_cache.cpp) and their
-// kernels (rf_rope.hip, rf_attend.hip, rf_evict.hip).
+// kernels (rf_rope.hip, rf_attend.hip, rf_weight.hip, rf_evict.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -12,12 +12,12 @@
 // M <= 64 (decoding, small trees): bound by the read of K.  A workgroup takes 64 or more cache
 // rows and all key heads (its waves share them out), joins the heads in LDS and writes the
 // accumulated weight: one launch.  16 sequences of up to 16,384 rows, one token, 8 key heads of
-// 128: 73 us, 5.5 TB/s, as a large copy.
+// 128 (380 MB): 73 us, 5.2 TB/s, as a large copy.
 // M > 64: bound by the exponentials (16 cycles a wave of 64) and the matrix cores.  Q of one key
 // head (256 rows a block) lies in LDS and a workgroup walks a long range of cache rows with it;
 // the heads' sums meet in a second launch.  The last 64 tokens of 32,768 rows, 32 query heads: 33 + 5
 // us, 35 in one call after another, 485 TFLOP/s; the exponentials alone are 12 us (24 cycles with
-// their addition), staging Q 7.
+// their addition), staging Q 7 (whose writes meet in LDS banks: 40% of the kernel's LDS cycles).
 #include "rf_cache_dev.h"
 #include "rf_split.h"
 
