@@ -21,7 +21,7 @@
  *  - `stream` is a hipStream_t (NULL = the null stream).  Device work is enqueued
  *    on it and the call returns without waiting, except where stated.  ridgefill_fill
  *    with resident maps (plain or folded) and the cache calls (ridgefill_rope to
- *    ridgefill_evict_rows) enqueue kernels only (the status word is cleared by a kernel,
+ *    ridgefill_evict_rows, ridgefill_norm_rope to ridgefill_cache_attention) enqueue kernels only (the status word is cleared by a kernel,
  *    not a memset), so they can be captured into a HIP graph and replayed; workspaces,
  *    index lists and pools must then stay at their addresses.
  *  - Errors found on the host (null pointers, shapes, sizes, workspace too small,
@@ -644,6 +644,103 @@ rf_status ridgefill_evict_rows(const rf_paged_batch* kv, const rf_layer* layers,
                                int32_t n_keep, int32_t n_sink, int32_t n_recent, float* acc_out,
                                int32_t* positions_out, int32_t* lengths_out, void* ws,
                                size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Norms of query and key heads with their rotation, in one pass (section "Hybrid layers and
+ * two corrections": layers that norm their keys, as the fill does with k_norm_w).  For a head x
+ * with weight w, r = (mean x^2 + eps)^(-1/2) over its head_dim features and R the rotation:
+ *     y = R (w r x)
+ * A tensor without a weight is only rotated.  Sums of squares are fp32 (magnitudes above 2^60
+ * overflow them), results are rounded once.  With eps = 0 a head of zeros gives NaN.
+ * ------------------------------------------------------------------------------ */
+typedef struct rf_head_norm {
+  const void* q_w;              /* device [head_dim], of the tensors' type, 16-byte aligned;
+                                   NULL: q is not normed                                     */
+  const void* k_w;              /* the same for k                                            */
+  float eps;                    /* >= 0                                                      */
+  int32_t reserved;             /* must be 0                                                 */
+} rf_head_norm;
+
+/* q [n_rows][n_q_heads][head_dim] into q_out and k [n_rows][n_k_heads][head_dim] into k_out;
+ * either may be NULL, with n_q_heads or n_k_heads 0.
+ *   rope        NULL: no rotation (positions may then be NULL)
+ *   norm        NULL: no norm
+ *   q, k, q_out, k_out   device, all of `type` (RF_TYPE_BF16 or RF_TYPE_F32), 16-byte aligned;
+ *               strides (elements between rows) >= heads * head_dim and multiples of 8 (bf16)
+ *               or 4 (fp32); an output may be its input with equal strides, other overlaps are
+ *               not allowed
+ *   positions   device int32 [n_rows]
+ * head_dim: a multiple of 16 up to 256; heads up to 4096 each; n_rows: 0 .. 2^23. */
+rf_status ridgefill_norm_rope(const rf_rope* rope, const rf_head_norm* norm, int32_t type,
+                              int64_t n_rows, int32_t head_dim, const int32_t* positions,
+                              const void* q, int32_t n_q_heads, int64_t q_stride, void* q_out,
+                              int64_t q_out_stride, const void* k, int32_t n_k_heads,
+                              int64_t k_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* Its gradient: of the inputs q and k (as they went in) and the gradients gq and gk of the
+ * outputs, q_grad and k_grad, and in fp32 [head_dim] those of the weights, qw_grad and kw_grad
+ * (each may be NULL; not written for a tensor without a weight).  With g = R^T gy, xh = r x:
+ *     q_grad = r (w g - xh mean(w g xh)),   qw_grad = sum over rows and heads of g xh
+ * q and k may be NULL where they have no weight (their values are not needed), q_grad may be gq
+ * and k_grad gk with equal strides.  The weights' sums are fp32, added in a fixed order.
+ *   ws          >= ridgefill_norm_rope_grad_workspace_bytes(...), 256-byte aligned
+ * Size query: 0 on invalid input. */
+size_t ridgefill_norm_rope_grad_workspace_bytes(int64_t n_rows, int32_t n_q_heads,
+                                                int32_t n_k_heads, int32_t head_dim);
+rf_status ridgefill_norm_rope_grad(const rf_rope* rope, const rf_head_norm* norm, int32_t type,
+                                   int64_t n_rows, int32_t head_dim, const int32_t* positions,
+                                   const void* q, int32_t n_q_heads, int64_t q_stride,
+                                   const void* gq, int64_t gq_stride, void* q_grad,
+                                   int64_t q_grad_stride, float* qw_grad, const void* k,
+                                   int32_t n_k_heads, int64_t k_stride, const void* gk,
+                                   int64_t gk_stride, void* k_grad, int64_t k_grad_stride,
+                                   float* kw_grad, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * Caches in 16 or 8 bits.  RF_CACHE_BF16 is the cache of the calls above.  The others hold codes
+ * of 8 bits (e4m3 floats, or whole numbers) in blocks of 32 features of a head that share a power
+ * of two, as the OCP microscaling formats do: for a block x, e is the smallest exponent with
+ * max |x| <= M 2^e (M = 448 for e4m3, 127 for int8), kept to -110 .. 118; a code is x 2^-e rounded
+ * to its type (ties to even, magnitudes above M to M) and stands for code * 2^e; the scale byte is
+ * e + 127.  A block with an infinity or NaN is NaN altogether: scale byte 255.  Every value that a
+ * cache can hold is exactly a bf16: reads give it as it is, and attention over such a cache gives
+ * what it gives over a bf16 cache of the same values, bit for bit.  Scale bytes other than 17 .. 245
+ * and 255 are not allowed in a cache written elsewhere.
+ * ------------------------------------------------------------------------------ */
+#define RF_CACHE_BF16 0
+#define RF_CACHE_FP8 1
+#define RF_CACHE_INT8 2
+typedef struct rf_cache {       /* one layer's pools, device, 16-byte aligned                */
+  int32_t type;
+  int32_t reserved;             /* must be 0                                                 */
+  void* k_pages;                /* bf16 or 8-bit codes [num_pages][page_size][n_kv_heads][head_dim] */
+  void* v_pages;
+  uint8_t* k_scales;            /* [num_pages][page_size][n_kv_heads][head_dim / 32]; NULL for bf16 */
+  uint8_t* v_scales;
+} rf_cache;
+
+/* ridgefill_append_rows for a cache of any type and for layers with head norms: q and k are
+ * normed where norm has a weight (bf16 [head_dim]), rotated, and k and v are rounded once to what
+ * the cache holds.  Arguments as there; head_dim a multiple of 32 for 8 bits (16 for bf16).  With
+ * norm NULL and a bf16 cache it does what that call does. */
+rf_status ridgefill_append_cache(const rf_rope* rope, const rf_head_norm* norm,
+                                 const rf_paged_batch* kv, const rf_cache* cache,
+                                 const uint16_t* q, int32_t n_q_heads, int64_t q_stride,
+                                 uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+                                 int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                 int64_t n_rows, const int32_t* seq, const int32_t* rows,
+                                 const int32_t* positions, uint32_t* status, void* stream);
+
+/* Cached rows back: k_out[i] and v_out[i] receive cache row rows[i] of sequence seq[i].
+ *   k_out, v_out   device [n_rows][n_kv_heads][head_dim] of `type` (RF_TYPE_BF16 or RF_TYPE_F32;
+ *                  both exact), 16-byte aligned, strides as in ridgefill_norm_rope; one may be NULL
+ *   seq, rows, status   as in ridgefill_append_rows, but the same row may come more than once;
+ *                  rows that are out of range, on a bad page or padding are left as they were
+ * kv->lengths is not read.  n_rows: 0 .. 2^23, n_rows * n_kv_heads * head_dim <= 2^34. */
+rf_status ridgefill_read_rows(const rf_paged_batch* kv, const rf_cache* cache, int64_t n_rows,
+                              const int32_t* seq, const int32_t* rows, int32_t type, void* k_out,
+                              int64_t k_out_stride, void* v_out, int64_t v_out_stride,
+                              uint32_t* status, void* stream);
 
 /* Waits for `stream`, then returns the device status word of a fill, solve or selection
  * workspace, or of a cache call's workspace or status word: RF_OK, RF_E_ROWS, RF_E_NOT_SPD,

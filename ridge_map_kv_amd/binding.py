@@ -53,6 +53,11 @@ EXPORTED = [
     "ridgefill_attention_weight",
     "ridgefill_evict_workspace_bytes",
     "ridgefill_evict_rows",
+    "ridgefill_norm_rope",
+    "ridgefill_norm_rope_grad_workspace_bytes",
+    "ridgefill_norm_rope_grad",
+    "ridgefill_append_cache",
+    "ridgefill_read_rows",
     "ridgefill_read_status",
     "ridgefill_solve_info",
     "ridgefill_profile_enable",
@@ -104,9 +109,19 @@ class rf_rope(C.Structure):
                 ("low", C.c_double), ("high", C.c_double), ("mscale", C.c_double)]
 
 
+class rf_head_norm(C.Structure):
+    _fields_ = [("q_w", C.c_void_p), ("k_w", C.c_void_p), ("eps", C.c_float), ("reserved", C.c_int32)]
+
+
+class rf_cache(C.Structure):
+    _fields_ = [("type", C.c_int32), ("reserved", C.c_int32), ("k_pages", C.c_void_p),
+                ("v_pages", C.c_void_p), ("k_scales", C.c_void_p), ("v_scales", C.c_void_p)]
+
+
 RF_ROPE_HALF, RF_ROPE_INTERLEAVED = range(2)
 RF_ROPE_PLAIN, RF_ROPE_LINEAR, RF_ROPE_NTK, RF_ROPE_BANDS, RF_ROPE_YARN = range(5)
 RF_TYPE_BF16, RF_TYPE_F32 = range(2)
+RF_CACHE_BF16, RF_CACHE_FP8, RF_CACHE_INT8 = range(3)
 
 _lib = None
 
@@ -167,6 +182,14 @@ def lib() -> C.CDLL:
         "ridgefill_evict_workspace_bytes": (sz, [vp, i32]),
         "ridgefill_evict_rows": (st, [vp, C.POINTER(rf_layer), i32, vp, vp, i64, i32, i32, i32, vp,
                                       vp, vp, vp, sz, vp]),
+        "ridgefill_norm_rope": (st, [vp, vp, i32, i64, i32, vp, vp, i32, i64, vp, i64, vp, i32, i64,
+                                     vp, i64, vp]),
+        "ridgefill_norm_rope_grad_workspace_bytes": (sz, [i64, i32, i32, i32]),
+        "ridgefill_norm_rope_grad": (st, [vp, vp, i32, i64, i32, vp, vp, i32, i64, vp, i64, vp, i64,
+                                          vp, vp, i32, i64, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "ridgefill_append_cache": (st, [vp, vp, vp, vp, vp, i32, i64, vp, i64, vp, i64, vp, i64, i64,
+                                        vp, vp, vp, vp, vp]),
+        "ridgefill_read_rows": (st, [vp, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, vp]),
         "ridgefill_read_status": (st, [vp, vp]),
         "ridgefill_solve_info": (st, [vp, C.POINTER(C.c_double), C.POINTER(i32), vp]),
         "ridgefill_profile_enable": (st, [i32]),
@@ -476,26 +499,25 @@ def ridgefill_rope(rope: rf_rope, x, positions, out, transpose: bool = False, st
         positions.data_ptr(), out.data_ptr(), os_, 1 if transpose else 0)
 
 
-def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, k_pages, v_pages,
-                          status, seq=None, positions=None, q=None, q_out=None, stream=None) -> None:
-    """k (rotated) and v, bf16 [n][n_kv][head_dim], into cache rows `rows` (int32 [n]) of
-    sequences `seq` (int32 [n]; None: sequence 0; negative: a padding row); q rotated into
-    q_out.  positions (int32 [n]) default to the rows.  status: device int32 tensor."""
+def _status_of(status, device) -> None:
+    if status.device != device or status.numel() < 1 or status.element_size() != 4:
+        raise ValueError("status must be a 4-byte integer tensor on the cache's device")
+
+
+def _appended(kv: rf_paged_batch, k, v, rows, status, seq, positions, q, q_out) -> tuple:
+    """Checks of what an append writes; q, k and v as the C side takes them."""
     import torch
     dev, n, hd = kv._device, k.shape[0], kv.head_dim
     ks = _rows_of("k", k, torch.bfloat16, dev, hd, n)
     vs = _rows_of("v", v, torch.bfloat16, dev, hd, n)
     if k.shape[1] != kv.n_kv_heads or v.shape[1] != kv.n_kv_heads:
         raise ValueError(f"k and v must have {kv.n_kv_heads} heads")
-    _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
-    _flat("v_pages", v_pages, torch.bfloat16, dev, 4, kv._pool)
     _flat("rows", rows, torch.int32, dev, 1, (n,))
     if seq is not None:
         _flat("seq", seq, torch.int32, dev, 1, (n,))
     if positions is not None:
         _flat("positions", positions, torch.int32, dev, 1, (n,))
-    if status.device != dev or status.numel() < 1 or status.element_size() != 4:
-        raise ValueError("status must be a 4-byte integer tensor on the cache's device")
+    _status_of(status, dev)
     heads = qs = qos = 0
     if q is not None:
         if q_out is None:
@@ -507,10 +529,22 @@ def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, 
             raise ValueError(f"q_out has {q_out.shape[1]} heads, q {heads}")
     elif q_out is not None:
         raise ValueError("q_out without q")
+    return _ptr(q), heads, qs, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs
+
+
+def ridgefill_append_rows(rope: rf_rope | None, kv: rf_paged_batch, k, v, rows, k_pages, v_pages,
+                          status, seq=None, positions=None, q=None, q_out=None, stream=None) -> None:
+    """k (rotated) and v, bf16 [n][n_kv][head_dim], into cache rows `rows` (int32 [n]) of
+    sequences `seq` (int32 [n]; None: sequence 0; negative: a padding row); q rotated into
+    q_out.  positions (int32 [n]) default to the rows.  status: device int32 tensor."""
+    import torch
+    dev = kv._device
+    _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
+    _flat("v_pages", v_pages, torch.bfloat16, dev, 4, kv._pool)
+    args = _appended(kv, k, v, rows, status, seq, positions, q, q_out)
     _go(lib().ridgefill_append_rows, dev, stream, None if rope is None else C.byref(rope),
-        C.byref(kv), _ptr(q), heads, qs, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, n,
-        _ptr(seq), rows.data_ptr(), _ptr(positions), k_pages.data_ptr(), v_pages.data_ptr(),
-        status.data_ptr())
+        C.byref(kv), *args, k.shape[0], _ptr(seq), rows.data_ptr(), _ptr(positions),
+        k_pages.data_ptr(), v_pages.data_ptr(), status.data_ptr())
 
 
 def ridgefill_tree_attention_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int) -> int:
@@ -615,6 +649,173 @@ def ridgefill_evict_rows(kv: rf_paged_batch, layers, acc, positions, n_keep: int
         acc.data_ptr(), positions.data_ptr(), shape[1], n_keep, n_sink, n_recent,
         acc_out.data_ptr(), positions_out.data_ptr(), lengths_out.data_ptr(), ws.data_ptr(),
         _nbytes(ws))
+
+
+def make_head_norm(q_w=None, k_w=None, eps: float = 1e-6) -> rf_head_norm:
+    """Norms of query and key heads: weights [head_dim] (None: that tensor is not normed), of the
+    type of the tensors they are used on.  It keeps them alive."""
+    for name, w in (("q_w", q_w), ("k_w", k_w)):
+        if w is not None and (w.dim() != 1 or not w.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous [head_dim], not {tuple(w.shape)} with strides {w.stride()}")
+    norm = rf_head_norm(_ptr(q_w), _ptr(k_w), eps, 0)
+    norm._keep = (q_w, k_w)
+    return norm
+
+
+def make_cache(k_pages, v_pages, k_scales=None, v_scales=None) -> rf_cache:
+    """One layer's pools [num_pages][page_size][n_kv][head_dim]: bf16, or 8-bit codes
+    (float8_e4m3fn or int8) with their blocks' scales, uint8 [num_pages][page_size][n_kv]
+    [head_dim / 32].  v_pages may be None for attention that gives only lse.  It keeps them alive."""
+    import torch
+    kinds = {torch.bfloat16: RF_CACHE_BF16, torch.float8_e4m3fn: RF_CACHE_FP8, torch.int8: RF_CACHE_INT8}
+    dtype, dev = k_pages.dtype, k_pages.device
+    if dtype not in kinds:
+        raise ValueError(f"k_pages must be bfloat16, float8_e4m3fn or int8, not {dtype}")
+    _flat("k_pages", k_pages, dtype, dev, 4)
+    shape = tuple(k_pages.shape)
+    if v_pages is not None:
+        _flat("v_pages", v_pages, dtype, dev, 4, shape)
+    for name, pages, scales in (("k_scales", k_pages, k_scales), ("v_scales", v_pages, v_scales)):
+        if (scales is not None) != (dtype is not torch.bfloat16 and pages is not None):
+            raise ValueError(f"{name}: pages of 8 bits have scales, others have none")
+        if scales is not None:
+            _flat(name, scales, torch.uint8, dev, 4, shape[:3] + (shape[3] // 32,))
+    cache = rf_cache(kinds[dtype], 0, k_pages.data_ptr(), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales))
+    cache._keep = (k_pages, v_pages, k_scales, v_scales)
+    cache._pool, cache._device = shape, dev
+    return cache
+
+
+def _cache_of(kv: rf_paged_batch, cache: rf_cache) -> None:
+    if cache._pool != kv._pool or cache._device != kv._device:
+        raise ValueError(f"the cache's pools are {cache._pool} on {cache._device}, the batch's {kv._pool} on {kv._device}")
+
+
+def _normed(norm: rf_head_norm | None, dtype, device, head_dim: int) -> None:
+    """The weights of a norm that is used on tensors of this type."""
+    for name, w in zip(("q_w", "k_w"), norm._keep if norm is not None else ()):
+        if w is not None:
+            _flat(name, w, dtype, device, 1, (head_dim,))
+
+
+def ridgefill_norm_rope(rope: rf_rope | None, norm: rf_head_norm | None, positions, q=None, q_out=None,
+                        k=None, k_out=None, stream=None) -> None:
+    """q and k [rows][heads][head_dim] (bf16 or fp32; either may be None), normed per head where
+    `norm` has a weight and rotated by positions (int32 [rows]), into q_out and k_out (which may
+    be q and k)."""
+    import torch
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("neither q nor k")
+    dev, n, hd = x.device, x.shape[0], x.shape[-1]
+    dtype = torch.float32 if x.dtype is torch.float32 else torch.bfloat16
+    _normed(norm, dtype, dev, hd)
+    args = []
+    for name, t, out in (("q", q, q_out), ("k", k, k_out)):
+        if (t is None) != (out is None):
+            raise ValueError(f"{name} and {name}_out go together")
+        if t is None:
+            args += [None, 0, 0, None, 0]
+            continue
+        stride = _rows_of(name, t, dtype, dev, hd, n)
+        out_stride = _rows_of(name + "_out", out, dtype, dev, hd, n)
+        if out.shape[1] != t.shape[1]:
+            raise ValueError(f"{name}_out has {out.shape[1]} heads, {name} {t.shape[1]}")
+        args += [t.data_ptr(), t.shape[1], stride, out.data_ptr(), out_stride]
+    if rope is not None:
+        _flat("positions", positions, torch.int32, dev, 1, (n,))
+    _go(lib().ridgefill_norm_rope, dev, stream, None if rope is None else C.byref(rope),
+        None if norm is None else C.byref(norm), RF_TYPE_F32 if dtype is torch.float32 else RF_TYPE_BF16, n, hd,
+        None if rope is None else positions.data_ptr(), *args)
+
+
+def ridgefill_norm_rope_grad_workspace_bytes(n_rows: int, n_q_heads: int, n_k_heads: int, head_dim: int) -> int:
+    if not _fits(n_rows, n_q_heads, n_k_heads, head_dim):
+        return 0
+    return int(lib().ridgefill_norm_rope_grad_workspace_bytes(n_rows, n_q_heads, n_k_heads, head_dim))
+
+
+def ridgefill_norm_rope_grad(rope: rf_rope | None, norm: rf_head_norm | None, positions, ws, q=None, gq=None,
+                             q_grad=None, qw_grad=None, k=None, gk=None, k_grad=None, kw_grad=None,
+                             stream=None) -> None:
+    """From the gradients gq and gk of the outputs of ridgefill_norm_rope on q and k: q_grad and
+    k_grad (which may be gq and gk), and qw_grad and kw_grad (fp32 [head_dim], None: not wanted)
+    of the weights.  q or k may be None where it has no weight."""
+    import torch
+    x = gq if gq is not None else gk
+    if x is None:
+        raise ValueError("neither gq nor gk")
+    dev, n, hd = x.device, x.shape[0], x.shape[-1]
+    dtype = torch.float32 if x.dtype is torch.float32 else torch.bfloat16
+    _normed(norm, dtype, dev, hd)
+    args = []
+    weights = norm._keep if norm is not None else (None, None)
+    for name, w, t, g, out, dw in (("q", weights[0], q, gq, q_grad, qw_grad), ("k", weights[1], k, gk, k_grad, kw_grad)):
+        if (g is None) != (out is None) or (g is None and (t is not None or dw is not None)):
+            raise ValueError(f"{name}: g{name} and {name}_grad go together")
+        if g is None:
+            args += [None, 0, 0, None, 0, None, 0, None]
+            continue
+        if w is not None and t is None:
+            raise ValueError(f"the gradient of normed {name} needs {name}")
+        stride = _rows_of(name, t, dtype, dev, hd, n) if t is not None else 0
+        g_stride = _rows_of("g" + name, g, dtype, dev, hd, n)
+        out_stride = _rows_of(name + "_grad", out, dtype, dev, hd, n)
+        if out.shape[1] != g.shape[1] or (t is not None and t.shape[1] != g.shape[1]):
+            raise ValueError(f"{name}, g{name} and {name}_grad differ in heads")
+        if dw is not None:
+            _flat(name + "w_grad", dw, torch.float32, dev, 1, (hd,))
+        args += [_ptr(t), g.shape[1], stride, g.data_ptr(), g_stride, out.data_ptr(), out_stride, _ptr(dw)]
+    if rope is not None:
+        _flat("positions", positions, torch.int32, dev, 1, (n,))
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+    _go(lib().ridgefill_norm_rope_grad, dev, stream, None if rope is None else C.byref(rope),
+        None if norm is None else C.byref(norm), RF_TYPE_F32 if dtype is torch.float32 else RF_TYPE_BF16, n, hd,
+        None if rope is None else positions.data_ptr(), *args, ws.data_ptr(), _nbytes(ws))
+
+
+def ridgefill_append_cache(rope: rf_rope | None, norm: rf_head_norm | None, kv: rf_paged_batch, cache: rf_cache, k, v,
+                           rows, status, seq=None, positions=None, q=None, q_out=None, stream=None) -> None:
+    """ridgefill_append_rows into a cache of any type (from make_cache), with q and k normed per
+    head where `norm` has a weight (bf16)."""
+    import torch
+    dev, n, hd = kv._device, k.shape[0], kv.head_dim
+    _cache_of(kv, cache)
+    _normed(norm, torch.bfloat16, dev, hd)
+    if cache._keep[1] is None:
+        raise ValueError("the cache was made without v_pages")
+    args = _appended(kv, k, v, rows, status, seq, positions, q, q_out)
+    _go(lib().ridgefill_append_cache, dev, stream, None if rope is None else C.byref(rope),
+        None if norm is None else C.byref(norm), C.byref(kv), C.byref(cache), *args, n, _ptr(seq),
+        rows.data_ptr(), _ptr(positions), status.data_ptr())
+
+
+def ridgefill_read_rows(kv: rf_paged_batch, cache: rf_cache, rows, status, seq=None, k_out=None, v_out=None,
+                        stream=None) -> None:
+    """Cache rows `rows` (int32 [n]) of sequences `seq` (int32 [n]; None: sequence 0; negative:
+    left out) into k_out and v_out [n][n_kv][head_dim], bf16 or fp32; one of them may be None."""
+    import torch
+    dev, n, hd = kv._device, rows.shape[0], kv.head_dim
+    _cache_of(kv, cache)
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        raise ValueError("neither k_out nor v_out")
+    if v_out is not None and cache._keep[1] is None:
+        raise ValueError("v_out, and the cache was made without v_pages")
+    dtype = torch.float32 if out.dtype is torch.float32 else torch.bfloat16
+    strides = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        strides.append(0 if t is None else _rows_of(name, t, dtype, dev, hd, n))
+        if t is not None and t.shape[1] != kv.n_kv_heads:
+            raise ValueError(f"{name} must have {kv.n_kv_heads} heads")
+    _flat("rows", rows, torch.int32, dev, 1, (n,))
+    if seq is not None:
+        _flat("seq", seq, torch.int32, dev, 1, (n,))
+    _status_of(status, dev)
+    _go(lib().ridgefill_read_rows, dev, stream, C.byref(kv), C.byref(cache), n, _ptr(seq), rows.data_ptr(),
+        RF_TYPE_F32 if dtype is torch.float32 else RF_TYPE_BF16, _ptr(k_out), strides[0], _ptr(v_out), strides[1],
+        status.data_ptr())
 
 
 # ------------------------------------------------------------------------------ calibration

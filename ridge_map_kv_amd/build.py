@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libridgefill.so")
 
 SOURCES = ["rf_fill.hip", "rf_calib.hip", "rf_solve.hip", "rf_select.hip", "rf_fold.hip",
-           "rf_rope.hip", "rf_attend.hip", "rf_weight.hip", "rf_evict.hip", "ridgefill.cpp",
+           "rf_rope.hip", "rf_norm.hip", "rf_attend.hip", "rf_weight.hip", "rf_evict.hip", "ridgefill.cpp",
            "rf_cache.cpp", "rf_profile.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,6 +1,6 @@
-// C entry points of the cache calls (rotary positions, append, attention, attention weight,
-// eviction): argument checks and the host side of the rotation's frequencies.  Device work is
-// in rf_rope.hip, rf_attend.hip, rf_weight.hip and rf_evict.hip.
+// C entry points of the cache calls (rotary positions, head norms, append, read, attention,
+// attention weight, eviction): argument checks and the host side of the rotation's frequencies.
+// Device work is in rf_rope.hip, rf_norm.hip, rf_attend.hip, rf_weight.hip and rf_evict.hip.
 #include "rf_cache.h"
 
 #include <cmath>
@@ -134,6 +134,93 @@ rf_status check_queries(const rf::Batch& b, const uint16_t* q, int n_q_heads, in
   return RF_OK;
 }
 
+// The arguments of an append, and the rotation's frequencies.
+rf_status check_append(const rf_rope* rope, const rf::Batch& b, const uint16_t* q, int32_t n_q_heads, int64_t q_stride,
+                       const uint16_t* q_out, int64_t q_out_stride, const uint16_t* k, int64_t k_stride,
+                       const uint16_t* v, int64_t v_stride, int64_t n_rows, const int32_t* seq, const int32_t* rows,
+                       const int32_t* positions, const void* k_pages, const void* v_pages, const uint32_t* status,
+                       rf::RopeFreq& f) {
+  if (!status || !aligned(status, 4))
+    return fail(RF_E_INVALID, "status must be a 4-byte aligned device pointer");
+  if (n_rows < 0 || n_rows > kMaxRows)
+    return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23", (long long)n_rows);
+  f = {};
+  f.layout = RF_ROPE_HALF;
+  if (rope) {
+    const rf_status s = make_freq(rope, b.hd, f);
+    if (s != RF_OK) return s;
+  }
+  if (n_q_heads < 0 || n_q_heads > 4096) return fail(RF_E_SHAPE, "n_q_heads = %d must be in 0..4096", n_q_heads);
+  if ((n_q_heads > 0) != (q != nullptr || q_out != nullptr) || (q != nullptr) != (q_out != nullptr)) {
+    if (n_rows > 0 || n_q_heads == 0)
+      return fail(RF_E_INVALID, "q and q_out go together, and with n_q_heads > 0");
+  }
+  const int64_t kw = (int64_t)b.n_kv * b.hd, qw = (int64_t)n_q_heads * b.hd;
+  if (k_stride < kw || v_stride < kw || k_stride % 8 || v_stride % 8)
+    return fail(RF_E_SHAPE, "k_stride and v_stride must be >= n_kv_heads * head_dim and multiples of 8");
+  if (n_q_heads && (q_stride < qw || q_out_stride < qw || q_stride % 8 || q_out_stride % 8))
+    return fail(RF_E_SHAPE, "q_stride and q_out_stride must be >= n_q_heads * head_dim and multiples of 8");
+  if (n_q_heads && q == q_out && q_stride != q_out_stride)
+    return fail(RF_E_INVALID, "rotating q in place needs equal strides");
+  if (n_rows == 0) return RF_OK;
+  if (!k || !v || !rows || !k_pages || !v_pages || !b.tables)
+    return fail(RF_E_INVALID, "null pointer among k, v, rows, k_pages, v_pages, block_tables");
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(rows, 4) || !aligned(seq, 4) ||
+      !aligned(positions, 4) || !aligned(b.tables, 4))
+    return fail(RF_E_SHAPE, "q, q_out, k, v and the pages need 16-byte, the index lists 4-byte alignment");
+  return RF_OK;
+}
+
+// A tensor of heads and what is made of it; strides in elements of `step` to 16 bytes.
+rf_status check_heads_of(const char* name, const void* x, int heads, int hd, int64_t stride, int step) {
+  if (stride < (int64_t)heads * hd || stride % step)
+    return fail(RF_E_SHAPE, "%s: the stride must be >= heads * head_dim and a multiple of %d", name, step);
+  if (!aligned(x, 16)) return fail(RF_E_SHAPE, "%s needs 16-byte alignment", name);
+  return RF_OK;
+}
+
+rf_status check_norm(const rf_head_norm* norm) {
+  if (!norm) return RF_OK;
+  if (norm->reserved != 0) return fail(RF_E_INVALID, "norm.reserved must be 0");
+  if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps)) return fail(RF_E_INVALID, "norm.eps must be finite and >= 0");
+  if (!aligned(norm->q_w, 16) || !aligned(norm->k_w, 16))
+    return fail(RF_E_SHAPE, "the norms' weights need 16-byte alignment");
+  return RF_OK;
+}
+
+// What the norm's forward and backward calls share.
+rf_status check_norm_call(const rf_rope* rope, const rf_head_norm* norm, int32_t type, int64_t n, int hd, int n_q,
+                          int n_k, rf::RopeFreq& f) {
+  if (type != RF_TYPE_BF16 && type != RF_TYPE_F32) return fail(RF_E_INVALID, "type = %d", type);
+  if (hd < 16 || hd > 256 || hd % 16) return fail(RF_E_SHAPE, "head_dim = %d must be a multiple of 16 up to 256", hd);
+  if (n_q < 0 || n_q > 4096 || n_k < 0 || n_k > 4096 || n_q + n_k == 0)
+    return fail(RF_E_SHAPE, "n_q_heads = %d and n_k_heads = %d must be in 0..4096, not both 0", n_q, n_k);
+  if (n < 0 || n > kMaxRows) return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23", (long long)n);
+  f = {};
+  f.layout = RF_ROPE_HALF;
+  const rf_status s = check_norm(norm);
+  return s != RF_OK || !rope ? s : make_freq(rope, hd, f);
+}
+
+// One layer's pools.
+rf_status check_pools(const rf_cache* cache, const rf::Batch& b, rf::Pools& p) {
+  if (!cache) return fail(RF_E_INVALID, "cache is NULL");
+  if (cache->type != RF_CACHE_BF16 && cache->type != RF_CACHE_FP8 && cache->type != RF_CACHE_INT8)
+    return fail(RF_E_INVALID, "cache.type = %d", cache->type);
+  if (cache->reserved != 0) return fail(RF_E_INVALID, "cache.reserved must be 0");
+  const bool held = cache->type != RF_CACHE_BF16;
+  if (held && b.hd % 32) return fail(RF_E_SHAPE, "head_dim = %d must be a multiple of 32 for 8 bits", b.hd);
+  if (held != (cache->k_scales != nullptr) || (held && cache->v_pages && !cache->v_scales) || (!held && cache->v_scales))
+    return fail(RF_E_INVALID, "caches of 8 bits have k_scales and v_scales, others have none");
+  if (!cache->k_pages) return fail(RF_E_INVALID, "cache.k_pages is NULL");
+  if (!aligned(cache->k_pages, 16) || !aligned(cache->v_pages, 16) || !aligned(cache->k_scales, 16) ||
+      !aligned(cache->v_scales, 16))
+    return fail(RF_E_SHAPE, "the cache's pools need 16-byte alignment");
+  p = {cache->type, cache->k_pages, cache->v_pages, cache->k_scales, cache->v_scales};
+  return RF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -179,38 +266,14 @@ rf_status ridgefill_append_rows(const rf_rope* rope, const rf_paged_batch* kv, c
   rf::Batch b;
   rf_status s = check_batch(kv, true, b);
   if (s != RF_OK) return s;
-  if (!status || !aligned(status, 4))
-    return fail(RF_E_INVALID, "status must be a 4-byte aligned device pointer");
-  if (n_rows < 0 || n_rows > kMaxRows)
-    return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23", (long long)n_rows);
-  rf::RopeFreq f = {};
-  f.layout = RF_ROPE_HALF;
-  if (rope) {
-    s = make_freq(rope, b.hd, f);
-    if (s != RF_OK) return s;
-  }
-  if (n_q_heads < 0 || n_q_heads > 4096) return fail(RF_E_SHAPE, "n_q_heads = %d must be in 0..4096", n_q_heads);
-  if ((n_q_heads > 0) != (q != nullptr || q_out != nullptr) || (q != nullptr) != (q_out != nullptr)) {
-    if (n_rows > 0 || n_q_heads == 0)
-      return fail(RF_E_INVALID, "q and q_out go together, and with n_q_heads > 0");
-  }
-  const int64_t kw = (int64_t)b.n_kv * b.hd, qw = (int64_t)n_q_heads * b.hd;
-  if (k_stride < kw || v_stride < kw || k_stride % 8 || v_stride % 8)
-    return fail(RF_E_SHAPE, "k_stride and v_stride must be >= n_kv_heads * head_dim and multiples of 8");
-  if (n_q_heads && (q_stride < qw || q_out_stride < qw || q_stride % 8 || q_out_stride % 8))
-    return fail(RF_E_SHAPE, "q_stride and q_out_stride must be >= n_q_heads * head_dim and multiples of 8");
-  if (n_q_heads && q == q_out && q_stride != q_out_stride)
-    return fail(RF_E_INVALID, "rotating q in place needs equal strides");
+  rf::RopeFreq f;
+  s = check_append(rope, b, q, n_q_heads, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, n_rows, seq, rows,
+                   positions, k_pages, v_pages, status, f);
+  if (s != RF_OK) return s;
   if (n_rows == 0) {
     hipError_t e = rf::launch_clear_status(status, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, "status clear");
   }
-  if (!k || !v || !rows || !k_pages || !v_pages || !b.tables)
-    return fail(RF_E_INVALID, "null pointer among k, v, rows, k_pages, v_pages, block_tables");
-  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) ||
-      !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(rows, 4) || !aligned(seq, 4) ||
-      !aligned(positions, 4) || !aligned(b.tables, 4))
-    return fail(RF_E_SHAPE, "q, q_out, k, v and the pages need 16-byte, the index lists 4-byte alignment");
   const rf::AppendCall c = {q, q_out, k, v, k_pages, v_pages, seq, rows, positions, status,
                             n_rows, q_stride, q_out_stride, k_stride, v_stride, n_q_heads};
   hipError_t e = rf::launch_append(f, b, c, static_cast<hipStream_t>(stream));
@@ -323,6 +386,152 @@ rf_status ridgefill_evict_rows(const rf_paged_batch* kv, const rf_layer* layers,
   hipError_t e = rf::launch_evict(b, c, pools, 2 * n_layers, ws, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "eviction launch");
   return ok();
+}
+
+rf_status ridgefill_norm_rope(const rf_rope* rope, const rf_head_norm* norm, int32_t type,
+                              int64_t n_rows, int32_t head_dim, const int32_t* positions,
+                              const void* q, int32_t n_q_heads, int64_t q_stride, void* q_out,
+                              int64_t q_out_stride, const void* k, int32_t n_k_heads,
+                              int64_t k_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  rf::RopeFreq f;
+  rf_status s = check_norm_call(rope, norm, type, n_rows, head_dim, n_q_heads, n_k_heads, f);
+  if (s != RF_OK) return s;
+  const int step = type == RF_TYPE_F32 ? 4 : 8;
+  const rf::NormTensor t[2] = {
+      {q, norm ? norm->q_w : nullptr, nullptr, q_out, nullptr, q_stride, 0, q_out_stride, n_q_heads},
+      {k, norm ? norm->k_w : nullptr, nullptr, k_out, nullptr, k_stride, 0, k_out_stride, n_k_heads}};
+  for (int i = 0; i < 2; ++i) {
+    const char* name = i ? "k" : "q";
+    if ((t[i].x || t[i].out) && !t[i].heads) return fail(RF_E_INVALID, "%s without heads", name);
+    if (!t[i].heads) continue;
+    s = check_heads_of(name, t[i].x, t[i].heads, head_dim, t[i].x_stride, step);
+    if (s == RF_OK) s = check_heads_of(i ? "k_out" : "q_out", t[i].out, t[i].heads, head_dim, t[i].out_stride, step);
+    if (s != RF_OK) return s;
+    if (n_rows > 0 && (!t[i].x || !t[i].out)) return fail(RF_E_INVALID, "%s or its output is NULL", name);
+    if (t[i].x && t[i].x == t[i].out && t[i].x_stride != t[i].out_stride)
+      return fail(RF_E_INVALID, "%s in place needs equal strides", name);
+  }
+  if (n_rows == 0) return ok();
+  if (rope && !positions) return fail(RF_E_INVALID, "positions is NULL");
+  if (!aligned(positions, 4)) return fail(RF_E_SHAPE, "positions needs 4-byte alignment");
+  const rf::NormCall c = {{t[0], t[1]}, positions, n_rows, norm ? norm->eps : 0.f, head_dim};
+  hipError_t e = rf::launch_norm_rope(f, c, type == RF_TYPE_F32, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "norm launch");
+}
+
+size_t ridgefill_norm_rope_grad_workspace_bytes(int64_t n_rows, int32_t n_q_heads,
+                                                int32_t n_k_heads, int32_t head_dim) {
+  rf::RopeFreq f;
+  if (check_norm_call(nullptr, nullptr, RF_TYPE_BF16, n_rows, head_dim, n_q_heads, n_k_heads, f) != RF_OK) return 0;
+  return rf::norm_grad_workspace(n_rows, head_dim);
+}
+
+rf_status ridgefill_norm_rope_grad(const rf_rope* rope, const rf_head_norm* norm, int32_t type,
+                                   int64_t n_rows, int32_t head_dim, const int32_t* positions,
+                                   const void* q, int32_t n_q_heads, int64_t q_stride,
+                                   const void* gq, int64_t gq_stride, void* q_grad,
+                                   int64_t q_grad_stride, float* qw_grad, const void* k,
+                                   int32_t n_k_heads, int64_t k_stride, const void* gk,
+                                   int64_t gk_stride, void* k_grad, int64_t k_grad_stride,
+                                   float* kw_grad, void* ws, size_t ws_bytes, void* stream) {
+  rf::RopeFreq f;
+  rf_status s = check_norm_call(rope, norm, type, n_rows, head_dim, n_q_heads, n_k_heads, f);
+  if (s != RF_OK) return s;
+  const int step = type == RF_TYPE_F32 ? 4 : 8;
+  const rf::NormTensor t[2] = {
+      {q, norm ? norm->q_w : nullptr, gq, q_grad, qw_grad, q_stride, gq_stride, q_grad_stride, n_q_heads},
+      {k, norm ? norm->k_w : nullptr, gk, k_grad, kw_grad, k_stride, gk_stride, k_grad_stride, n_k_heads}};
+  for (int i = 0; i < 2; ++i) {
+    const char* name = i ? "k" : "q";
+    if ((t[i].x || t[i].g || t[i].out || t[i].dw) && !t[i].heads) return fail(RF_E_INVALID, "%s without heads", name);
+    if (!t[i].heads) continue;
+    if (t[i].w) s = check_heads_of(name, t[i].x, t[i].heads, head_dim, t[i].x_stride, step);
+    if (s == RF_OK) s = check_heads_of(i ? "gk" : "gq", t[i].g, t[i].heads, head_dim, t[i].g_stride, step);
+    if (s == RF_OK) s = check_heads_of(i ? "k_grad" : "q_grad", t[i].out, t[i].heads, head_dim, t[i].out_stride, step);
+    if (s != RF_OK) return s;
+    if (!aligned(t[i].dw, 4)) return fail(RF_E_SHAPE, "%sw_grad needs 4-byte alignment", name);
+    if (n_rows > 0 && (!t[i].g || !t[i].out || (t[i].w && !t[i].x)))
+      return fail(RF_E_INVALID, "%s, g%s or %s_grad is NULL", name, name, name);
+    if (t[i].g && t[i].g == t[i].out && t[i].g_stride != t[i].out_stride)
+      return fail(RF_E_INVALID, "%s_grad in place of g%s needs equal strides", name, name);
+  }
+  if (n_rows > 0 && rope && !positions) return fail(RF_E_INVALID, "positions is NULL");
+  if (!aligned(positions, 4)) return fail(RF_E_SHAPE, "positions needs 4-byte alignment");
+  if (!ws) return fail(RF_E_INVALID, "workspace is NULL");
+  if (!aligned(ws, 256)) return fail(RF_E_WORKSPACE, "workspace must be 256-byte aligned");
+  const size_t need = rf::norm_grad_workspace(n_rows, head_dim);
+  if (ws_bytes < need) return fail(RF_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  const rf::NormCall c = {{t[0], t[1]}, positions, n_rows, norm ? norm->eps : 0.f, head_dim};
+  hipError_t e = rf::launch_norm_grad(f, c, type == RF_TYPE_F32, ws, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "norm gradient launch");
+}
+
+rf_status ridgefill_append_cache(const rf_rope* rope, const rf_head_norm* norm,
+                                 const rf_paged_batch* kv, const rf_cache* cache,
+                                 const uint16_t* q, int32_t n_q_heads, int64_t q_stride,
+                                 uint16_t* q_out, int64_t q_out_stride, const uint16_t* k,
+                                 int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                 int64_t n_rows, const int32_t* seq, const int32_t* rows,
+                                 const int32_t* positions, uint32_t* status, void* stream) {
+  rf::Batch b;
+  rf::RopeFreq f;
+  rf::HoldCall c = {};
+  rf_status s = check_batch(kv, true, b);
+  if (s == RF_OK) s = check_pools(cache, b, c.pools);
+  if (s == RF_OK) s = check_norm(norm);
+  if (s == RF_OK)
+    s = check_append(rope, b, q, n_q_heads, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, n_rows, seq, rows,
+                     positions, c.pools.k, c.pools.v, status, f);
+  if (s != RF_OK) return s;
+  if (n_rows == 0) {
+    hipError_t e = rf::launch_clear_status(status, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "status clear");
+  }
+  c.a = {q, q_out, k, v, nullptr, nullptr, seq, rows, positions, status,
+         n_rows, q_stride, q_out_stride, k_stride, v_stride, n_q_heads};
+  c.q_w = norm ? static_cast<const uint16_t*>(norm->q_w) : nullptr;
+  c.k_w = norm ? static_cast<const uint16_t*>(norm->k_w) : nullptr;
+  c.eps = norm ? norm->eps : 0.f;
+  hipError_t e = rf::launch_hold(f, b, c, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "append launch");
+}
+
+rf_status ridgefill_read_rows(const rf_paged_batch* kv, const rf_cache* cache, int64_t n_rows,
+                              const int32_t* seq, const int32_t* rows, int32_t type, void* k_out,
+                              int64_t k_out_stride, void* v_out, int64_t v_out_stride,
+                              uint32_t* status, void* stream) {
+  rf::Batch b;
+  rf::ReadCall c = {};
+  rf_status s = check_batch(kv, true, b);
+  if (s == RF_OK) s = check_pools(cache, b, c.pools);
+  if (s != RF_OK) return s;
+  if (type != RF_TYPE_BF16 && type != RF_TYPE_F32) return fail(RF_E_INVALID, "type = %d", type);
+  if (!status || !aligned(status, 4))
+    return fail(RF_E_INVALID, "status must be a 4-byte aligned device pointer");
+  if (n_rows < 0 || n_rows > kMaxRows || n_rows * b.n_kv * b.hd > (int64_t)1 << 34)
+    return fail(RF_E_SHAPE, "n_rows = %lld must be in 0..2^23, n_rows * n_kv_heads * head_dim at most 2^34", (long long)n_rows);
+  const int step = type == RF_TYPE_F32 ? 4 : 8;
+  if (k_out) s = check_heads_of("k_out", k_out, b.n_kv, b.hd, k_out_stride, step);
+  if (s == RF_OK && v_out) s = check_heads_of("v_out", v_out, b.n_kv, b.hd, v_out_stride, step);
+  if (s != RF_OK) return s;
+  if (n_rows == 0) {
+    hipError_t e = rf::launch_clear_status(status, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "status clear");
+  }
+  if (!rows || !b.tables || (!k_out && !v_out) || (v_out && !c.pools.v))
+    return fail(RF_E_INVALID, "null pointer among rows, block_tables, v_pages, or no output");
+  if (!aligned(rows, 4) || !aligned(seq, 4) || !aligned(b.tables, 4))
+    return fail(RF_E_SHAPE, "the index lists need 4-byte alignment");
+  c.k_out = k_out;
+  c.v_out = v_out;
+  c.seq = seq;
+  c.rows = rows;
+  c.status = status;
+  c.n = n_rows;
+  c.k_stride = k_out_stride;
+  c.v_stride = v_out_stride;
+  hipError_t e = rf::launch_read(b, c, type == RF_TYPE_F32, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "read launch");
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // Internal interface between the C entry points of the cache calls (rf_cache.cpp) and their
-// kernels (rf_rope.hip, rf_attend.hip, rf_weight.hip, rf_evict.hip).
+// kernels (rf_rope.hip, rf_norm.hip, rf_attend.hip, rf_weight.hip, rf_evict.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -70,6 +70,56 @@ size_t weight_workspace(const Batch& b, int n_heads, int max_q);
 hipError_t launch_weight(const Batch& b, const uint16_t* kp, const Queries& q, const float* lse,
                          float decay, const float* acc, float* acc_out, int64_t acc_stride,
                          void* ws, hipStream_t stream);
+
+// Host-side copy of rf_cache: one layer's pools and how they hold their values.
+struct Pools {
+  int type;
+  void* k;
+  void* v;
+  uint8_t* ks;
+  uint8_t* vs;
+};
+
+// Norms of heads with their rotation.  Tensor 0 is q, tensor 1 k (heads 0 where it is not given).
+struct NormTensor {
+  const void* x;
+  const void* w;                // [hd], of x's type, or null: not normed
+  const void* g;                // backward: the gradient of the outputs
+  void* out;                    // the outputs; backward: the gradient of x
+  float* dw;                    // backward: the gradient of w
+  int64_t x_stride, g_stride, out_stride;
+  int heads;
+};
+struct NormCall {
+  NormTensor t[2];
+  const int32_t* pos;
+  int64_t n;
+  float eps;
+  int hd;
+};
+hipError_t launch_norm_rope(const RopeFreq& f, const NormCall& c, bool f32, hipStream_t stream);
+size_t norm_grad_workspace(int64_t n, int hd);
+hipError_t launch_norm_grad(const RopeFreq& f, const NormCall& c, bool f32, void* ws, hipStream_t stream);
+
+// The append of normed, rotated rows to a cache of any type; the rows' values back.
+struct HoldCall {
+  AppendCall a;                 // kp and vp are not used
+  Pools pools;
+  const uint16_t* q_w;
+  const uint16_t* k_w;
+  float eps;
+};
+hipError_t launch_hold(const RopeFreq& f, const Batch& b, const HoldCall& c, hipStream_t stream);
+struct ReadCall {
+  Pools pools;
+  void* k_out;
+  void* v_out;
+  const int32_t* seq;
+  const int32_t* rows;
+  unsigned* status;
+  int64_t n, k_stride, v_stride;
+};
+hipError_t launch_read(const Batch& b, const ReadCall& c, bool f32, hipStream_t stream);
 
 constexpr int kEvictPools = 128;   // page pools moved by one launch
 struct EvictPools {

@@ -1,0 +1,77 @@
+// How a cache holds its values (rf_cache.type): bf16 as they are, or codes of 8 bits in blocks of 32
+// features that share a power of two, as the OCP microscaling formats do.  For a block whose largest
+// magnitude is top, the exponent e is the smallest with top <= M 2^e (M = 448 for e4m3, 127 for int8),
+// kept to -110 .. 118; a code is the nearest value of its type (ties to even) to x 2^-e, and stands for
+// code 2^e; the scale byte is e + 127.  These values have at most eight significant bits and are
+// normal numbers of bf16, so that a bf16 operand of the matrix cores holds each exactly, and whatever
+// reads such a cache computes what it would from a bf16 cache of them.  A block that holds an infinity
+// or NaN is NaN altogether: scale byte 255.
+#pragma once
+
+#include "rf_common.h"
+#include "ridgefill.h"
+
+namespace rf {
+
+constexpr int kBlock = 32;
+constexpr int kScaleLeast = 17, kScaleMost = 245, kScaleNan = 255;
+
+// The scale byte of a block, from the bits of its largest magnitude.
+template <int kType>
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return kScaleNan;
+  // top = (1 + m 2^-23) 2^k; 448 = 1.75 2^8, 127 = 1.984375 2^6
+  const int k = (int)(top >> 23), m = (int)(top & 0x7fffffu);
+  const int e = kType == RF_CACHE_FP8 ? k - 8 + (m > 0x600000) : k - 6 + (m > 0x7e0000);
+  return e < kScaleLeast ? kScaleLeast : e > kScaleMost ? kScaleMost : e;
+}
+
+// Codes of eight values of a block with this scale byte.
+template <int kType>
+__device__ __forceinline__ u32x2 codes_of(const float (&x)[8], int byte) {
+  const float inv = __uint_as_float((unsigned)(254 - byte) << 23);
+  u32x2 w = {0u, 0u};
+  if (byte == kScaleNan) return kType == RF_CACHE_FP8 ? u32x2{0x7f7f7f7fu, 0x7f7f7f7fu} : w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // values of a block whose exponent is cut to 118 stay finite
+      const float most = kType == RF_CACHE_FP8 ? 448.f : 127.f;
+      y[i] = fminf(fmaxf(x[4 * h + i] * inv, -most), most);
+    }
+    if constexpr (kType == RF_CACHE_FP8) {
+      int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+      w[h] = (unsigned)c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[h] |= ((unsigned)(int)rintf(y[i]) & 0xffu) << (8 * i);
+    }
+  }
+  return w;
+}
+
+// The factor of a block's codes: 2^(byte - 127), infinity for a NaN block (which makes any code NaN in
+// both conversions below).
+__device__ __forceinline__ float scale_of(unsigned byte) { return __uint_as_float(byte << 23); }
+
+// The values of four codes as bf16 pairs.  e4m3: one instruction for two codes, exact for the scale
+// bytes above.  int8: code + 128 as a float, then (code + 128) s - 128 s in one step, exact too.
+template <int kType>
+__device__ __forceinline__ u32x2 values_of(unsigned w, float s) {
+  if constexpr (kType == RF_CACHE_FP8) {
+    return {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)),
+            __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))};
+  } else {
+    const unsigned u = w ^ 0x80808080u;
+    const float off = -128.f * s;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fmaf((float)(u >> (8 * i) & 0xffu), s, off);
+    return {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  }
+}
+
+}  // namespace rf

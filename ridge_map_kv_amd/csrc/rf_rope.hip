@@ -11,73 +11,13 @@
 // neighbouring pieces; its first units are on their way while cos and sin are formed.  Measured:
 // 8,191 rows of 32 fp32 heads of 128 in 48 us, 5.6 TB/s; 4,096 rows of 32 query and 8 key heads of
 // 128 appended in 23 us, 4.4 TB/s (reads and writes of 100 MB, a large copy's rate 4.9 to 5.5).
-#include "rf_cache_dev.h"
-#include "ridgefill.h"
+#include "rf_rope_dev.h"
 
 namespace rf {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// 16 bytes of a head: 8 (bf16) or 4 (fp32) features.
-template <typename T>
-struct Piece;
-template <>
-struct Piece<uint16_t> {
-  static constexpr int kN = 8;
-  u32x4 r;
-  __device__ void get(float (&f)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_to_f32(r[i] & 0xffffu);
-      f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-    }
-  }
-  __device__ void set(const float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-  }
-};
-template <>
-struct Piece<float> {
-  static constexpr int kN = 4;
-  u32x4 r;
-  __device__ void get(float (&f)[4]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
-  }
-  __device__ void set(const float (&f)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(f[i]);
-  }
-};
-
-// cos and sin of `pos` at pair j, times m.
-__device__ __forceinline__ float2 turn_of(const RopeFreq& f, int j, int pos, float sign) {
-  double t = (double)pos * f.turns[j];
-  t -= rint(t);
-  float s, c;
-  sincospif(2.0f * (float)t, &s, &c);
-  return make_float2(f.m * c, sign * f.m * s);
-}
-
-// Where the two pieces of unit u of a head lie, and the first pair of each when they rotate.  Units
-// past the rotated part pass unchanged (pair < 0).
-struct Unit {
-  int lo, hi, pair_lo, pair_hi;
-};
-template <typename T>
-__device__ __forceinline__ Unit unit_of(const RopeFreq& f, int hd, int u) {
-  constexpr int kN = Piece<T>::kN;
-  const int turned = f.rot / (2 * kN), half = f.rot / 2;
-  if (u >= turned) {
-    const int lo = f.rot + (u - turned) * kN;
-    return {lo, lo + (hd - f.rot) / 2, -1, -1};
-  }
-  if (f.layout == RF_ROPE_HALF) return {u * kN, half + u * kN, u * kN, u * kN};
-  return {u * kN, half + u * kN, u * kN / 2, (half + u * kN) / 2};
-}
 
 template <typename T>
 __device__ __forceinline__ void turn_unit(Piece<T>& lo, Piece<T>& hi, const float2* cs, const Unit& u,
@@ -86,25 +26,7 @@ __device__ __forceinline__ void turn_unit(Piece<T>& lo, Piece<T>& hi, const floa
   float a[kN], b[kN];
   lo.get(a);
   hi.get(b);
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
-      const float2 p = cs[u.pair_lo + i], q = cs[u.pair_hi + i];
-      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * p.x - a1 * p.y;
-      a[2 * i + 1] = a1 * p.x + a0 * p.y;
-      b[2 * i] = b0 * q.x - b1 * q.y;
-      b[2 * i + 1] = b1 * q.x + b0 * q.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float2 p = cs[u.pair_lo + i];
-      const float x = a[i], y = b[i];
-      a[i] = x * p.x - y * p.y;
-      b[i] = y * p.x + x * p.y;
-    }
-  }
+  turn_values<kN>(a, b, cs, u, interleaved);
   lo.set(a);
   hi.set(b);
 }
@@ -180,15 +102,6 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeFreq f, RopeCall c, 
       });
 }
 
-// Pool slot of cache row `row` of sequence `seq`, or -1 if any of them is out of range (then the
-// table's first entry is looked at instead: no branch keeps several lookups from running together).
-__device__ __forceinline__ int append_slot(const Batch& b, Divide by_page, int seq, int row) {
-  const bool in = seq < b.batch && row >= 0 && row < b.max_len;
-  const int pi = in ? (int)quotient((unsigned)row, by_page) : 0;
-  const int page = b.tables[(int64_t)(in ? seq : 0) * b.table_stride + pi];
-  return in && page >= 0 && page < b.num_pages ? page * b.page_size + (row - pi * b.page_size) : -1;
-}
-
 // The same for the append: heads 0 .. n_q-1 of a row are q, then k (rotated into the key
 // pages), then v (copied).  With kScan the first workgroup writes the status word: it alone looks
 // all rows over, beside the others' work, so that the word needs no clearing launch; else it is clear,
@@ -197,24 +110,7 @@ template <bool kScan>
 __global__ __launch_bounds__(kThreads) void append_kernel(RopeFreq f, Batch b, AppendCall c,
                                                           Units d, int per) {
   extern __shared__ float2 cs[];                    // [per][rot / 2], then the rows' slots
-  if (kScan && blockIdx.x == 0) {
-    int bad = 0;
-    for (int64_t i0 = threadIdx.x; i0 < c.n; i0 += 8 * kThreads) {   // eight lookups at a time
-      int slot[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t i = i0 + j * kThreads < c.n ? i0 + j * kThreads : i0;
-        const int s = c.seq ? c.seq[i] : 0;
-        const int at = append_slot(b, d.page, s < 0 ? 0 : s, c.rows[i]);
-        slot[j] = s < 0 ? 0 : at;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bad |= slot[j] < 0;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *c.status = bad ? kStatusRowsBit : 0u;
-    return;
-  }
+  if (kScan && blockIdx.x == 0) return scan_rows(b, d.page, c.seq, c.rows, c.n, c.status);
   const int64_t row0 = (int64_t)(blockIdx.x - kScan) * per;
   const int rows = (int)(c.n - row0 < per ? c.n - row0 : per);
   const int pairs = f.rot / 2;
