@@ -742,6 +742,43 @@ rf_status ridgefill_read_rows(const rf_paged_batch* kv, const rf_cache* cache, i
                               int64_t k_out_stride, void* v_out, int64_t v_out_stride,
                               uint32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Attention over a cache of any type, also of sequences that share long prefixes (one prompt,
+ * filled once, under many answers).  Queries, q_start, max_q, tree_mask, scale, out and lse as in
+ * ridgefill_tree_attention; kv->lengths and its block tables are the sequences' own rows.  With
+ * `prefix`, sequences group_start[g] .. group_start[g+1]-1 all see the lengths[g] rows of prefix g
+ * before their own: one softmax over both.  A prefix's rows are read once for all its queries (for
+ * every 256 rows of the matrix of queries and query heads that share a key head).  Sequences before
+ * group_start[0] and from group_start[groups] on have no prefix.
+ * ------------------------------------------------------------------------------ */
+typedef struct rf_prefix {
+  const int32_t* block_tables;  /* device int32 [groups][table_stride]: pages of the same pools */
+  const int32_t* lengths;       /* device int32 [groups]: rows of each prefix, 0 .. max_len   */
+  const int32_t* group_start;   /* device int32 [groups + 1], ascending, within 0 .. batch    */
+  int64_t table_stride;         /* >= ceil(max_len / kv->page_size)                           */
+  int32_t groups;               /* 1 .. 65535; groups * n_kv_heads <= 2^22                    */
+  int32_t max_len;              /* 1 .. 2^30: the host's bound on the lengths                 */
+} rf_prefix;
+
+/*   prefix      NULL: sequences of their own rows alone, which over a bf16 cache is
+ *               ridgefill_tree_attention
+ *   cache       v_pages (and v_scales) may be NULL with out
+ *   n_q         with a prefix batch * n_q_heads * max_q <= 2^25
+ *   ws          >= ridgefill_cache_attention_workspace_bytes(kv, prefix, n_q_heads, max_q, n_q), of
+ *               which the pointers in kv and prefix are not read; 256-byte aligned; its first 256
+ *               bytes hold the status
+ * A group whose length or sequences are out of range, or whose queries are out of order or more
+ * than max_q for each sequence, sets RF_E_ROWS, and its sequences are skipped; where groups overlap,
+ * a sequence belongs to the first.  Precision and repeatability as in ridgefill_tree_attention. */
+size_t ridgefill_cache_attention_workspace_bytes(const rf_paged_batch* kv, const rf_prefix* prefix,
+                                                 int32_t n_q_heads, int32_t max_q, int64_t n_q);
+rf_status ridgefill_cache_attention(const rf_paged_batch* kv, const rf_prefix* prefix,
+                                    const rf_cache* cache, const uint16_t* q, int32_t n_q_heads,
+                                    int64_t q_stride, const int32_t* q_start, int64_t n_q,
+                                    int32_t max_q, const uint64_t* tree_mask, float scale,
+                                    uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream);
+
 /* Waits for `stream`, then returns the device status word of a fill, solve or selection
  * workspace, or of a cache call's workspace or status word: RF_OK, RF_E_ROWS, RF_E_NOT_SPD,
  * RF_E_WORKSPACE for a solve on a calibration state whose header disagrees with the solve's

@@ -58,6 +58,8 @@ EXPORTED = [
     "ridgefill_norm_rope_grad",
     "ridgefill_append_cache",
     "ridgefill_read_rows",
+    "ridgefill_cache_attention_workspace_bytes",
+    "ridgefill_cache_attention",
     "ridgefill_read_status",
     "ridgefill_solve_info",
     "ridgefill_profile_enable",
@@ -116,6 +118,11 @@ class rf_head_norm(C.Structure):
 class rf_cache(C.Structure):
     _fields_ = [("type", C.c_int32), ("reserved", C.c_int32), ("k_pages", C.c_void_p),
                 ("v_pages", C.c_void_p), ("k_scales", C.c_void_p), ("v_scales", C.c_void_p)]
+
+
+class rf_prefix(C.Structure):
+    _fields_ = [("block_tables", C.c_void_p), ("lengths", C.c_void_p), ("group_start", C.c_void_p),
+                ("table_stride", C.c_int64), ("groups", C.c_int32), ("max_len", C.c_int32)]
 
 
 RF_ROPE_HALF, RF_ROPE_INTERLEAVED = range(2)
@@ -190,6 +197,9 @@ def lib() -> C.CDLL:
         "ridgefill_append_cache": (st, [vp, vp, vp, vp, vp, i32, i64, vp, i64, vp, i64, vp, i64, i64,
                                         vp, vp, vp, vp, vp]),
         "ridgefill_read_rows": (st, [vp, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, vp]),
+        "ridgefill_cache_attention_workspace_bytes": (sz, [vp, vp, i32, i32, i64]),
+        "ridgefill_cache_attention": (st, [vp, vp, vp, vp, i32, i64, vp, i64, i32, vp, C.c_float, vp, i64,
+                                           vp, vp, sz, vp]),
         "ridgefill_read_status": (st, [vp, vp]),
         "ridgefill_solve_info": (st, [vp, C.POINTER(C.c_double), C.POINTER(i32), vp]),
         "ridgefill_profile_enable": (st, [i32]),
@@ -560,7 +570,8 @@ def _queries(kv: rf_paged_batch, k_pages, q, q_start, max_q, tree_mask, lse, ws)
     if kv._keep[1] is None:
         raise ValueError("the batch was made without lengths")
     stride = _rows_of("q", q, torch.bfloat16, dev, kv.head_dim)
-    _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
+    if k_pages is not None:
+        _flat("k_pages", k_pages, torch.bfloat16, dev, 4, kv._pool)
     _flat("q_start", q_start, torch.int32, dev, 1, (kv.batch + 1,))
     n, heads = q.shape[0], q.shape[1]
     if tree_mask is not None:
@@ -816,6 +827,57 @@ def ridgefill_read_rows(kv: rf_paged_batch, cache: rf_cache, rows, status, seq=N
     _go(lib().ridgefill_read_rows, dev, stream, C.byref(kv), C.byref(cache), n, _ptr(seq), rows.data_ptr(),
         RF_TYPE_F32 if dtype is torch.float32 else RF_TYPE_BF16, _ptr(k_out), strides[0], _ptr(v_out), strides[1],
         status.data_ptr())
+
+
+def make_prefix(block_tables, lengths, group_start, max_len: int) -> rf_prefix:
+    """Prefixes that groups of sequences share: block_tables int32 [groups][pages], lengths int32
+    [groups], group_start int32 [groups + 1] (the groups' sequences, ascending); max_len bounds the
+    lengths.  It keeps the tensors alive."""
+    import torch
+    dev = block_tables.device
+    _need("block_tables", block_tables, torch.int32, dev, 2)
+    groups, per = block_tables.shape
+    if block_tables.stride(1) != 1 and per > 1:
+        raise ValueError("the entries of a block table must lie in one piece")
+    _flat("lengths", lengths, torch.int32, dev, 1, (groups,))
+    _flat("group_start", group_start, torch.int32, dev, 1, (groups + 1,))
+    _ints(max_len=max_len, groups=groups)
+    prefix = rf_prefix(block_tables.data_ptr(), lengths.data_ptr(), group_start.data_ptr(),
+                       block_tables.stride(0) if groups > 1 else per, groups, max_len)
+    prefix._keep = (block_tables, lengths, group_start)
+    prefix._per, prefix._device = per, dev
+    return prefix
+
+
+def ridgefill_cache_attention_workspace_bytes(kv: rf_paged_batch, n_q_heads: int, max_q: int, n_q: int,
+                                              prefix: rf_prefix | None = None) -> int:
+    if not _fits(n_q_heads, max_q, n_q):
+        return 0
+    return int(lib().ridgefill_cache_attention_workspace_bytes(C.byref(kv), None if prefix is None else C.byref(prefix),
+                                                               n_q_heads, max_q, n_q))
+
+
+def ridgefill_cache_attention(kv: rf_paged_batch, cache: rf_cache, q, q_start, max_q: int, scale: float, out, ws,
+                              prefix: rf_prefix | None = None, lse=None, tree_mask=None, stream=None) -> None:
+    """ridgefill_tree_attention over a cache of any type (from make_cache); with `prefix` (from
+    make_prefix) the sequences of a group see their prefix's rows before their own."""
+    _cache_of(kv, cache)
+    qs = _queries(kv, None, q, q_start, max_q, tree_mask, lse, ws)
+    os_ = 0
+    if out is not None:
+        if cache._keep[1] is None:
+            raise ValueError("out, and the cache was made without v_pages")
+        os_ = _rows_of("out", out, q.dtype, kv._device, kv.head_dim, q.shape[0])
+        if out.shape[1] != q.shape[1]:
+            raise ValueError(f"out has {out.shape[1]} heads, q {q.shape[1]}")
+    if prefix is not None:
+        if prefix._device != kv._device:
+            raise ValueError(f"the prefix's tables are on {prefix._device}, the batch's on {kv._device}")
+        if prefix._per * kv.page_size < prefix.max_len:
+            raise ValueError(f"a prefix's table of {prefix._per} pages holds fewer than max_len = {prefix.max_len} rows")
+    _go(lib().ridgefill_cache_attention, kv._device, stream, C.byref(kv), None if prefix is None else C.byref(prefix),
+        C.byref(cache), q.data_ptr(), q.shape[1], qs, q_start.data_ptr(), q.shape[0], max_q, _ptr(tree_mask), scale,
+        _ptr(out), os_, _ptr(lse), ws.data_ptr(), _nbytes(ws))
 
 
 # ------------------------------------------------------------------------------ calibration

@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libridgefill.so")
 
 SOURCES = ["rf_fill.hip", "rf_calib.hip", "rf_solve.hip", "rf_select.hip", "rf_fold.hip",
-           "rf_rope.hip", "rf_norm.hip", "rf_attend.hip", "rf_weight.hip", "rf_evict.hip", "ridgefill.cpp",
+           "rf_attend.hip", "rf_attend_shared.hip", "rf_attend_fp8.hip", "rf_attend_int8.hip",
+           "rf_rope.hip", "rf_norm.hip", "rf_weight.hip", "rf_evict.hip", "ridgefill.cpp",
            "rf_cache.cpp", "rf_profile.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -49,7 +50,7 @@ def build(extra: list[str] | None = None, verbose: bool = False) -> str:
     """Compile every source and link the shared library; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
-    with cf.ThreadPoolExecutor(max_workers=min(5, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]

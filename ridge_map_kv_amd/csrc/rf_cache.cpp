@@ -221,6 +221,23 @@ rf_status check_pools(const rf_cache* cache, const rf::Batch& b, rf::Pools& p) {
   return RF_OK;
 }
 
+constexpr int64_t kMaxSharedQueries = 1 << 25;   // batch * query heads * max_q of a call with prefixes
+
+// The prefixes of a batch, and that its queries fit a call with them.
+rf_status check_prefix(const rf_prefix* pre, const rf::Batch& b, int n_q_heads, int max_q, rf::PrefixCall& p) {
+  if (pre->groups < 1 || pre->groups > 65535 || (int64_t)pre->groups * b.n_kv > 1 << 22)
+    return fail(RF_E_SHAPE, "prefix.groups = %d must be in 1..65535, times n_kv_heads at most 2^22", pre->groups);
+  if (pre->max_len < 1 || pre->max_len > 1 << 30)
+    return fail(RF_E_SHAPE, "prefix.max_len = %d must be in 1..2^30", pre->max_len);
+  if (pre->table_stride < ((int64_t)pre->max_len + b.page_size - 1) / b.page_size)
+    return fail(RF_E_SHAPE, "prefix.table_stride = %lld holds fewer than max_len = %d rows",
+                (long long)pre->table_stride, pre->max_len);
+  if ((int64_t)b.batch * n_q_heads * max_q > kMaxSharedQueries)
+    return fail(RF_E_SHAPE, "batch * n_q_heads * max_q must be at most 2^25 with a prefix");
+  p = {pre->block_tables, pre->lengths, pre->group_start, pre->table_stride, pre->groups, pre->max_len};
+  return RF_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -532,6 +549,50 @@ rf_status ridgefill_read_rows(const rf_paged_batch* kv, const rf_cache* cache, i
   c.v_stride = v_out_stride;
   hipError_t e = rf::launch_read(b, c, type == RF_TYPE_F32, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "read launch");
+}
+
+size_t ridgefill_cache_attention_workspace_bytes(const rf_paged_batch* kv, const rf_prefix* prefix,
+                                                 int32_t n_q_heads, int32_t max_q, int64_t n_q) {
+  rf::Batch b;
+  rf::PrefixCall p;
+  if (check_batch(kv, false, b) != RF_OK || check_heads(b, n_q_heads, max_q) != RF_OK || n_q < 0 || n_q > INT32_MAX ||
+      (prefix && check_prefix(prefix, b, n_q_heads, max_q, p) != RF_OK))
+    return 0;
+  return rf::cache_attend_workspace(b, prefix ? &p : nullptr, n_q_heads, max_q, n_q);
+}
+
+rf_status ridgefill_cache_attention(const rf_paged_batch* kv, const rf_prefix* prefix,
+                                    const rf_cache* cache, const uint16_t* q, int32_t n_q_heads,
+                                    int64_t q_stride, const int32_t* q_start, int64_t n_q,
+                                    int32_t max_q, const uint64_t* tree_mask, float scale,
+                                    uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  rf::Batch b;
+  rf::Pools pools;
+  rf::PrefixCall p = {};
+  rf_status s = check_batch(kv, false, b);
+  if (s == RF_OK) s = check_pools(cache, b, pools);
+  if (s == RF_OK)
+    s = check_queries(b, q, n_q_heads, q_stride, q_start, n_q, max_q, tree_mask, scale);
+  if (s == RF_OK && prefix) s = check_prefix(prefix, b, n_q_heads, max_q, p);
+  if (s == RF_OK)
+    s = check_memory(b, ws, ws_bytes, rf::cache_attend_workspace(b, prefix ? &p : nullptr, n_q_heads, max_q, n_q));
+  if (s != RF_OK) return s;
+  if (prefix) {
+    if (!p.tables || !p.lengths || !p.starts)
+      return fail(RF_E_INVALID, "prefix: block_tables, lengths or group_start is NULL");
+    if (!aligned(p.tables, 4) || !aligned(p.lengths, 4) || !aligned(p.starts, 4))
+      return fail(RF_E_SHAPE, "prefix: block_tables, lengths and group_start need 4-byte alignment");
+  }
+  if ((!out && !lse && n_q > 0) || (out && !pools.v))
+    return fail(RF_E_INVALID, "one of out and lse, and with out cache.v_pages are required");
+  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(RF_E_SHAPE, "out needs 16-byte, lse 4-byte alignment");
+  if (out && (out_stride < (int64_t)n_q_heads * b.hd || out_stride % 8))
+    return fail(RF_E_SHAPE, "out_stride must be >= n_q_heads * head_dim and a multiple of 8");
+  const rf::Queries Q = {q, q_start, tree_mask, q_stride, n_q, n_q_heads, max_q, scale};
+  hipError_t e = rf::launch_cache_attend(b, prefix ? &p : nullptr, pools, Q, out, out_stride, lse, ws,
+                                         static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
 }
 
 }  // extern "C"

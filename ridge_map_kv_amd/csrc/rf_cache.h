@@ -80,6 +80,18 @@ struct Pools {
   uint8_t* vs;
 };
 
+// Host-side copy of rf_prefix.
+struct PrefixCall {
+  const int32_t* tables;
+  const int32_t* lengths;
+  const int32_t* starts;
+  int64_t table_stride;
+  int groups, max_len;
+};
+size_t cache_attend_workspace(const Batch& b, const PrefixCall* prefix, int n_heads, int max_q, int64_t n_q);
+hipError_t launch_cache_attend(const Batch& b, const PrefixCall* prefix, const Pools& pools, const Queries& q,
+                               uint16_t* out, int64_t out_stride, float* lse, void* ws, hipStream_t stream);
+
 // Norms of heads with their rotation.  Tensor 0 is q, tensor 1 k (heads 0 where it is not given).
 struct NormTensor {
   const void* x;

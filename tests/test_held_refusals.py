@@ -212,3 +212,83 @@ def test_plain_blocks(kind):
         assert torch.equal((code * f[..., None]).flatten(-2), want)
     else:
         assert ((want - x.double()).abs().unflatten(-1, (-1, 32)) <= 0.5 * f[..., None]).all()
+
+
+# ------------------------------------------------------------------------------ attention
+
+def _prefix(tables=FAKE, lengths=FAKE, starts=FAKE, stride=8, groups=2, max_len=100):
+    return B.rf_prefix(tables, lengths, starts, stride, groups, max_len)
+
+
+def _attend(kv=None, prefix=None, cache=None, q=FAKE, heads=4, qs=256, start=FAKE, n=3, max_q=2, mask=None, scale=0.1, out=FAKE,
+            os_=256, lse=FAKE, ws=FAKE, ws_bytes=1 << 30):
+    return B.lib().ridgefill_cache_attention(C.byref(kv or _kv()), C.byref(prefix) if prefix else None, C.byref(cache or _cache()), q,
+                                             heads, qs, start, n, max_q, mask, scale, out, os_, lse, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_attention_refusals(shared):
+    pre = dict(prefix=_prefix()) if shared else {}
+    for kw in BAD_KV + [dict(head_dim=32), dict(head_dim=96), dict(head_dim=256)]:
+        _refused(_attend(kv=_kv(**kw), **pre), B.RF_E_SHAPE)
+    for kw in (dict(kind=3), dict(reserved=1), dict(kp=None), dict(vp=None), dict(ks=FAKE), dict(vs=FAKE), dict(kind=1),
+               dict(kind=2, ks=FAKE), dict(kind=2, vs=FAKE)):
+        _refused(_attend(cache=_cache(**kw), **pre), B.RF_E_INVALID)
+    for kw in (dict(kp=FAKE + 8), dict(vp=FAKE + 2), dict(HELD, ks=FAKE + 4), dict(HELD, vs=FAKE + 1)):
+        _refused(_attend(cache=_cache(**kw), **pre), B.RF_E_SHAPE)
+    for kw in (dict(heads=0), dict(heads=3), dict(heads=4098), dict(max_q=0), dict(max_q=65), dict(n=-1), dict(n=1 << 31), dict(qs=248),
+               dict(qs=260), dict(q=FAKE + 8), dict(start=FAKE + 2), dict(mask=FAKE + 4), dict(lse=FAKE + 2), dict(os_=248), dict(os_=257),
+               dict(out=FAKE + 8), dict(kv=_kv(lengths=FAKE + 2)), dict(kv=_kv(batch=1 << 14), heads=4096, qs=1 << 18, os_=1 << 18)):
+        _refused(_attend(**kw, **pre), B.RF_E_SHAPE)
+    for kw in (dict(q=None), dict(start=None), dict(scale=float("nan")), dict(scale=float("inf")), dict(ws=None), dict(out=None, lse=None),
+               dict(kv=_kv(lengths=None)), dict(kv=_kv(block_tables=None))):
+        _refused(_attend(**kw, **pre), B.RF_E_INVALID)
+    for kw in (dict(ws=FAKE + 64), dict(ws_bytes=255)):
+        _refused(_attend(**kw, **pre), B.RF_E_WORKSPACE)
+
+
+def test_prefix_refusals():
+    for kw in (dict(groups=0), dict(groups=65536), dict(max_len=0), dict(max_len=(1 << 30) + 1, stride=1 << 27), dict(stride=6),
+               dict(tables=FAKE + 2), dict(lengths=FAKE + 1), dict(starts=FAKE + 2)):
+        _refused(_attend(prefix=_prefix(**kw)), B.RF_E_SHAPE)
+    for kw in (dict(tables=None), dict(lengths=None), dict(starts=None)):
+        _refused(_attend(prefix=_prefix(**kw)), B.RF_E_INVALID)
+    # many groups of many key heads; many queries
+    _refused(_attend(prefix=_prefix(groups=1 << 15), kv=_kv(n_kv_heads=256), heads=256, qs=1 << 14, os_=1 << 14), B.RF_E_SHAPE)
+    _refused(_attend(prefix=_prefix(), kv=_kv(batch=1 << 13), heads=4096, max_q=2, qs=1 << 18, os_=1 << 18, ws_bytes=1 << 60), B.RF_E_SHAPE)
+    need = B.ridgefill_cache_attention_workspace_bytes(_kv(), 4, 2, 3, _prefix())
+    _refused(_attend(prefix=_prefix(), ws_bytes=need - 1), B.RF_E_WORKSPACE)
+
+
+def test_attention_workspace():
+    size = B.ridgefill_cache_attention_workspace_bytes
+    assert size(_kv(), 4, 2, 3) == B.ridgefill_tree_attention_workspace_bytes(_kv(), 4, 2) > 0
+    assert size(_kv(), 4, 2, 3, _prefix()) > size(_kv(), 4, 2, 3)
+    # more queries than the sequences can have need no more
+    assert size(_kv(), 4, 2, 1 << 30, _prefix()) == size(_kv(), 4, 2, 4, _prefix())
+    for args in ((4, 2, -1), (4, 65, 3), (3, 2, 3), (4, 2, 1 << 31), (1 << 33, 2, 3), (4, 1 << 32, 3)):
+        assert size(_kv(), *args) == 0 and size(_kv(), *args, _prefix()) == 0
+    assert size(_kv(), 4, 2, 3, _prefix(groups=0)) == 0 and size(_kv(head_dim=96), 4, 2, 3) == 0
+
+
+def test_attention_binding_refusals():
+    kv = B.make_batch(_i32(2, 8), _i32(2), 16, 20, 2, 64, 100)
+    pool, q, ws = _bf(20, 16, 2, 64), _bf(3, 4, 64), torch.zeros(1 << 20, dtype=torch.uint8)
+    cache = B.make_cache(pool, pool)
+    ok = B.make_prefix(_i32(2, 8), _i32(2), _i32(3), 100)
+    assert ok.groups == 2 and ok.table_stride == 8
+    call = lambda **kw: B.ridgefill_cache_attention(kv, kw.pop("cache", cache), kw.pop("q", q), kw.pop("start", _i32(3)), kw.pop("max_q", 2),  # noqa: E731
+                                                    0.1, kw.pop("out", q), kw.pop("ws", ws), **kw)
+    for bad, text in ((lambda: B.make_prefix(_i32(2, 8), _i32(3), _i32(3), 100), "lengths"),
+                      (lambda: B.make_prefix(_i32(2, 8), _i32(2), _i32(2), 100), "group_start"),
+                      (lambda: B.make_prefix(_i32(2, 16)[:, ::2], _i32(2), _i32(3), 100), "block table"),
+                      (lambda: B.make_prefix(_i32(2, 8).long(), _i32(2), _i32(3), 100), "block_tables"),
+                      (lambda: B.make_prefix(_i32(2, 8), _i32(2), _i32(3), 1 << 32), "32 bits"),
+                      (lambda: call(prefix=B.make_prefix(_i32(2, 8), _i32(2), _i32(3), 129)), "129"),
+                      (lambda: call(max_q=1 << 32), "32 bits"), (lambda: call(cache=B.make_cache(pool, None)), "v_pages"),
+                      (lambda: call(cache=B.make_cache(pool[:10], pool[:10])), "pools"), (lambda: call(out=_bf(3, 2, 64)), "heads"),
+                      (lambda: call(start=_i32(4)), "q_start"), (lambda: call(lse=torch.zeros(3, 2)), "lse"),
+                      (lambda: call(tree_mask=_i32(3)), "tree_mask"), (lambda: call(q=q.float()), "q "),
+                      (lambda: call(ws=ws[::2]), "workspace"), (lambda: call(prefix=ok), "GPU memory")):
+        with pytest.raises(ValueError, match=text):
+            bad()
