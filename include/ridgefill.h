@@ -702,10 +702,11 @@ rf_status ridgefill_norm_rope_grad(const rf_rope* rope, const rf_head_norm* norm
  * of two, as the OCP microscaling formats do: for a block x, e is the smallest exponent with
  * max |x| <= M 2^e (M = 448 for e4m3, 127 for int8), kept to -110 .. 118; a code is x 2^-e rounded
  * to its type (ties to even, magnitudes above M to M) and stands for code * 2^e; the scale byte is
- * e + 127.  A block with an infinity or NaN is NaN altogether: scale byte 255.  Every value that a
- * cache can hold is exactly a bf16: reads give it as it is, and attention over such a cache gives
- * what it gives over a bf16 cache of the same values, bit for bit.  Scale bytes other than 17 .. 245
- * and 255 are not allowed in a cache written elsewhere.
+ * e + 127.  A block with an infinity or NaN is NaN altogether: scale byte 255, and codes 0 (int8) or
+ * 0x7f (e4m3).  Every value that a cache can hold is exactly a bf16: reads give it as it is, and
+ * attention over such a cache is attention over a bf16 cache of the same values (up to the order of
+ * sums).  Other scale bytes than 17 .. 245 and such blocks are not allowed in a cache written
+ * elsewhere; each pool of scales has to be readable to the end of its last word of 4 bytes.
  * ------------------------------------------------------------------------------ */
 #define RF_CACHE_BF16 0
 #define RF_CACHE_FP8 1

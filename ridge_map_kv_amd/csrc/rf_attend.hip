@@ -26,8 +26,12 @@ __device__ inline void scan_prefix(const AttendArgs& a, int g, int part) {
 // over 65,536 rows, 8 key heads: 64 us by four waves a row, 72 by one; one key head 26 and 40.
 // Eight workgroups fit a compute unit (with more registers for the scan: five, 12.6 instead of 9.4
 // us for the trees above).
+// Sequences of more than 128 parts in the mean (of codes, whose workgroups of four key heads make four times as many, or
+// of prefixes): sixteen waves a row.  One fp8 sequence of 65,536 rows, 8 key heads, 512 parts: 48.5 us by
+// four, 42.7 by sixteen.
+constexpr int kManyWaves = 16;
 template <int HD, int kPer, bool kShared>
-__global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kPer > kWaves ? 64 * kPer : kThreads, 8) void join_kernel(AttendArgs a) {
   constexpr int kE = HD / 16;
   __shared__ float sh_o[kPer][HD + 1];
   const int rows = a.q.max_q * a.group;
@@ -40,7 +44,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
     const int i = blockIdx.x - own_scans;
     if ((int)blockIdx.x < scans) return scan_prefix(a, i / a.sh.scan_parts, i % a.sh.scan_parts);
   }
-  const int64_t id = (int64_t)(blockIdx.x - scans) * (kWaves / kPer) + wave / kPer;
+  const int64_t id = kPer > kWaves ? (int64_t)blockIdx.x - scans : (int64_t)(blockIdx.x - scans) * (kWaves / kPer) + wave / kPer;
   const int sh = (int)(id / rows), m = (int)(id % rows);
   if (sh >= a.b.batch * a.b.n_kv) return;
   const int kh = sh % a.b.n_kv, seq = sh / a.b.n_kv;
@@ -54,8 +58,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
     own = (self.grains + each - 1) / each;
     before = lane < seq ? (mine.grains + each - 1) / each : 0;
     for (int b = 64 + lane; b < seq; b += 64) before += (look_up(a, b).grains + each - 1) / each;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+    before = wave_sum(before);
   }
   const int64_t at = ((int64_t)before * a.b.n_kv + kh) * rows + m, step = (int64_t)a.b.n_kv * rows;
   int64_t more_at = 0, more_step = 0;
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
   if constexpr (kPer > 1) {                         // one row to a workgroup: all its waves are here
-    static_assert(kPer == kWaves, "a row is one workgroup's");
+    static_assert(kPer >= kWaves, "a row is one workgroup's");
     if (a.out && g == 0) {
 #pragma unroll
       for (int e = 0; e < kE; ++e) sh_o[wave][c * kE + e] = o[e];
@@ -154,19 +157,26 @@ __global__ __launch_bounds__(kThreads, 8) void join_kernel(AttendArgs a) {
 // How a call is laid out.
 struct AttendPlan {
   int rows;                     // query rows of a workgroup
+  int heads;                    // key heads of a workgroup
   int mblocks, group, parts, goal, least;
   size_t ml, o, total;
 };
+// Key heads of a workgroup: of codes up to four (where they share lines of scales), each for its own waves.
+int heads_together(const Batch& b, int rows, bool codes) {
+  return !codes || rows != 16 ? 1 : b.n_kv % 4 == 0 ? 4 : b.n_kv % 2 == 0 ? 2 : 1;
+}
 // `joined`: all parts are joined, also those of sequences that have one.
-AttendPlan attend_plan(const Batch& b, int n_heads, int max_q, bool joined = false) {
+// `codes`: a cache of 8 bits.
+AttendPlan attend_plan(const Batch& b, int n_heads, int max_q, bool joined = false, bool codes = false) {
   AttendPlan p;
   p.group = n_heads / b.n_kv;
   const int rows = max_q * p.group;
   p.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.mblocks = (rows + p.rows - 1) / p.rows;
   // enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS
-  const int per_part = b.n_kv * p.mblocks, want = p.rows == 16 ? 1024 : 256;
-  p.least = p.rows == 16 ? 256 : 128;
+  p.heads = heads_together(b, p.rows, codes);
+  const int per_part = b.n_kv / p.heads * p.mblocks, want = p.rows == 16 ? 1024 : 256;
+  p.least = p.rows == 16 ? 256 / p.heads : 128;
   p.goal = parts_goal(want, per_part);
   if (p.goal <= b.batch || b.max_len <= p.least) p.goal = 0;
   const int64_t most = (int64_t)b.batch * ((b.max_len + p.least - 1) / p.least);
@@ -180,9 +190,9 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q, bool joined = fal
 
 // The prefixes of a call: their form, and the pairs of a part and a block of query rows.
 struct PrefixPlan {
-  int rows, goal, least, pairs;
+  int rows, heads, goal, least, parts, pairs;
 };
-PrefixPlan prefix_plan(const Batch& b, const PrefixCall& pre, int n_heads, int max_q, int64_t n_q) {
+PrefixPlan prefix_plan(const Batch& b, const PrefixCall& pre, int n_heads, int max_q, int64_t n_q, bool codes) {
   PrefixPlan p;
   const int group = n_heads / b.n_kv;
   const int64_t most = (int64_t)b.batch * max_q, n = n_q < most ? n_q : most;      // queries that can have sequences
@@ -190,10 +200,13 @@ PrefixPlan prefix_plan(const Batch& b, const PrefixCall& pre, int n_heads, int m
   // Few query rows to a prefix: in registers, unless one prefix could have many of them, since each
   // block of 16 reads its rows again.
   p.rows = mean <= 16 && all <= 64 ? 16 : mean <= 128 ? 128 : 256;
-  p.least = p.rows == 16 ? 256 : 128;
-  p.goal = parts_goal(p.rows == 16 ? 1024 : 256, b.n_kv);
+  p.heads = heads_together(b, p.rows, codes);
+  p.least = p.rows == 16 ? 256 / p.heads : 128;
+  p.goal = parts_goal(p.rows == 16 ? 1024 : 256, b.n_kv / p.heads);
   const int64_t blocks = all / p.rows + groups;         // at most: each group's last block may not be full
-  p.pairs = (int)(blocks > p.goal ? blocks : p.goal);
+  p.parts = (pre.max_len + p.least - 1) / p.least;      // of one block, at most
+  const int64_t pairs = blocks > p.goal ? blocks : p.goal;
+  p.pairs = blocks == 0 ? 1 : (int)(blocks * p.parts < pairs ? blocks * p.parts : pairs);
   return p;
 }
 
@@ -212,12 +225,16 @@ CacheLayout cache_layout(const Batch& b, const PrefixCall& pre, const AttendPlan
   return l;
 }
 
+// `parts`: what sequences have in the mean; `many`: sixteen waves a row where they pay (not for plain bf16
+// caches: their sums keep their order).
 template <int HD, bool kShared>
-void launch_join(const AttendArgs& a, int most_parts, hipStream_t stream) {
+void launch_join(const AttendArgs& a, int most_parts, int parts, bool many, hipStream_t stream) {
   const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
   const int64_t scans = (int64_t)a.b.batch * a.scan_parts + (kShared ? (int64_t)a.sh.groups * a.sh.scan_parts : 0);
   // a sequence can have more parts than a wave has under way; not where there are rows for all waves
-  if (most_parts > 32 && (!kShared || rows <= 65536))
+  if (many && parts > 128 && rows <= 65536)
+    hipLaunchKernelGGL((join_kernel<HD, kManyWaves, kShared>), dim3((unsigned)(rows + scans)), dim3(64 * kManyWaves), 0, stream, a);
+  else if (most_parts > 32 && (!kShared || rows <= 65536))
     hipLaunchKernelGGL((join_kernel<HD, kWaves, kShared>), dim3((unsigned)(rows + scans)), dim3(kThreads), 0, stream, a);
   else
     hipLaunchKernelGGL((join_kernel<HD, 1, kShared>), dim3((unsigned)((rows + kWaves - 1) / kWaves + scans)),
@@ -241,6 +258,7 @@ AttendArgs attend_args(const Batch& b, const Queries& q, const AttendPlan& p, ui
   a.parts = p.parts;
   a.goal = p.goal;
   a.least = p.least;
+  a.heads = p.heads;
   a.mblocks = p.mblocks;
   a.group = p.group;
   a.scan_parts = scan_parts(b);
@@ -248,7 +266,7 @@ AttendArgs attend_args(const Batch& b, const Queries& q, const AttendPlan& p, ui
 }
 
 // A call without prefixes: one launch, and the join where sequences are split.
-hipError_t launch_plain(AttendArgs& a, const AttendPlan& p, void (*rows)(const AttendArgs&, int, unsigned, hipStream_t),
+hipError_t launch_plain(AttendArgs& a, const AttendPlan& p, bool codes, void (*rows)(const AttendArgs&, int, unsigned, hipStream_t),
                         hipStream_t stream) {
   a.scan = !p.goal && scans(a.b) ? 1 : 0;
   a.report = !p.goal && !a.scan ? 1 : 0;
@@ -256,9 +274,10 @@ hipError_t launch_plain(AttendArgs& a, const AttendPlan& p, void (*rows)(const A
     const hipError_t e = launch_clear_status(a.status, stream);
     if (e != hipSuccess) return e;
   }
-  a.own = (int)((int64_t)p.parts * a.b.n_kv * p.mblocks);
+  a.own = (int)((int64_t)p.parts * (a.b.n_kv / p.heads) * p.mblocks);
   rows(a, p.rows, (unsigned)a.own + a.scan, stream);
-  if (p.goal) a.b.hd == 128 ? launch_join<128, false>(a, p.goal, stream) : launch_join<64, false>(a, p.goal, stream);
+  const auto join = a.b.hd == 128 ? launch_join<128, false> : launch_join<64, false>;
+  if (p.goal) join(a, p.goal, p.parts / a.b.batch, codes, stream);
   return hipGetLastError();
 }
 
@@ -275,13 +294,19 @@ hipError_t launch_attend(const Batch& b, const uint16_t* kp, const uint16_t* vp,
   AttendArgs a = attend_args(b, q, p, out, out_stride, lse, static_cast<unsigned char*>(ws));
   a.kp = kp;
   a.vp = vp;
-  return launch_plain(a, p, launch_rows<RF_CACHE_BF16, false>, stream);
+  return launch_plain(a, p, false, launch_rows<RF_CACHE_BF16, false>, stream);
 }
 
+// What caches of either kind need.
 size_t cache_attend_workspace(const Batch& b, const PrefixCall* prefix, int n_heads, int max_q, int64_t n_q) {
-  if (!prefix) return attend_workspace(b, n_heads, max_q);
-  const AttendPlan p = attend_plan(b, n_heads, max_q, true);
-  return cache_layout(b, *prefix, p, prefix_plan(b, *prefix, n_heads, max_q, n_q), max_q * p.group).total;
+  size_t most = 0;
+  for (const bool codes : {false, true}) {
+    const AttendPlan p = attend_plan(b, n_heads, max_q, prefix != nullptr, codes);
+    const size_t need = prefix ? cache_layout(b, *prefix, p, prefix_plan(b, *prefix, n_heads, max_q, n_q, codes), max_q * p.group).total
+                               : p.total;
+    most = most < need ? need : most;
+  }
+  return most;
 }
 
 hipError_t launch_cache_attend(const Batch& b, const PrefixCall* prefix, const Pools& pools, const Queries& q,
@@ -292,15 +317,16 @@ hipError_t launch_cache_attend(const Batch& b, const PrefixCall* prefix, const P
   const auto rows = pools.type == RF_CACHE_BF16  ? launch_rows<RF_CACHE_BF16, true>
                     : pools.type == RF_CACHE_FP8 ? launch_rows<RF_CACHE_FP8, true>
                                                  : launch_rows<RF_CACHE_INT8, true>;
-  const AttendPlan p = attend_plan(b, q.n_heads, q.max_q, prefix != nullptr);
+  const bool codes = pools.type != RF_CACHE_BF16;
+  const AttendPlan p = attend_plan(b, q.n_heads, q.max_q, prefix != nullptr, codes);
   unsigned char* w = static_cast<unsigned char*>(ws);
   AttendArgs a = attend_args(b, q, p, out, out_stride, lse, w);
   a.kp = kp;
   a.vp = vp;
   a.ks = pools.ks;
   a.vs = pools.vs;
-  if (!prefix) return launch_plain(a, p, rows, stream);
-  const PrefixPlan pp = prefix_plan(b, *prefix, q.n_heads, q.max_q, q.n_q);
+  if (!prefix) return launch_plain(a, p, codes, rows, stream);
+  const PrefixPlan pp = prefix_plan(b, *prefix, q.n_heads, q.max_q, q.n_q, codes);
   const CacheLayout l = cache_layout(b, *prefix, p, pp, q.max_q * p.group);
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_o = reinterpret_cast<float*>(w + l.o);
@@ -309,15 +335,19 @@ hipError_t launch_cache_attend(const Batch& b, const PrefixCall* prefix, const P
   a.sh = {prefix->tables, prefix->lengths, prefix->starts, prefix->table_stride, prefix->groups, prefix->max_len,
           pp.goal, pp.least, pp.rows, l.own_rows, scan_parts(as), reinterpret_cast<unsigned*>(w + l.plan)};
   // The sequences' own rows and the prefixes, in one launch where both take the same kernel.
-  const int own = (int)((int64_t)p.parts * b.n_kv * p.mblocks), more = pp.pairs * b.n_kv;
+  const int own = (int)((int64_t)p.parts * (b.n_kv / p.heads) * p.mblocks), more = pp.pairs * (b.n_kv / pp.heads);
   a.own = own;
   rows(a, p.rows, (unsigned)(p.rows == pp.rows ? own + more : own), stream);
   if (p.rows != pp.rows) {
     a.own = 0;
+    a.heads = pp.heads;
     rows(a, pp.rows, (unsigned)more, stream);
   }
-  const int most_parts = p.goal > pp.goal ? p.goal : pp.goal;
-  b.hd == 128 ? launch_join<128, true>(a, most_parts, stream) : launch_join<64, true>(a, most_parts, stream);
+  const int most_parts = p.parts > pp.pairs ? p.parts : pp.pairs;
+  // its own parts, and those of a prefix
+  const int groups = prefix->groups < b.batch ? prefix->groups : b.batch, shared = pp.goal / groups;
+  const int mean = p.parts / b.batch + (shared < pp.parts ? shared : pp.parts);
+  (b.hd == 128 ? launch_join<128, true> : launch_join<64, true>)(a, most_parts, mean, true, stream);
   return hipGetLastError();
 }
 

@@ -70,6 +70,7 @@ struct AttendArgs {
   Divide page;
   int parts, goal, least;       // parts of the grid; wanted of all sequences (0: one each), rows of one
   int own;                      // workgroups before those of the prefixes
+  int heads;                    // key heads of a workgroup of the kernel over codes: 1, 2 or 4
   int mblocks;                  // blocks of query rows
   int group;                    // query heads of a key head
   int scan;                     // 1: the first workgroup looks all pages over for the status
@@ -134,17 +135,12 @@ __device__ __forceinline__ Seq look_up(const AttendArgs& a, int b) {
 // Grains of one part; `mine`: sequence lane.
 inline __device__ int grains_of_part(const AttendArgs& a, const Seq& mine) {
   const int lane = threadIdx.x & 63;
-  const auto sum = [](auto v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-  };
-  long long total = mine.grains;
+  int total = mine.grains;                  // batch * max_len <= 2^36: below 2^31
   for (int b = 64 + lane; b < a.b.batch; b += 64) total += look_up(a, b).grains;
-  return part_grains(sum(total), a.b.batch, a.goal, a.least / kGrain, [&](int each) {
+  return part_grains(wave_sum(total), a.b.batch, a.goal, a.least / kGrain, [&](int each) {
     int parts = (mine.grains + each - 1) / each;
     for (int b = 64 + lane; b < a.b.batch; b += 64) parts += (look_up(a, b).grains + each - 1) / each;
-    return sum(parts);
+    return wave_sum(parts);
   });
 }
 
@@ -160,11 +156,12 @@ __device__ __forceinline__ void place_part(const AttendArgs& a, int seq, int id,
   p->table = a.b.tables + (int64_t)seq * a.b.table_stride;
   p->at = whole ? -1 : ((int64_t)id * a.b.n_kv + p->kh) * (a.q.max_q * a.group);
 }
+// `heads`: key heads of a workgroup, of which this wave takes number `head`.
 template <bool kShared>
-__device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
+__device__ bool find_part(const AttendArgs& a, int unit, Part* p, int heads = 1, int head = 0) {
   const int lane = threadIdx.x & 63;
-  p->kh = unit % a.b.n_kv;
-  const int id = unit / a.b.n_kv;
+  const int groups = a.b.n_kv / heads, id = unit / groups;
+  p->kh = unit % groups * heads + head;
   if (!a.goal) {
     const bool shared = kShared && a.sh.groups;
     if (shared && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;    // the join adds what is wrong
@@ -186,12 +183,7 @@ __device__ bool find_part(const AttendArgs& a, int unit, Part* p) {
   for (int b0 = 0; b0 < a.b.batch; b0 += 64) {
     if (b0) s = look_up(a, b0 + lane);
     const int mine = (s.grains + each - 1) / each;
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(upto, d);
-      if (lane >= d) upto += o;
-    }
+    const int upto = wave_scan(mine);
     const uint64_t past = __ballot(before + upto > id);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
@@ -236,14 +228,9 @@ __device__ __forceinline__ Group look_up_group(const AttendArgs& a, int g) {
 // The same for the prefixes: each group's rows are cut into parts, and its query rows into blocks; the
 // pairs of a part and a block take turns with the key heads, blocks first, so that the workgroups
 // that read the same rows run side by side.  *mb: the block.
-inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* mb) {
-  const int lane = threadIdx.x & 63, id = unit / a.b.n_kv;
-  p->kh = unit % a.b.n_kv;
-  const auto sum = [](auto v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-  };
+inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* mb, int heads = 1, int head = 0) {
+  const int lane = threadIdx.x & 63, groups = a.b.n_kv / heads, id = unit / groups;
+  p->kh = unit % groups * heads + head;
   Group r = look_up_group(a, lane);
   long long total = (long long)r.blocks * r.grains;
   int blocks = r.blocks;
@@ -252,26 +239,21 @@ inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* 
     total += (long long)o.blocks * o.grains;
     blocks += o.blocks;
   }
-  total = sum(total);
-  blocks = sum(blocks);
+  total = wave_sum(total);
+  blocks = wave_sum(blocks);
   const auto parts_of = [](const Group& x, int each) { return x.blocks * ((x.grains + each - 1) / each); };
   int each = kMostGrains;
   if (blocks < a.sh.goal)
     each = part_grains(total, blocks, a.sh.goal, a.sh.least / kGrain, [&](int e) {
       int parts = parts_of(r, e);
       for (int g = 64 + lane; g < a.sh.groups; g += 64) parts += parts_of(look_up_group(a, g), e);
-      return sum(parts);
+      return wave_sum(parts);
     });
   int before = 0;
   for (int g0 = 0; g0 < a.sh.groups; g0 += 64) {
     if (g0) r = look_up_group(a, g0 + lane);
     const int mine = parts_of(r, each);
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(upto, d);
-      if (lane >= d) upto += o;
-    }
+    const int upto = wave_scan(mine);
     const uint64_t past = __ballot(before + upto > id);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
@@ -315,118 +297,106 @@ __device__ __forceinline__ void place_block(const AttendArgs& a, int* unit, int*
 }
 
 template <int HD>
-struct CodeTile;
-template <int HD, int kType>
-__device__ __forceinline__ u32x4 code_key(const CodeTile<HD>& t, int h, int s);
-template <int HD, int kType>
-__device__ __forceinline__ void code_row(const CodeTile<HD>& t, int j, uint32_t (&w)[HD / 32]);
-
-// Scale bytes of a row's blocks: 4 (hd 128) or 2.
-template <int HD>
-__device__ __forceinline__ unsigned row_scales(const uint8_t* scales, int64_t at) {
-  if constexpr (HD == 128) return *reinterpret_cast<const unsigned*>(scales + 4 * at);
-  return *reinterpret_cast<const uint16_t*>(scales + 2 * at);
-}
-
-template <int HD, int kType>
 struct Tile {                   // 32 cache rows of one head, as a wave holds them
   static constexpr int kSteps = HD / 32;
   u32x4 k[2][kSteps];           // rows 16 t + c, features 32 s + 8 g ..
   uint32_t v[8][HD / 32];       // rows 16 (j/4) + 4 g + j % 4, features (HD/16) c ..
-  __device__ u32x4 key(int h, int s) const { return k[h][s]; }
-  __device__ void row(int j, uint32_t (&w)[HD / 32]) const {
-#pragma unroll
-    for (int i = 0; i < HD / 32; ++i) w[i] = v[j][i];
-  }
-};
-// Of 8 bits: codes and scales, in the same places; they become values where they are used.
-template <int HD>
-struct CodeTile {
-  u32x2 k[2][HD / 32];
-  unsigned ks[2], vs[8];
-  unsigned v[8][HD / 64];
-};
-template <int HD>
-struct Tile<HD, RF_CACHE_FP8> : CodeTile<HD> {
-  static constexpr int kType = RF_CACHE_FP8;
-  __device__ u32x4 key(int h, int s) const { return code_key<HD, kType>(*this, h, s); }
-  __device__ void row(int j, uint32_t (&w)[HD / 32]) const { code_row<HD, kType>(*this, j, w); }
-};
-template <int HD>
-struct Tile<HD, RF_CACHE_INT8> : CodeTile<HD> {
-  static constexpr int kType = RF_CACHE_INT8;
-  __device__ u32x4 key(int h, int s) const { return code_key<HD, kType>(*this, h, s); }
-  __device__ void row(int j, uint32_t (&w)[HD / 32]) const { code_row<HD, kType>(*this, j, w); }
 };
 
-template <int HD, int kType>
-__device__ __forceinline__ u32x4 code_key(const CodeTile<HD>& t, int h, int s) {
-  const float f = scale_of(t.ks[h] >> (8 * s) & 255u);
-  const u32x2 x = values_of<kType>(t.k[h][s][0], f), y = values_of<kType>(t.k[h][s][1], f);
-  return {x[0], x[1], y[0], y[1]};
-}
-template <int HD, int kType>
-__device__ __forceinline__ void code_row(const CodeTile<HD>& t, int j, uint32_t (&w)[HD / 32]) {
-  const float f = scale_of(t.vs[j]);
+template <int HD, bool kV>
+__device__ __forceinline__ void load_tile(Tile<HD>& t, const AttendArgs& a, const uint16_t* kh,
+                                          const uint16_t* vh, int slot, int c, int g) {
+  const int64_t row = (int64_t)a.b.n_kv * HD;
 #pragma unroll
-  for (int i = 0; i < HD / 64; ++i) {
-    const u32x2 x = values_of<kType>(t.v[j][i], f);
-    w[2 * i] = x[0];
-    w[2 * i + 1] = x[1];
+  for (int h = 0; h < 2; ++h) {
+    const uint16_t* p = kh + (int64_t)__shfl(slot, 16 * h + c) * row + 8 * g;
+#pragma unroll
+    for (int s = 0; s < HD / 32; ++s) t.k[h][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
   }
-}
-
-template <int HD, bool kV, int kType>
-__device__ __forceinline__ void load_tile(Tile<HD, kType>& t, const AttendArgs& a, int kh, int slot, int c, int g) {
-  if constexpr (kType == RF_CACHE_BF16) {
-    const int64_t row = (int64_t)a.b.n_kv * HD;
-    const uint16_t* kb = a.kp + kh * HD;
-    const uint16_t* vb = a.vp + kh * HD;
+  if constexpr (kV) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint16_t* p = kb + (int64_t)__shfl(slot, 16 * h + c) * row + 8 * g;
+    for (int j = 0; j < 8; ++j) {
+      const uint16_t* p = vh + (int64_t)__shfl(slot, 16 * (j / 4) + 4 * g + j % 4) * row + (HD / 16) * c;
+      if constexpr (HD == 128) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
-      for (int s = 0; s < HD / 32; ++s) t.k[h][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
-    }
-    if constexpr (kV) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint16_t* p = vb + (int64_t)__shfl(slot, 16 * (j / 4) + 4 * g + j % 4) * row + (HD / 16) * c;
-        if constexpr (HD == 128) {
-          const u32x4 w = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t.v[j][i] = w[i];
-        } else {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-          t.v[j][0] = w[0];
-          t.v[j][1] = w[1];
-        }
+        for (int i = 0; i < 4; ++i) t.v[j][i] = w[i];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+        t.v[j][0] = w[0];
+        t.v[j][1] = w[1];
       }
     }
-  } else {
-    const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kp);
-    const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vp);
+  }
+}
+
+// The end of the kernels of up to 16 query rows: the workgroup's waves' results joined and written, those of
+// waves w and w + heads where the workgroup has several key heads.
+template <int HD, bool kOut>
+__device__ __forceinline__ void join_waves(const AttendArgs& a, const Part& pt, int heads, int m, bool in, int64_t row, int head, float m_run,
+                                           float l_run, f32x4 (&o)[kOut ? HD / 16 : 1], float (*sh_o)[16][HD + 4],
+                                           float2 (*sh_ml)[16]) {
+  constexpr int kFeat = HD / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  // sums over g, then the waves: 2 and 3 into 0 and 1, then 1 into 0
+  l_run += __shfl_xor(l_run, 16);
+  l_run += __shfl_xor(l_run, 32);
+  for (int half = kWaves / 2; half >= heads; half /= 2) {
+    if (wave >= half && wave < 2 * half) {
+      const int w = wave - half;
+      if (g == 0) sh_ml[w][c] = make_float2(m_run, l_run);
+      if constexpr (kOut) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t at = (int64_t)__shfl(slot, 16 * h + c) * a.b.n_kv + kh;
-      const uint8_t* p = kb + at * HD + 8 * g;
+        for (int f = 0; f < kFeat; ++f)
 #pragma unroll
-      for (int s = 0; s < HD / 32; ++s) t.k[h][s] = *reinterpret_cast<const u32x2*>(p + 32 * s);
-      t.ks[h] = row_scales<HD>(a.ks, at);
+          for (int r = 0; r < 4; ++r) sh_o[w][c][kFeat * (4 * g + r) + f] = o[f][r];
+      }
     }
-    if constexpr (kV) {
+    __syncthreads();
+    if (wave < half) {
+      const float2 ml = sh_ml[wave][c];
+      const float m_new = fmaxf(m_run, ml.x), zero = m_new == -INFINITY ? 0.f : m_new;
+      const float mine = __builtin_amdgcn_exp2f(m_run - zero), theirs = __builtin_amdgcn_exp2f(ml.x - zero);
+      m_run = m_new;
+      l_run = l_run * mine + ml.y * theirs;
+      if constexpr (kOut) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t at = (int64_t)__shfl(slot, 16 * (j / 4) + 4 * g + j % 4) * a.b.n_kv + kh;
-        const uint8_t* p = vb + at * HD + (HD / 16) * c;
-        if constexpr (HD == 128) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-          t.v[j][0] = w[0];
-          t.v[j][1] = w[1];
-        } else {
-          t.v[j][0] = *reinterpret_cast<const unsigned*>(p);
-        }
-        t.vs[j] = a.vs[at * (HD / kBlock) + c * (HD / 16) / kBlock];
+        for (int f = 0; f < kFeat; ++f)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[f][r] = o[f][r] * mine + sh_o[wave][c][kFeat * (4 * g + r) + f] * theirs;
+      }
+    }
+    __syncthreads();
+  }
+  if (wave >= heads || !in) return;
+  if (pt.at >= 0) {
+    const int64_t part = pt.at + m;
+    if (g == 0) a.part_ml[part] = make_float2(m_run, l_run);
+    if constexpr (kOut) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float* p = a.part_o + part * HD + kFeat * (4 * g + r);
+#pragma unroll
+        for (int f = 0; f < kFeat; f += 4)
+          *reinterpret_cast<f32x4*>(p + f) = f32x4{o[f][r], o[f + 1][r], o[f + 2][r], o[f + 3][r]};
+      }
+    }
+    return;
+  }
+  const bool none = l_run == 0.f;
+  if (a.lse && g == 0) a.lse[row * a.q.n_heads + head] = none ? -INFINITY : m_run * kLn2 + __logf(l_run);
+  if constexpr (kOut) {
+    const float inv = none ? 0.f : 1.f / l_run;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint16_t* p = a.out + row * a.out_stride + head * HD + kFeat * (4 * g + r);
+#pragma unroll
+      for (int f = 0; f < kFeat; f += 4) {
+        u32x2 w;
+        w[0] = pack_bf16x2(o[f][r] * inv, o[f + 1][r] * inv);
+        w[1] = pack_bf16x2(o[f + 2][r] * inv, o[f + 3][r] * inv);
+        *reinterpret_cast<u32x2*>(p + f) = none ? u32x2{0u, 0u} : w;
       }
     }
   }
@@ -437,7 +407,7 @@ __device__ __forceinline__ void load_tile(Tile<HD, kType>& t, const AttendArgs& 
 // 8 key heads of 128 (760 MB): 148 us of the call's 153, 5.1 TB/s, as a large copy.  (The tile kernel
 // below took 187 us there; this one, with four tiles of 16 queries, 120 us for 64 query rows over 65,536
 // where that took 70; both with one operand a weight.)
-template <int HD, bool kOut, int kType, bool kShared>
+template <int HD, bool kOut, bool kShared>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   constexpr int kSteps = HD / 32, kFeat = HD / 16;
   __shared__ float sh_o[kWaves / 2][16][HD + 4];
@@ -451,7 +421,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   const int unit = blockIdx.x - a.scan;
   if constexpr (kShared) prefix = unit >= a.own;
   if (prefix ? !find_prefix(a, unit - a.own, &pt, &mb) : !find_part<kShared>(a, unit, &pt)) return;
-  const int kh = pt.kh, len = pt.len, first = pt.first, begin = pt.begin, end = pt.end;
+  // the end as a value of each lane: counted in scalars the loop spills (and lost 5 us of 200 before)
+  const int kh = pt.kh, len = pt.len, first = pt.first, begin = pt.begin, end = fresh(pt.end);
   const int m_rows = pt.n * a.group, ctx = pt.ctx, m = 16 * mb + c;
 
   // Q^T fragments: query row m, zero past the last
@@ -475,6 +446,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   for (int f = 0; f < (kOut ? kFeat : 1); ++f) o[f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int32_t* table = pt.table;
+  const uint16_t* kbase = a.kp + kh * HD;
+  const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
   const float scale2 = a.q.scale * kLog2e;
   int page_err = 0;
   // page of row r (the last row for rows past it), then the pool slot: -1 on a bad page
@@ -490,18 +463,18 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 
   int base = begin + wave * kRows;
   constexpr int kStride = kWaves * kRows;
-  Tile<HD, kType> cur;
+  Tile<HD> cur;
   int page_next = 0, slot = -1;
   if (base < end) {
     slot = slot_of(base, page_of(base));
-    load_tile<HD, kOut>(cur, a, kh, slot < 0 ? 0 : slot, c, g);
+    load_tile<HD, kOut>(cur, a, kbase, vbase, slot < 0 ? 0 : slot, c, g);
     page_next = page_of(base + kStride);
   }
   for (; base < end; base += kStride) {
     // the next rows on their way (rows past the end repeat the last one, and are not used)
     const int slot_next = slot_of(base + kStride, page_next);
-    Tile<HD, kType> next;
-    if (base + kStride < end) load_tile<HD, kOut>(next, a, kh, slot_next < 0 ? 0 : slot_next, c, g);
+    Tile<HD> next;
+    if (base + kStride < end) load_tile<HD, kOut>(next, a, kbase, vbase, slot_next < 0 ? 0 : slot_next, c, g);
     page_next = page_of(base + 2 * kStride);
 
     const uint64_t good64 = __ballot(slot >= 0);
@@ -515,9 +488,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     bf16x8 vf[kOut ? kFeat : 1];
     bool wild = false;                                // a value that is not finite
     if constexpr (kOut) {
-      uint32_t rows[8][HD / 32];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) cur.row(j, rows[j]);
       if (masked) {
         bool w = false;
 #pragma unroll
@@ -525,8 +495,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
           const bool in = there >> (16 * (j / 4) + 4 * g + j % 4) & 1;
 #pragma unroll
           for (int i = 0; i < HD / 32; ++i) {
-            if (!in) rows[j][i] = 0u;
-            w |= (rows[j][i] & 0x7f80u) == 0x7f80u || (rows[j][i] & 0x7f800000u) == 0x7f800000u;
+            if (!in) cur.v[j][i] = 0u;
+            w |= (cur.v[j][i] & 0x7f80u) == 0x7f80u || (cur.v[j][i] & 0x7f800000u) == 0x7f800000u;
           }
         }
         wild = __any(w);
@@ -535,7 +505,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       for (int f = 0; f < kFeat; ++f) {
         u32x4 w;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) w[p] = half_pair(rows[2 * p][f / 2], rows[2 * p + 1][f / 2], f & 1);
+        for (int p = 0; p < 4; ++p) w[p] = half_pair(cur.v[2 * p][f / 2], cur.v[2 * p + 1][f / 2], f & 1);
         vf[f] = __builtin_bit_cast(bf16x8, w);
       }
     }
@@ -544,7 +514,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, cur.key(h, st)), qf[st], s[h]);
+      for (int h = 0; h < 2; ++h) s[h] = mfma16(__builtin_bit_cast(bf16x8, cur.k[h][st]), qf[st], s[h]);
     uint32_t seen = 0xffffffffu;                    // rows that this lane's query sees
     if (masked) {
       seen = there;
@@ -620,69 +590,393 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     slot = slot_next;
   }
   if (page_err && a.report && lane == 0) atomicOr(a.status, kStatusRowsBit);
+  join_waves<HD, kOut>(a, pt, 1, m, in, first + qi, head, m_run, l_run, o, sh_o, sh_ml);
+}
 
-  // sums over g, then the waves: 2 and 3 into 0 and 1, then 1 into 0
-  l_run += __shfl_xor(l_run, 16);
-  l_run += __shfl_xor(l_run, 32);
-  for (int half = kWaves / 2; half; half /= 2) {
-    if (wave >= half && wave < 2 * half) {
-      const int w = wave - half;
-      if (g == 0) sh_ml[w][c] = make_float2(m_run, l_run);
+// 16 bytes per lane from base + off (bytes) to the LDS address lds + 16 lane (lds: the same in the wave).  The
+// compiler does not see the load: dma_wait before the barrier that hands the data on.
+__device__ __forceinline__ void dma_row(const uint16_t* base, uint64_t off, uint32_t lds) {
+  const unsigned char* p = reinterpret_cast<const unsigned char*>(base) + off;
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory", "m0");
+}
+template <int kLeft>                  // until at most kLeft loads are under way
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+template <int kBytes>                 // 4 or 16 of each lane
+__device__ __forceinline__ void dma_to(const uint8_t* p, uint32_t lds) {
+  if constexpr (kBytes == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                 :
+                 : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory", "m0");
+}
+// The value of lane ^ 32.
+__device__ __forceinline__ float other_half(float v) {
+  const int x = __builtin_bit_cast(int, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// The value of lane ^ 16.
+__device__ __forceinline__ float other_sixteen(float v) {
+  const int x = __builtin_bit_cast(int, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  return __builtin_bit_cast(float, (threadIdx.x & 16) ? r[0] : r[1]);
+}
+
+// What was read of LDS has arrived: it may be overwritten.
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+// The same over codes.  A step's bytes are half as many, so twice as many waves have to be under way:
+// each has its 32 rows in LDS of its own, where direct loads put them without holding registers, and
+// sends for the next rows' keys as soon as the scores are formed, for their values as soon as the
+// product is.  No wave waits for another.  Values exist two features at a time.
+// A head's scales are 4 bytes of each line of 128, and what a compute unit can have under way is counted in
+// lines (its first cache holds 256): four waves that take different rows of one head have 80 lines of a
+// step where 64 hold its codes.  So they take the same rows of four heads, whose scales share the lines.
+// Row r lies at place r ^ (r / 4 & kSwap), its pieces of 16 bytes turned by the place: neither the keys'
+// reads (16 rows at a time) nor the values' (rows 4 apart) meet in a bank.
+constexpr int kCodeTiles = 8;         // steps of a wave whose slots are looked up at a time
+template <int HD>
+struct WaveRows {                     // a wave's rows in LDS
+  static constexpr int kSwap = HD == 128 ? 1 : 3, kPieces = HD / 16;
+  unsigned char k[kRows * HD], v[kRows * HD];
+  unsigned scales[2][64];             // k's, then v's, by turns
+  int slot[kCodeTiles * kRows];
+  static constexpr unsigned turn_shift = HD == 128 ? 1 : 2;
+  __host__ __device__ static constexpr unsigned place(unsigned row) { return row ^ (row >> 2 & kSwap); }
+  __host__ __device__ static constexpr unsigned turn(unsigned place) { return place >> turn_shift & (kPieces - 1); }
+  // Byte offsets in k or v; the parts that the lane and the loop's index give differ in their bits, so that
+  // one kept address and a constant make each.
+  // Features 32 s + 8 g .. of row c (and of 16 + c, 16 HD further).
+  __device__ static unsigned key(unsigned c, unsigned g) { return place(c) * HD + (((g >> 1) ^ turn(place(c))) << 4) + 8 * (g & 1); }
+  static constexpr unsigned key_step(int s) { return 32u * s; }
+  // Features (HD/16) c .. of row 4 g + j, j < 4 (and of 16 + 4 g + j).
+  __device__ static unsigned value(unsigned c, unsigned g) {
+    return place(4 * g) * HD + (((c * (HD / 16) >> 4) ^ turn(place(4 * g))) << 4) + c * (HD / 16) % 16;
+  }
+  static constexpr unsigned value_step(int j) { return (unsigned)j * HD + (turn((unsigned)j) << 4); }
+};
+// Rows 4 g + j for j < 4 lie at place(4 g) ^ j and are turned by turn(place(4 g)) ^ turn(j); rows c and 16 + c
+// are turned alike.
+template <int HD>
+constexpr bool places_split() {
+  using R = WaveRows<HD>;
+  for (unsigned r = 0; r < 32; ++r) {
+    if (R::place(r) != (R::place(r & ~3u) ^ (r & 3))) return false;
+    if (R::turn(R::place(r)) != (R::turn(R::place(r & ~3u)) ^ R::turn(r & 3))) return false;
+    if (R::turn(R::place(r & 15)) != R::turn(R::place(r))) return false;
+    if (R::place(R::place(r)) != r) return false;
+  }
+  return true;
+}
+static_assert(places_split<128>() && places_split<64>(), "how rows lie in LDS");
+
+template <int HD, bool kOut, int kType>
+__global__ __launch_bounds__(kThreads, 4) void attend_codes_kernel(AttendArgs a) {
+  constexpr int kSteps = HD / 32, kFeat = HD / 16;
+  using Rows = WaveRows<HD>;
+  constexpr int kLoads = kRows * HD / 1024;             // direct loads of a step's keys, and values
+  struct Join {
+    float o[kWaves / 2][16][HD + 4];
+    float2 ml[kWaves / 2][16];
+  };
+  __shared__ union __attribute__((aligned(256))) {
+    Rows rows[kWaves];
+    Join join;
+  } sh;
+  if (a.scan && blockIdx.x == 0) return scan_status(a.b, a.q, a.status);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  Part pt;
+  int mb = 0;
+  const int unit = blockIdx.x - a.scan;
+  const bool prefix = unit >= a.own;
+  const int heads = a.heads, rank = wave / heads, ranks = kWaves / heads;   // which of a head's waves this is
+  if (prefix ? !find_prefix(a, unit - a.own, &pt, &mb, heads, wave % heads) : !find_part<true>(a, unit, &pt, heads, wave % heads)) return;
+  const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };   // in all lanes: scalar
+  const int kh = same(pt.kh), len = same(pt.len), first = same(pt.first), begin = same(pt.begin), end = same(pt.end);
+  const int m_rows = same(pt.n * a.group), ctx = same(pt.ctx);
+  const auto same_pointer = [&](const void* p) {
+    typedef const __attribute__((address_space(1))) uint8_t* global;
+    const uint64_t bits = reinterpret_cast<uint64_t>(p);
+    return (global)((uint64_t)(uint32_t)same((int)(bits >> 32)) << 32 | (uint32_t)same((int)bits));
+  };
+  const auto table = (const __attribute__((address_space(1))) int32_t*)same_pointer(pt.table);
+  // query row of this lane, its query and head; formed where they are used
+  struct Row {
+    int m, qi, head;
+    bool in;
+  };
+  const auto row_of_query = [&]() -> Row {
+    const int m = 16 * mb + (fresh(lane) & 15);
+    const bool in = m < m_rows;
+    return {m, in ? m / a.group : 0, kh * a.group + (in ? m % a.group : 0), in};
+  };
+  bf16x8 qf[kSteps];
+  // a load of it in the loop would be waited for with the rows under way
+  uint64_t word = 0ull;
+  {
+    const Row q = row_of_query();
+    if (!prefix) word = draft_word(a.q, first + q.qi, q.qi);
+    const uint16_t* p = a.q.q + (int64_t)(first + q.qi) * a.q.q_stride + q.head * HD + 8 * g;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (q.in) w = *reinterpret_cast<const u32x4*>(p + 32 * s);
+      qf[s] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+  f32x4 o[kOut ? kFeat : 1];
+  float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll
+  for (int f = 0; f < (kOut ? kFeat : 1); ++f) o[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float scale2 = a.q.scale * kLog2e;
+  int page_err = 0;
+  Rows& rows = sh.rows[wave];
+  constexpr int kPages = kCodeTiles * kRows / 64;
+  const int stride = ranks * kRows, base0 = begin + rank * kRows;
+  const int tiles = base0 < end ? (end - base0 + stride - 1) / stride : 0;
+  // the wave's row of one of its steps; rows past the last repeat it
+  const auto row_of = [&](int i) {
+    const int r = base0 + i / kRows * stride + i % kRows;
+    return r < len ? r : len - 1;
+  };
+  const auto look_up_pages = [&](int tile, int (&page)[kPages]) {
+    const int ln = fresh(lane);
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) page[i] = table[quotient((unsigned)row_of(tile * kRows + 64 * i + ln), a.page)];
+  };
+  const auto set_slots = [&](int tile, const int (&page)[kPages]) {
+    const int ln = fresh(lane);
+#pragma unroll
+    for (int i = 0; i < kPages; ++i) {
+      const int r = row_of(tile * kRows + 64 * i + ln);
+      rows.slot[64 * i + ln] = page[i] < 0 || page[i] >= a.b.num_pages
+                                     ? -1 : page[i] * a.b.page_size + (r - (int)quotient((unsigned)r, a.page) * a.b.page_size);
+    }
+  };
+  // Where a row lies in the pools: slot n_kv + kh, in rows of one head.  Of a direct load's 64 / kPieces rows this
+  // lane loads one piece; the rows of the next load are 64 / kPieces on in either order.
+  const unsigned row_bytes = a.b.n_kv * HD;
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(a.kp) + (int64_t)kh * HD;
+  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(a.vp) + (int64_t)kh * HD;
+  constexpr int kEach = 64 / Rows::kPieces;
+  static_assert(Rows::turn(kEach) == 0 || Rows::turn(kEach) == Rows::kPieces / 2, "every other load is turned the other way");
+  const unsigned mine = lane / Rows::kPieces, my_row = Rows::place(mine), my_piece = 16 * ((lane % Rows::kPieces) ^ Rows::turn(mine));
+  const auto slots_of = [&](int tile) { return rows.slot + tile % kCodeTiles * kRows; };
+  const auto load_rows = [&](const uint8_t* base, unsigned char* to, int tile) {
+    const unsigned row0 = fresh(my_row), piece0 = fresh(my_piece);   // what is formed from them is not kept
+    int slot[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) slot[i] = slots_of(tile)[row0 + kEach * i];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint64_t off = (uint64_t)(unsigned)(slot[i] < 0 ? 0 : slot[i]) * row_bytes;
+      dma_to<16>(base + off + (piece0 ^ Rows::turn(kEach * i) << 4), lds_address(to) + 1024 * i);
+    }
+  };
+  const auto load_keys = [&](int tile) {
+    load_rows(kbase, rows.k, tile);
+    const int ln = fresh(lane), slot = slots_of(tile)[ln & 31];
+    const int64_t at = (int64_t)(slot < 0 ? 0 : slot) * a.b.n_kv + kh;
+    const uint8_t* p = (kOut && (ln & 32) ? a.vs : a.ks) + (HD == 128 ? 4 * at : 2 * at & ~(int64_t)3);
+    dma_to<4>(p, lds_address(rows.scales[tile & 1]));
+  };
+  // the scales of a row's blocks: of hd 64 half of a word
+  const auto scales_of = [&](unsigned w, int tile, int row) -> unsigned {
+    if constexpr (HD == 128) return w;
+    const int slot = slots_of(tile)[row];
+    return ((slot < 0 ? 0 : slot) * (a.b.n_kv & 1) + kh) & 1 ? w >> 16 : w & 0xffffu;
+  };
+  const unsigned key_at = Rows::key(c, g), value_at = Rows::value(c, g);
+
+  int page[kPages];
+  if (tiles) {
+    look_up_pages(0, page);
+    set_slots(0, page);
+    load_keys(0);
+    if constexpr (kOut) load_rows(vbase, rows.v, 0);
+  }
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int base = base0 + tile * stride;
+    const uint32_t good = (uint32_t)__ballot(slots_of(tile)[lane & 31] >= 0);
+    const bool masked = base + kRows > ctx || base + kRows > end || good != 0xffffffffu, more = tile + 1 < tiles;
+    if (good != 0xffffffffu) page_err = 1;
+    uint32_t there = good;                            // rows of this step that exist
+    if (end - base < 32) there &= (1u << (end - base)) - 1u;
+
+    dma_wait<kOut ? kLoads : 0>();                    // the keys and scales; the values may be under way
+    f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const unsigned* scales = rows.scales[tile & 1];
+    const unsigned key0 = fresh(key_at);
+    unsigned vscale[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned ks = scales_of(scales[16 * h + c], tile, 16 * h + c);
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(rows.k + (key0 ^ Rows::key_step(st)) + 16 * h * HD);
+        const float f = scale_of(ks >> (8 * st) & 255u);
+        const u32x2 x = values_of<kType>(w[0], f), y = values_of<kType>(w[1], f);
+        s[h] = mfma16(__builtin_bit_cast(bf16x8, (u32x4{x[0], x[1], y[0], y[1]})), qf[st], s[h]);
+      }
       if constexpr (kOut) {
+        // of rows 16 h + 4 g .. + 3, this lane's block
+        const u32x4 w = *reinterpret_cast<const u32x4*>(scales + 32 + 16 * h + 4 * g);
 #pragma unroll
-        for (int f = 0; f < kFeat; ++f)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sh_o[w][c][kFeat * (4 * g + r) + f] = o[f][r];
+        for (int j = 0; j < 4; ++j)
+          vscale[4 * h + j] = scales_of(w[j], tile, 16 * h + 4 * g + j) >> (8 * (c * (HD / 16) / kBlock)) & 255u;
       }
     }
-    __syncthreads();
-    if (wave < half) {
-      const float2 ml = sh_ml[wave][c];
-      const float m_new = fmaxf(m_run, ml.x), zero = m_new == -INFINITY ? 0.f : m_new;
-      const float mine = __builtin_amdgcn_exp2f(m_run - zero), theirs = __builtin_amdgcn_exp2f(ml.x - zero);
+    reads_done();
+    if (more) {
+      if ((tile + 1) % kCodeTiles == 0) {
+        look_up_pages(tile + 1, page);
+        set_slots(tile + 1, page);
+      }
+      load_keys(tile + 1);
+    }
+
+    uint32_t seen = 0xffffffffu;                      // rows that this lane's query sees
+    if (masked) {
+      seen = there;
+      if (base + kRows > ctx) seen &= seen_rows(word, base - ctx);
+    }
+    float x[8];
+    {
+      // rounded here, as the kernel of bf16 caches does, not joined with the subtraction below
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = s[j / 4][j % 4] * scale2;
+    }
+    if (masked) {
+      const uint32_t mine = seen >> (4 * (fresh(lane) >> 4));   // a branch: not what all steps would compute
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(mine >> (16 * (j / 4) + j % 4) & 1)) x[j] = -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+    top = fmaxf(top, other_sixteen(top));
+    top = fmaxf(top, other_half(top));
+    if (__any(top > m_run + kSlack)) {
+      const float m_new = fmaxf(m_run, top);
+      const float shrink = __builtin_amdgcn_exp2f(m_run - (m_new == -INFINITY ? 0.f : m_new));
+      l_run *= shrink;
+      if constexpr (kOut) {
+#pragma unroll
+        for (int f = 0; f < kFeat; ++f) o[f] *= shrink;
+      }
       m_run = m_new;
-      l_run = l_run * mine + ml.y * theirs;
-      if constexpr (kOut) {
+    }
+    const float zero = m_run == -INFINITY ? 0.f : m_run;
+    float p[8], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = __builtin_amdgcn_exp2f(x[j] - zero);
+      sum += p[j];
+    }
+    l_run += sum;
+    if constexpr (kOut) {
+      u32x4 pw[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Weights w = split_weights(p[2 * i], p[2 * i + 1]);
+        pw[0][i] = w.lead;
+        pw[1][i] = w.rest;
+      }
+      if (more)
+        dma_wait<kLoads + 1>();                       // only the next keys and scales may be under way
+      else
+        dma_wait<0>();
+      unsigned w[8][HD / 64];
+      const unsigned value0 = fresh(value_at);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned char* at = rows.v + (value0 ^ Rows::value_step(j % 4)) + j / 4 * 16 * HD;
+        if constexpr (HD == 128) {
+          const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+          w[j][0] = y[0];
+          w[j][1] = y[1];
+        } else {
+          w[j][0] = *reinterpret_cast<const unsigned*>(at);
+        }
+      }
+      reads_done();
+      if (more) load_rows(vbase, rows.v, tile + 1);
+      uint32_t lost = 0u;                             // rows whose block of this lane's outputs is NaN
+      if (masked) {
+        // 0 times what a query does not see has to be 0: rows that are not there and NaN blocks become 0;
+        // queries that see such a block get its NaN below
+        const int g = fresh(lane) >> 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 16 * (j / 4) + 4 * g + j % 4;
+          bool gone = !(there >> r & 1), nan = false;
+#pragma unroll
+          for (int i = 0; i < HD / 64; ++i) nan |= not_finite<kType>(w[j][i], vscale[j]);
+          if (nan && !gone) lost |= 1u << r;
+          gone |= nan;
+          if (gone) vscale[j] = 127u;
+#pragma unroll
+          for (int i = 0; i < HD / 64; ++i)
+            if (gone) w[j][i] = 0u;
+        }
+        if (__any(lost != 0u)) {
+          // a block lies in 4 (hd 128) or 8 lanes c of all g; its outputs in the lanes of one or two g
+#pragma unroll
+          for (int d = 16; d < 64; d <<= 1) lost |= __shfl_xor(lost, d);
+#pragma unroll
+          for (int d = 1; d < 512 / HD; d <<= 1) lost |= __shfl_xor(lost, d);
+          lost = __shfl(lost, HD == 128 ? 4 * g : 8 * (g / 2));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFeat / 2; ++i) {
+        __builtin_amdgcn_sched_barrier(0);            // features 2 i and 2 i + 1 of every lane's eight
+        unsigned row[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) row[j] = value_pair<kType>(w[j][i / 2], i & 1, scale_of(vscale[j]));
+        u32x4 vf[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) vf[e][q] = half_pair(row[2 * q], row[2 * q + 1], e);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            o[2 * i + e] = mfma16(__builtin_bit_cast(bf16x8, vf[e]), __builtin_bit_cast(bf16x8, pw[n]), o[2 * i + e]);
+      }
+      if (__ballot(masked && (seen & lost)) && (seen & lost)) {
+        asm volatile("");
 #pragma unroll
         for (int f = 0; f < kFeat; ++f)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[f][r] = o[f][r] * mine + sh_o[wave][c][kFeat * (4 * g + r) + f] * theirs;
-      }
-    }
-    __syncthreads();
-  }
-  if (wave != 0 || !in) return;
-  if (pt.at >= 0) {
-    const int64_t part = pt.at + m;
-    if (g == 0) a.part_ml[part] = make_float2(m_run, l_run);
-    if constexpr (kOut) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float* p = a.part_o + part * HD + kFeat * (4 * g + r);
-#pragma unroll
-        for (int f = 0; f < kFeat; f += 4)
-          *reinterpret_cast<f32x4*>(p + f) = f32x4{o[f][r], o[f + 1][r], o[f + 2][r], o[f + 3][r]};
-      }
-    }
-    return;
-  }
-  const int64_t row = first + qi;
-  const bool none = l_run == 0.f;
-  if (a.lse && g == 0) a.lse[row * a.q.n_heads + head] = none ? -INFINITY : m_run * kLn2 + __logf(l_run);
-  if constexpr (kOut) {
-    const float inv = none ? 0.f : 1.f / l_run;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      uint16_t* p = a.out + row * a.out_stride + head * HD + kFeat * (4 * g + r);
-#pragma unroll
-      for (int f = 0; f < kFeat; f += 4) {
-        u32x2 w;
-        w[0] = pack_bf16x2(o[f][r] * inv, o[f + 1][r] * inv);
-        w[1] = pack_bf16x2(o[f + 2][r] * inv, o[f + 3][r] * inv);
-        *reinterpret_cast<u32x2*>(p + f) = none ? u32x2{0u, 0u} : w;
+          for (int r = 0; r < 4; ++r) o[f][r] = NAN;
       }
     }
   }
+  if (page_err && a.report && lane == 0) atomicOr(a.status, kStatusRowsBit);
+  __syncthreads();                                    // all waves are done with their rows
+  const Row q = row_of_query();
+  join_waves<HD, kOut>(a, pt, heads, q.m, q.in, first + q.qi, q.head, m_run, l_run, o, sh.join.o, sh.join.ml);
 }
 
 // More than 16 query rows: bound by the matrix cores and the exponentials, so K and V go
@@ -712,37 +1006,12 @@ constexpr int kTileWaves = 8;
 constexpr int kBufs = 4;
 constexpr int kSlots = 4096;          // cache rows whose slots are looked up at a time
 
-// 16 bytes per lane from base + off (bytes) to the LDS address lds + 16 lane (lds: the same in the wave).  The
-// compiler does not see the load: dma_wait before the barrier that hands the data on.
-__device__ __forceinline__ void dma_row(const uint16_t* base, uint64_t off, uint32_t lds) {
-  const unsigned char* p = reinterpret_cast<const unsigned char*>(base) + off;
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :
-               : "v"(p), "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory", "m0");
-}
-template <int kLeft>                  // until at most kLeft loads are under way
-__device__ __forceinline__ void dma_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLeft) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
 // Whether one of eight bf16 values is infinite or NaN.
 __device__ __forceinline__ bool not_finite(u32x4 w) {
   bool any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
   return any;
-}
-
-// The value of lane ^ 32.
-__device__ __forceinline__ float other_half(float v) {
-  const int x = __builtin_bit_cast(int, v);
-  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -1178,9 +1447,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
 // The first kernel of a call, by its query rows to a workgroup.
 template <int HD, bool kOut, int kType, bool kShared>
 void launch_form(const AttendArgs& a, int rows, unsigned grid, hipStream_t stream) {
-  if (rows == 16)
-    hipLaunchKernelGGL((attend_kernel<HD, kOut, kType, kShared>), dim3(grid), dim3(kThreads), 0, stream, a);
-  else if (rows == 128)
+  if (rows == 16) {
+    if constexpr (kType == RF_CACHE_BF16)
+      hipLaunchKernelGGL((attend_kernel<HD, kOut, kShared>), dim3(grid), dim3(kThreads), 0, stream, a);
+    else
+      hipLaunchKernelGGL((attend_codes_kernel<HD, kOut, kType>), dim3(grid), dim3(kThreads), 0, stream, a);
+  } else if (rows == 128)
     hipLaunchKernelGGL((attend_tile_kernel<HD, 4, kOut, kType, kShared>), dim3(grid), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((attend_tile_kernel<HD, 8, kOut, kType, kShared>), dim3(grid), dim3(512), 0, stream, a);

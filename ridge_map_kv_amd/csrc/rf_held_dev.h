@@ -5,7 +5,7 @@
 // code 2^e; the scale byte is e + 127.  These values have at most eight significant bits and are
 // normal numbers of bf16, so that a bf16 operand of the matrix cores holds each exactly, and whatever
 // reads such a cache computes what it would from a bf16 cache of them.  A block that holds an infinity
-// or NaN is NaN altogether: scale byte 255.
+// or NaN is NaN altogether: scale byte 255, codes 0 (int8: 0 times infinity) or 0x7f (e4m3).
 #pragma once
 
 #include "rf_common.h"
@@ -53,24 +53,43 @@ __device__ __forceinline__ u32x2 codes_of(const float (&x)[8], int byte) {
   return w;
 }
 
-// The factor of a block's codes: 2^(byte - 127), infinity for a NaN block (which makes any code NaN in
-// both conversions below).
+// The factor of a block's codes: 2^(byte - 127), infinity for a NaN block (which makes its codes NaN in both
+// conversions below).
 __device__ __forceinline__ float scale_of(unsigned byte) { return __uint_as_float(byte << 23); }
 
 // The values of four codes as bf16 pairs.  e4m3: one instruction for two codes, exact for the scale
-// bytes above.  int8: code + 128 as a float, then (code + 128) s - 128 s in one step, exact too.
+// bytes above.  int8: code and product as floats, exact too.
 template <int kType>
 __device__ __forceinline__ u32x2 values_of(unsigned w, float s) {
   if constexpr (kType == RF_CACHE_FP8) {
     return {__builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)),
             __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))};
   } else {
-    const unsigned u = w ^ 0x80808080u;
-    const float off = -128.f * s;
     float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = fmaf((float)(u >> (8 * i) & 0xffu), s, off);
+    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i)) * s;
     return {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  }
+}
+
+// Whether one of four codes stands for NaN.
+template <int kType>
+__device__ __forceinline__ bool not_finite(unsigned w, unsigned byte) {
+  if (byte == kScaleNan) return true;
+  if (kType != RF_CACHE_FP8) return false;
+  const unsigned x = ~w & 0x7f7f7f7fu;              // a byte 0 where the code is 0x7f or 0xff
+  return ((x - 0x01010101u) & ~x & 0x80808080u) != 0u;
+}
+
+// Those of two codes of a word, the first two or the last.
+template <int kType>
+__device__ __forceinline__ unsigned value_pair(unsigned w, bool second, float s) {
+  if constexpr (kType == RF_CACHE_FP8) {
+    return second ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))
+                  : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+  } else {
+    const unsigned u = second ? w >> 16 : w;
+    return pack_bf16x2((float)(int8_t)u * s, (float)(int8_t)(u >> 8) * s);
   }
 }
 

@@ -93,10 +93,18 @@ def test_cache_attention(name, kind):
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
 @pytest.mark.parametrize("name", CASES)
 def test_codes_give_what_their_values_give(name, kind):
+    # the same operands of the same products: kernels of more than 16 query rows give the same bits, those of up to
+    # 16 cut the rows into other parts, so that each may be off by its own tolerance
     c, q, starts, words, max_q = _make(CASES[name], kind, seed=2)
     got = _attend(c, q, starts, words, max_q, 0.1)
     want = _attend(c, q, starts, words, max_q, 0.1, cache=c.values(B))
-    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    group = q.shape[1] // c.n_kv
+    if max_q * group > 16 and (not c.plens or starts[-1] * group > 64):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    else:
+        _, _, ot, lt = S.attention(c, q, starts, words, 0.1)
+        _close(got[0], want[0].cpu().double(), 2 * ot, "out")
+        _close(got[1], want[1].cpu().double(), 2 * lt, "lse")
 
 
 @pytest.mark.parametrize("name", [n for n in CASES if n.startswith("no prefix")])
@@ -197,6 +205,18 @@ def test_bounds_larger_than_what_there_is():
                 n = q.shape[0]
                 _check(c, q, starts, words, max_q, 0.09, out[:n], lse[:n])
                 assert (out[n:] == 3).all()
+
+
+@pytest.mark.parametrize("kind", H.KINDS)
+def test_no_queries(kind):
+    c, q, starts, words, _ = _make(([5, 9], [0, 0], [40], [0, 2], 4, 2, 64, 16, False), kind)
+    for max_q in (1, 20):
+        out, lse, st = _attend(c, q, starts, words, max_q, 0.1, n_pad=2)
+        assert st == B.RF_OK and (out == 3).all() and (lse == 3).all()
+        kv, pre = c.kv(B), c.prefix(B)
+        ws = torch.empty(B.ridgefill_cache_attention_workspace_bytes(kv, 4, max_q, 0, pre), dtype=torch.uint8, device=DEV)
+        B.ridgefill_cache_attention(kv, c.cache(B), q, torch.tensor(starts, dtype=torch.int32, device=DEV), max_q, 0.1, q, ws, prefix=pre)
+        assert B.ridgefill_read_status(ws) == B.RF_OK
 
 
 @pytest.mark.parametrize("batch,groups", [(150, 3), (200, 100), (70, 70)])

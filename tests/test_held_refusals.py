@@ -262,7 +262,7 @@ def test_prefix_refusals():
 
 def test_attention_workspace():
     size = B.ridgefill_cache_attention_workspace_bytes
-    assert size(_kv(), 4, 2, 3) == B.ridgefill_tree_attention_workspace_bytes(_kv(), 4, 2) > 0
+    assert size(_kv(), 4, 2, 3) >= B.ridgefill_tree_attention_workspace_bytes(_kv(), 4, 2) > 0
     assert size(_kv(), 4, 2, 3, _prefix()) > size(_kv(), 4, 2, 3)
     # more queries than the sequences can have need no more
     assert size(_kv(), 4, 2, 1 << 30, _prefix()) == size(_kv(), 4, 2, 4, _prefix())
