@@ -19,7 +19,13 @@ namespace rf {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 2;               // heads of a thread under way
+// Heads that a thread takes in turn where there are rows for kBlocks workgroups, forward: for 8,191 rows of 40 heads
+// of 128 features in bf16 (168 MB read and written) 37.5 us with 3, 39.3 with 4, 41.8 with 2, 57.7 with 2 under way
+// at a time.
+constexpr int kRounds = 3, kBlocks = 2048;
+// Backward, and its workgroups to a compute unit: 8,192 rows of 48 heads of 128 in bf16 (302 MB) 70.5 us with 4 and 3,
+// 81 with 8 and 3, 80.5 with 2 workgroups, 128 with 4 (registers in scratch memory).
+constexpr int kGradRounds = 4, kGradGroups = 3;
 
 template <int kControl>
 __device__ __forceinline__ float lanes(float v) {
@@ -43,7 +49,8 @@ __device__ __forceinline__ float sum_lanes(float v, int lp) {
 
 // How a workgroup's threads lie over the heads of its rows.
 struct Layout {
-  Divide heads;                 // of a row
+  Divide heads;                 // of a row, and of each of its tensors
+  Divide q_heads, k_heads;
   int lp, shift;                // lanes of a head: 2^shift
   int per;                      // rows of a workgroup
 };
@@ -81,185 +88,185 @@ __device__ __forceinline__ float squares(const float (&a)[kN], const float (&b)[
   return s;
 }
 
-// A thread's two pieces of the heads' weights, q's and k's.
+// A thread's two pieces of a weight.
 template <typename T>
-struct Weights {
-  Piece<T> lo[2], hi[2];
-  __device__ void load(int t, const void* w, const Unit& u) {
-    lo[t].r = hi[t].r = u32x4{0u, 0u, 0u, 0u};
+struct Weight {
+  Piece<T> lo, hi;
+  __device__ void load(const void* w, const Unit& u) {
+    lo.r = hi.r = u32x4{0u, 0u, 0u, 0u};
     if (!w) return;
-    lo[t].r = *reinterpret_cast<const u32x4*>(static_cast<const T*>(w) + u.lo);
-    hi[t].r = *reinterpret_cast<const u32x4*>(static_cast<const T*>(w) + u.hi);
-  }
-  __device__ void get(bool k, float (&a)[Piece<T>::kN], float (&b)[Piece<T>::kN]) const {
-    Piece<T> l, h;                                  // chosen, not indexed: they stay in registers
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      l.r[i] = k ? lo[1].r[i] : lo[0].r[i];
-      h.r[i] = k ? hi[1].r[i] : hi[0].r[i];
-    }
-    l.get(a);
-    h.get(b);
+    lo.r = *reinterpret_cast<const u32x4*>(static_cast<const T*>(w) + u.lo);
+    hi.r = *reinterpret_cast<const u32x4*>(static_cast<const T*>(w) + u.hi);
   }
 };
 
+// A thread's place: its unit of a head, and which of the heads that the workgroup takes at a time.
+template <typename T>
+struct Seat {
+  Unit u;
+  int slot, slots;
+  bool in_head;
+  __device__ Seat(const RopeFreq& f, int hd, const Layout& l) {
+    const int at = threadIdx.x & (l.lp - 1);
+    slot = threadIdx.x >> l.shift;
+    slots = kThreads >> l.shift;
+    in_head = at < hd / (2 * Piece<T>::kN);
+    u = unit_of<T>(f, hd, in_head ? at : 0);
+  }
+};
+
+// q's heads of the rows first, then k's: a thread's weight and sums are one tensor's at a time.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeFreq f, NormCall c, Layout l) {
   constexpr int kN = Piece<T>::kN;
   extern __shared__ float2 cs[];                    // [per][rot / 2]
   const int64_t row0 = (int64_t)blockIdx.x * l.per;
   const int rows = (int)(c.n - row0 < l.per ? c.n - row0 : l.per);
-  const int pairs = f.rot / 2, total = rows * (int)l.heads.d, slots = kThreads >> l.shift;
-  const int at = threadIdx.x & (l.lp - 1), slot = threadIdx.x >> l.shift;
-  const bool in_head = at < c.hd / (2 * kN);
-  const Unit u = unit_of<T>(f, c.hd, in_head ? at : 0);
+  const int pairs = f.rot / 2;
+  const Seat<T> seat(f, c.hd, l);
+  const Unit u = seat.u;
   const float inv_hd = 1.f / (float)c.hd;
-  Weights<T> w;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) w.load(t, c.t[t].w, u);
-  for (int i0 = 0; i0 == 0 || i0 < total; i0 += kUnits * slots) {
-    Piece<T> lo[kUnits], hi[kUnits];
-    int row[kUnits], head[kUnits];
-    bool is_k[kUnits], in[kUnits];
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int i = i0 + j * slots + slot;
-      in[j] = i < total && in_head;
-      row[j] = (int)quotient((unsigned)(in[j] ? i : 0), l.heads);
-      const int h = (in[j] ? i : 0) - row[j] * (int)l.heads.d;
-      is_k[j] = h >= c.t[0].heads;
-      head[j] = is_k[j] ? h - c.t[0].heads : h;
-      lo[j].r = hi[j].r = u32x4{0u, 0u, 0u, 0u};
-      if (in[j]) {
-        const T* x = static_cast<const T*>(is_k[j] ? c.t[1].x : c.t[0].x) +
-                     (row0 + row[j]) * (is_k[j] ? c.t[1].x_stride : c.t[0].x_stride) + head[j] * c.hd;
-        lo[j].r = *reinterpret_cast<const u32x4*>(x + u.lo);
-        hi[j].r = *reinterpret_cast<const u32x4*>(x + u.hi);
+  bool filled = false;
+  const auto tensor = [&](const NormTensor& t, Divide by_heads) {
+    Weight<T> w;
+    w.load(t.w, u);
+    const int total = rows * t.heads;
+    for (int i0 = 0; i0 < total; i0 += seat.slots) {
+      const int i = i0 + seat.slot;
+      const bool in = i < total && seat.in_head;
+      const int row = (int)quotient((unsigned)(in ? i : 0), by_heads), head = (in ? i : 0) - row * t.heads;
+      Piece<T> lo, hi;
+      lo.r = hi.r = u32x4{0u, 0u, 0u, 0u};
+      if (in) {
+        const T* x = static_cast<const T*>(t.x) + (row0 + row) * t.x_stride + head * c.hd;
+        lo.r = *reinterpret_cast<const u32x4*>(x + u.lo);
+        hi.r = *reinterpret_cast<const u32x4*>(x + u.hi);
       }
-    }
-    if (i0 == 0) {
-      fill_turns(cs, f, c.pos, row0, rows, 1.f);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
+      if (!filled) {
+        fill_turns(cs, f, c.pos, row0, rows, 1.f);
+        __syncthreads();
+        filled = true;
+      }
       float a[kN], b[kN];
-      lo[j].get(a);
-      hi[j].get(b);
-      const float mean = sum_lanes(squares(a, b), l.lp) * inv_hd;
-      const bool normed = is_k[j] ? c.t[1].w != nullptr : c.t[0].w != nullptr, turned = u.pair_lo >= 0;
-      if (normed) {
-        const float r = 1.f / sqrtf(mean + c.eps);
+      lo.get(a);
+      hi.get(b);
+      const bool turned = u.pair_lo >= 0;
+      if (t.w) {
+        const float r = 1.f / sqrtf(sum_lanes(squares(a, b), l.lp) * inv_hd + c.eps);
         float x[kN], y[kN];
-        w.get(is_k[j], x, y);
+        w.lo.get(x);
+        w.hi.get(y);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
           a[i] = a[i] * r * x[i];
           b[i] = b[i] * r * y[i];
         }
       }
-      if (turned) turn_values<kN>(a, b, cs + row[j] * pairs, u, f.layout != RF_ROPE_HALF);
-      if (normed || turned) {
-        lo[j].set(a);
-        hi[j].set(b);
+      if (turned) turn_values<kN>(a, b, cs + row * pairs, u, f.layout != RF_ROPE_HALF);
+      if (t.w || turned) {
+        lo.set(a);
+        hi.set(b);
       }
-      if (in[j]) {
-        T* out = static_cast<T*>(is_k[j] ? c.t[1].out : c.t[0].out) +
-                 (row0 + row[j]) * (is_k[j] ? c.t[1].out_stride : c.t[0].out_stride) + head[j] * c.hd;
-        *reinterpret_cast<u32x4*>(out + u.lo) = lo[j].r;
-        *reinterpret_cast<u32x4*>(out + u.hi) = hi[j].r;
+      if (in) {
+        T* out = static_cast<T*>(t.out) + (row0 + row) * t.out_stride + head * c.hd;
+        *reinterpret_cast<u32x4*>(out + u.lo) = lo.r;
+        *reinterpret_cast<u32x4*>(out + u.hi) = hi.r;
       }
     }
-  }
+  };
+  tensor(c.t[0], l.q_heads);
+  tensor(c.t[1], l.k_heads);
 }
 
 // Backward.  A workgroup takes row blocks in turn and keeps its threads' share of both weights'
 // gradients in fp32; what all of them hold goes to `part` [workgroups][2][hd], which a second launch
 // adds in a fixed order.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void norm_grad_kernel(RopeFreq f, NormCall c, Layout l, float* part) {
+__global__ __launch_bounds__(kThreads, kGradGroups) void norm_grad_kernel(RopeFreq f, NormCall c, Layout l, float* part) {
   constexpr int kN = Piece<T>::kN;
   extern __shared__ float2 cs[];                    // [per][rot / 2]; at the end [4][2][hd] floats
-  const int pairs = f.rot / 2, slots = kThreads >> l.shift;
-  const int at = threadIdx.x & (l.lp - 1), slot = threadIdx.x >> l.shift;
-  const bool in_head = at < c.hd / (2 * kN);
-  const Unit u = unit_of<T>(f, c.hd, in_head ? at : 0);
+  const int pairs = f.rot / 2;
+  const Seat<T> seat(f, c.hd, l);
+  const Unit u = seat.u;
   const float inv_hd = 1.f / (float)c.hd;
-  Weights<T> w;
+  Weight<T> w[2];
   float acc[2][2 * kN];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    w.load(t, c.t[t].w, u);
+    w[t].load(c.t[t].w, u);
 #pragma unroll
     for (int i = 0; i < 2 * kN; ++i) acc[t][i] = 0.f;
   }
   for (int64_t row0 = (int64_t)blockIdx.x * l.per; row0 < c.n; row0 += (int64_t)gridDim.x * l.per) {
-    const int rows = (int)(c.n - row0 < l.per ? c.n - row0 : l.per), total = rows * (int)l.heads.d;
+    const int rows = (int)(c.n - row0 < l.per ? c.n - row0 : l.per);
+    bool filled = false;
     __syncthreads();                                // the rows before are done with
-    for (int i0 = 0; i0 == 0 || i0 < total; i0 += slots) {
-      const int i = i0 + slot;
-      const bool in = i < total && in_head;
-      const int row = (int)quotient((unsigned)(in ? i : 0), l.heads), h = (in ? i : 0) - row * (int)l.heads.d;
-      const bool k = h >= c.t[0].heads, normed = k ? c.t[1].w != nullptr : c.t[0].w != nullptr;
-      const int head = k ? h - c.t[0].heads : h;
-      Piece<T> xl, xh, gl, gh;
-      xl.r = xh.r = gl.r = gh.r = u32x4{0u, 0u, 0u, 0u};
-      if (in) {
-        const T* x = static_cast<const T*>(k ? c.t[1].x : c.t[0].x) + (row0 + row) * (k ? c.t[1].x_stride : c.t[0].x_stride) + head * c.hd;
-        const T* g = static_cast<const T*>(k ? c.t[1].g : c.t[0].g) + (row0 + row) * (k ? c.t[1].g_stride : c.t[0].g_stride) + head * c.hd;
-        if (normed) {
-          xl.r = *reinterpret_cast<const u32x4*>(x + u.lo);
-          xh.r = *reinterpret_cast<const u32x4*>(x + u.hi);
+    const auto tensor = [&](const NormTensor& t, Divide by_heads, const Weight<T>& weight, float (&sums)[2 * kN]) {
+      const int total = rows * t.heads;
+      for (int i0 = 0; i0 < total; i0 += seat.slots) {
+        const int i = i0 + seat.slot;
+        const bool in = i < total && seat.in_head;
+        const int row = (int)quotient((unsigned)(in ? i : 0), by_heads), head = (in ? i : 0) - row * t.heads;
+        Piece<T> xl, xh, gl, gh;
+        xl.r = xh.r = gl.r = gh.r = u32x4{0u, 0u, 0u, 0u};
+        if (in) {
+          const T* g = static_cast<const T*>(t.g) + (row0 + row) * t.g_stride + head * c.hd;
+          gl.r = *reinterpret_cast<const u32x4*>(g + u.lo);
+          gh.r = *reinterpret_cast<const u32x4*>(g + u.hi);
+          if (t.w) {
+            const T* x = static_cast<const T*>(t.x) + (row0 + row) * t.x_stride + head * c.hd;
+            xl.r = *reinterpret_cast<const u32x4*>(x + u.lo);
+            xh.r = *reinterpret_cast<const u32x4*>(x + u.hi);
+          }
         }
-        gl.r = *reinterpret_cast<const u32x4*>(g + u.lo);
-        gh.r = *reinterpret_cast<const u32x4*>(g + u.hi);
-      }
-      if (i0 == 0) {
-        fill_turns(cs, f, c.pos, row0, rows, -1.f);
-        __syncthreads();
-      }
-      float xa[kN], xb[kN], ga[kN], gb[kN];
-      xl.get(xa);
-      xh.get(xb);
-      gl.get(ga);
-      gh.get(gb);
-      if (u.pair_lo >= 0) turn_values<kN>(ga, gb, cs + row * pairs, u, f.layout != RF_ROPE_HALF);
-      float wa[kN], wb[kN], dot = 0.f;
-      w.get(k, wa, wb);
+        if (!filled) {
+          fill_turns(cs, f, c.pos, row0, rows, -1.f);
+          __syncthreads();
+          filled = true;
+        }
+        float ga[kN], gb[kN];
+        gl.get(ga);
+        gh.get(gb);
+        if (u.pair_lo >= 0) turn_values<kN>(ga, gb, cs + row * pairs, u, f.layout != RF_ROPE_HALF);
+        if (t.w) {
+          float xa[kN], xb[kN], wa[kN], wb[kN], dot = 0.f;
+          xl.get(xa);
+          xh.get(xb);
+          weight.lo.get(wa);
+          weight.hi.get(wb);
 #pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        wa[e] *= ga[e];
-        wb[e] *= gb[e];
-        dot = fmaf(wa[e], xa[e], dot);
-        dot = fmaf(wb[e], xb[e], dot);
-      }
-      const float mean = sum_lanes(squares(xa, xb), l.lp) * inv_hd;
-      dot = sum_lanes(in ? dot : 0.f, l.lp);
-      if (normed) {
-        const float r = 1.f / sqrtf(mean + c.eps), back = r * r * dot * inv_hd;
+          for (int e = 0; e < kN; ++e) {
+            wa[e] *= ga[e];
+            wb[e] *= gb[e];
+            dot = fmaf(wa[e], xa[e], dot);
+            dot = fmaf(wb[e], xb[e], dot);
+          }
+          const float mean = sum_lanes(squares(xa, xb), l.lp) * inv_hd;
+          dot = sum_lanes(in ? dot : 0.f, l.lp);
+          // no head, no share (r may be infinite there)
+          const float r = 1.f / sqrtf(mean + c.eps), back = r * r * dot * inv_hd;
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          // both tensors' sums in registers: chosen, not indexed; nothing where there is no head (r may
-          // be infinite there)
-          const float da = in ? ga[e] * xa[e] * r : 0.f, db = in ? gb[e] * xb[e] * r : 0.f;
-          acc[0][e] += k ? 0.f : da;
-          acc[1][e] += k ? da : 0.f;
-          acc[0][kN + e] += k ? 0.f : db;
-          acc[1][kN + e] += k ? db : 0.f;
-          ga[e] = r * (wa[e] - xa[e] * back);
-          gb[e] = r * (wb[e] - xb[e] * back);
+          for (int e = 0; e < kN; ++e) {
+            const float da = ga[e] * xa[e] * r, db = gb[e] * xb[e] * r;
+            sums[e] += in ? da : 0.f;
+            sums[kN + e] += in ? db : 0.f;
+            ga[e] = r * (wa[e] - xa[e] * back);
+            gb[e] = r * (wb[e] - xb[e] * back);
+          }
+        }
+        if (t.w || u.pair_lo >= 0) {
+          gl.set(ga);
+          gh.set(gb);
+        }
+        if (in) {
+          T* out = static_cast<T*>(t.out) + (row0 + row) * t.out_stride + head * c.hd;
+          *reinterpret_cast<u32x4*>(out + u.lo) = gl.r;
+          *reinterpret_cast<u32x4*>(out + u.hi) = gh.r;
         }
       }
-      if (normed || u.pair_lo >= 0) {
-        gl.set(ga);
-        gh.set(gb);
-      }
-      if (in) {
-        T* out = static_cast<T*>(k ? c.t[1].out : c.t[0].out) + (row0 + row) * (k ? c.t[1].out_stride : c.t[0].out_stride) + head * c.hd;
-        *reinterpret_cast<u32x4*>(out + u.lo) = gl.r;
-        *reinterpret_cast<u32x4*>(out + u.hi) = gh.r;
-      }
-    }
+    };
+    tensor(c.t[0], l.q_heads, w[0], acc[0]);
+    tensor(c.t[1], l.k_heads, w[1], acc[1]);
   }
   // the lanes that hold the same place of a head, then the waves
   float* sh = reinterpret_cast<float*>(cs);
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(RopeFreq f, NormCal
     for (int i = 0; i < 2 * kN; ++i) {
       float v = acc[t][i];
       for (int d = l.lp; d < 64; d <<= 1) v += __shfl_xor(v, d);
-      if (lane < l.lp && in_head) sh[(wave * 2 + t) * c.hd + (i < kN ? u.lo + i : u.hi + i - kN)] = v;
+      if (lane < l.lp && seat.in_head) sh[(wave * 2 + t) * c.hd + (i < kN ? u.lo + i : u.hi + i - kN)] = v;
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * c.hd; i += kThreads) {
@@ -282,17 +289,27 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(RopeFreq f, NormCal
   }
 }
 
-// Sixteen columns of [parts][2 hd] to a workgroup, sixteen rows at a time.
-__global__ __launch_bounds__(kThreads) void norm_grad_sum_kernel(NormCall c, const float* part, int parts) {
-  __shared__ float sh[16][17];
+// Sixteen columns of [parts][2 hd] to a workgroup, 64 rows at a time (sixteen at a time took 16 us for 768 parts).
+__global__ __launch_bounds__(1024) void norm_grad_sum_kernel(NormCall c, const float* part, int parts) {
+  constexpr int kRowsAt = 64, kAhead = 4;
+  __shared__ float sh[kRowsAt][17];
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 16 + x;
   float v = 0.f;
-  for (int p = y; p < parts; p += 16) v += part[(int64_t)p * 2 * c.hd + col];
+  for (int p0 = y; p0 < parts; p0 += kRowsAt * kAhead) {
+    float at[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int p = p0 + i * kRowsAt;
+      at[i] = p < parts ? part[(int64_t)p * 2 * c.hd + col] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) v += at[i];
+  }
   sh[y][x] = v;
   __syncthreads();
   if (y) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) v += sh[i][x];
+  for (int i = 1; i < kRowsAt; ++i) v += sh[i][x];
   const int t = col >= c.hd;
   if (c.t[t].dw && c.t[t].w) c.t[t].dw[col - t * c.hd] = v;
 }
@@ -316,28 +333,22 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(RopeFreq f, Batch b, Hol
   const bool in_head = at < hd / (2 * kN);
   const Unit u = unit_of<uint16_t>(f, hd, in_head ? at : 0);
   const float inv_hd = 1.f / (float)hd;
-  Weights<uint16_t> w;
-  w.load(0, c.q_w, u);
-  w.load(1, c.k_w, u);
-  for (int i0 = 0; i0 == 0 || i0 < total; i0 += kUnits * slots) {
-    Piece<uint16_t> lo[kUnits], hi[kUnits];
-    int row[kUnits], head[kUnits];
-    bool in[kUnits];
-#pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int i = i0 + j * slots + slot;
-      in[j] = i < total && in_head;
-      row[j] = (int)quotient((unsigned)(in[j] ? i : 0), l.heads);
-      const int h = head[j] = (in[j] ? i : 0) - row[j] * (int)l.heads.d;
-      lo[j].r = hi[j].r = u32x4{0u, 0u, 0u, 0u};
-      if (in[j]) {
-        const int64_t r = row0 + row[j];
-        const uint16_t* x = h < c.a.n_q ? c.a.q + r * c.a.q_stride + h * hd
-                            : h < c.a.n_q + b.n_kv ? c.a.k + r * c.a.k_stride + (h - c.a.n_q) * hd
-                                                   : c.a.v + r * c.a.v_stride + (h - c.a.n_q - b.n_kv) * hd;
-        lo[j].r = *reinterpret_cast<const u32x4*>(x + u.lo);
-        hi[j].r = *reinterpret_cast<const u32x4*>(x + u.hi);
-      }
+  Weight<uint16_t> w[2];
+  w[0].load(c.q_w, u);
+  w[1].load(c.k_w, u);
+  for (int i0 = 0; i0 == 0 || i0 < total; i0 += slots) {
+    const int i = i0 + slot;
+    const bool in = i < total && in_head;
+    const int row = (int)quotient((unsigned)(in ? i : 0), l.heads), h = (in ? i : 0) - row * (int)l.heads.d;
+    Piece<uint16_t> lo, hi;
+    lo.r = hi.r = u32x4{0u, 0u, 0u, 0u};
+    if (in) {
+      const int64_t r = row0 + row;
+      const uint16_t* x = h < c.a.n_q ? c.a.q + r * c.a.q_stride + h * hd
+                          : h < c.a.n_q + b.n_kv ? c.a.k + r * c.a.k_stride + (h - c.a.n_q) * hd
+                                                 : c.a.v + r * c.a.v_stride + (h - c.a.n_q - b.n_kv) * hd;
+      lo.r = *reinterpret_cast<const u32x4*>(x + u.lo);
+      hi.r = *reinterpret_cast<const u32x4*>(x + u.hi);
     }
     if (i0 == 0) {
       for (int r = threadIdx.x; r < rows; r += kThreads) {
@@ -349,76 +360,80 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(RopeFreq f, Batch b, Hol
       fill_turns<kType != RF_CACHE_BF16>(cs, f, pos, row0, rows, 1.f);
       __syncthreads();
     }
+    float x[kN], y[kN];
+    lo.get(x);
+    hi.get(y);
+    const int kind = h < c.a.n_q ? 0 : h < c.a.n_q + b.n_kv ? 1 : 2;
+    const float mean = sum_lanes(squares(x, y), l.lp) * inv_hd;
+    const bool normed = kind == 0 ? c.q_w != nullptr : kind == 1 && c.k_w, turned = kind < 2 && u.pair_lo >= 0;
+    if (normed) {
+      const float r = 1.f / sqrtf(mean + c.eps);
+      float s[kN], t[kN];
+      Weight<uint16_t> one;                         // chosen, not indexed: they stay in registers
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      float x[kN], y[kN];
-      lo[j].get(x);
-      hi[j].get(y);
-      const int h = head[j], kind = h < c.a.n_q ? 0 : h < c.a.n_q + b.n_kv ? 1 : 2;
-      const float mean = sum_lanes(squares(x, y), l.lp) * inv_hd;
-      const bool normed = kind == 0 ? c.q_w != nullptr : kind == 1 && c.k_w, turned = kind < 2 && u.pair_lo >= 0;
-      if (normed) {
-        const float r = 1.f / sqrtf(mean + c.eps);
-        float s[kN], t[kN];
-        w.get(kind == 1, s, t);
+      for (int i = 0; i < 4; ++i) {
+        one.lo.r[i] = kind == 1 ? w[1].lo.r[i] : w[0].lo.r[i];
+        one.hi.r[i] = kind == 1 ? w[1].hi.r[i] : w[0].hi.r[i];
+      }
+      one.lo.get(s);
+      one.hi.get(t);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          x[i] = x[i] * r * s[i];
-          y[i] = y[i] * r * t[i];
+      for (int i = 0; i < kN; ++i) {
+        x[i] = x[i] * r * s[i];
+        y[i] = y[i] * r * t[i];
+      }
+    }
+    if (turned) turn_values<kN>(x, y, cs + row * pairs, u, f.layout != RF_ROPE_HALF);
+    const int place = places[row];
+    if (normed || turned) {
+      lo.set(x);
+      hi.set(y);
+    }
+    if (kind == 0 || kType == RF_CACHE_BF16) {
+      const int64_t base = kind == 0 ? 0 : ((int64_t)place * b.n_kv + (h - c.a.n_q - (kind == 2 ? b.n_kv : 0))) * hd;
+      uint16_t* out = kind == 0 ? c.a.q_out + (row0 + row) * c.a.qo_stride + h * hd
+                                : static_cast<uint16_t*>(kind == 1 ? c.pools.k : c.pools.v) + base;
+      if (in && (kind == 0 ? place != -2 : place >= 0)) {
+        *reinterpret_cast<u32x4*>(out + u.lo) = lo.r;
+        *reinterpret_cast<u32x4*>(out + u.hi) = hi.r;
+      }
+    }
+    if constexpr (kType != RF_CACHE_BF16) {
+      // magnitudes as whole numbers, which order NaN above infinity
+      unsigned top[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const unsigned p = __float_as_uint(x[i]) & 0x7fffffffu, q = __float_as_uint(y[i]) & 0x7fffffffu;
+        top[0] = top[0] > p ? top[0] : p;
+        top[1] = top[1] > q ? top[1] : q;
+      }
+      const auto most = [](float p, float q) {
+        const unsigned a = __float_as_uint(p), c = __float_as_uint(q);
+        return __uint_as_float(a > c ? a : c);
+      };
+      if (aligned_blocks(f.rot, hd)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) top[e] = __float_as_uint(over_lanes(__uint_as_float(top[e]), 4, most));
+      } else {
+        const unsigned mine[2] = {top[0], top[1]};
+        for (int k = 0; k < hd / kBlock; ++k) {
+          unsigned t = u.lo / kBlock == k ? mine[0] : 0u;
+          if (u.hi / kBlock == k) t = t > mine[1] ? t : mine[1];
+          if (!in_head) t = 0u;
+          t = __float_as_uint(over_lanes(__uint_as_float(t), l.lp, most));
+          if (u.lo / kBlock == k) top[0] = t;
+          if (u.hi / kBlock == k) top[1] = t;
         }
       }
-      if (turned) turn_values<kN>(x, y, cs + row[j] * pairs, u, f.layout != RF_ROPE_HALF);
-      const int place = places[row[j]];
-      if (normed || turned) {
-        lo[j].set(x);
-        hi[j].set(y);
-      }
-      if (kind == 0 || kType == RF_CACHE_BF16) {
-        const int64_t base = kind == 0 ? 0 : ((int64_t)place * b.n_kv + (h - c.a.n_q - (kind == 2 ? b.n_kv : 0))) * hd;
-        uint16_t* out = kind == 0 ? c.a.q_out + (row0 + row[j]) * c.a.qo_stride + h * hd
-                                  : static_cast<uint16_t*>(kind == 1 ? c.pools.k : c.pools.v) + base;
-        if (in[j] && (kind == 0 ? place != -2 : place >= 0)) {
-          *reinterpret_cast<u32x4*>(out + u.lo) = lo[j].r;
-          *reinterpret_cast<u32x4*>(out + u.hi) = hi[j].r;
-        }
-      }
-      if constexpr (kType != RF_CACHE_BF16) {
-        // magnitudes as whole numbers, which order NaN above infinity
-        unsigned top[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const unsigned p = __float_as_uint(x[i]) & 0x7fffffffu, q = __float_as_uint(y[i]) & 0x7fffffffu;
-          top[0] = top[0] > p ? top[0] : p;
-          top[1] = top[1] > q ? top[1] : q;
-        }
-        const auto most = [](float p, float q) {
-          const unsigned a = __float_as_uint(p), c = __float_as_uint(q);
-          return __uint_as_float(a > c ? a : c);
-        };
-        if (aligned_blocks(f.rot, hd)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) top[e] = __float_as_uint(over_lanes(__uint_as_float(top[e]), 4, most));
-        } else {
-          const unsigned mine[2] = {top[0], top[1]};
-          for (int k = 0; k < hd / kBlock; ++k) {
-            unsigned t = u.lo / kBlock == k ? mine[0] : 0u;
-            if (u.hi / kBlock == k) t = t > mine[1] ? t : mine[1];
-            if (!in_head) t = 0u;
-            t = __float_as_uint(over_lanes(__uint_as_float(t), l.lp, most));
-            if (u.lo / kBlock == k) top[0] = t;
-            if (u.hi / kBlock == k) top[1] = t;
-          }
-        }
-        if (in[j] && kind != 0 && place >= 0) {
-          const int64_t at_head = (int64_t)place * b.n_kv + (h - c.a.n_q - (kind == 2 ? b.n_kv : 0));
-          uint8_t* codes = static_cast<uint8_t*>(kind == 1 ? c.pools.k : c.pools.v) + at_head * hd;
-          uint8_t* scales = (kind == 1 ? c.pools.ks : c.pools.vs) + at_head * (hd / kBlock);
-          const int s0 = scale_byte<kType>(top[0]), s1 = scale_byte<kType>(top[1]);
-          *reinterpret_cast<u32x2*>(codes + u.lo) = codes_of<kType>(x, s0);
-          *reinterpret_cast<u32x2*>(codes + u.hi) = codes_of<kType>(y, s1);
-          if (u.lo % kBlock == 0) scales[u.lo / kBlock] = (uint8_t)s0;
-          if (u.hi % kBlock == 0) scales[u.hi / kBlock] = (uint8_t)s1;
-        }
+      if (in && kind != 0 && place >= 0) {
+        const int64_t at_head = (int64_t)place * b.n_kv + (h - c.a.n_q - (kind == 2 ? b.n_kv : 0));
+        uint8_t* codes = static_cast<uint8_t*>(kind == 1 ? c.pools.k : c.pools.v) + at_head * hd;
+        uint8_t* scales = (kind == 1 ? c.pools.ks : c.pools.vs) + at_head * (hd / kBlock);
+        const int s0 = scale_byte<kType>(top[0]), s1 = scale_byte<kType>(top[1]);
+        *reinterpret_cast<u32x2*>(codes + u.lo) = codes_of<kType>(x, s0);
+        *reinterpret_cast<u32x2*>(codes + u.hi) = codes_of<kType>(y, s1);
+        if (u.lo % kBlock == 0) scales[u.lo / kBlock] = (uint8_t)s0;
+        if (u.hi % kBlock == 0) scales[u.hi / kBlock] = (uint8_t)s1;
       }
     }
   }
@@ -476,7 +491,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(Batch b, ReadCall c, Div
 }
 
 Layout layout_of(int heads, int units) {
-  Layout l = {divide_by((unsigned)heads), 1, 0, 1};
+  Layout l = {divide_by((unsigned)heads), divide_by(1u), divide_by(1u), 1, 0, 1};
   while (l.lp < units) {
     l.lp *= 2;
     ++l.shift;
@@ -484,18 +499,27 @@ Layout layout_of(int heads, int units) {
   return l;
 }
 
-// Rows per workgroup: enough that its threads all have work, one for wide rows.
-int rows_per_block(int per_row) {
-  const int per = kUnits * kThreads / per_row;
-  return per < 1 ? 1 : per > 32 ? 32 : per;
+// Rows per workgroup: what its threads take in `rounds` where that makes `blocks` workgroups, else in one round; one
+// row at least.
+int rows_per_block(int per_row, int64_t n, int rounds, int blocks) {
+  const auto rows = [&](int heads) {
+    const int per = heads * kThreads / per_row;
+    return per < 1 ? 1 : per > 32 ? 32 : per;
+  };
+  const int many = rows(rounds);
+  return n >= (int64_t)many * blocks ? many : rows(1);
 }
 
-constexpr int kMostParts = 1024;        // workgroups of a backward pass: four to a compute unit
+void set_heads(Layout& l, const NormCall& c) {
+  l.q_heads = divide_by((unsigned)(c.t[0].heads ? c.t[0].heads : 1));
+  l.k_heads = divide_by((unsigned)(c.t[1].heads ? c.t[1].heads : 1));
+}
 
-Layout grad_layout(int heads, int hd, bool f32) {
+constexpr int kMostParts = 256 * kGradGroups;      // workgroups of a backward pass: all at a time
+
+Layout grad_layout(int heads, int hd, bool f32, int64_t n) {
   Layout l = layout_of(heads, hd / (f32 ? 8 : 16));
-  const int per = kUnits * kThreads / (heads << l.shift);
-  l.per = per < 1 ? 1 : per > 32 ? 32 : per;
+  l.per = rows_per_block(heads << l.shift, n, kGradRounds, kMostParts);
   return l;
 }
 
@@ -509,7 +533,8 @@ int grad_parts(int64_t n, const Layout& l) {
 hipError_t launch_norm_rope(const RopeFreq& f, const NormCall& c, bool f32, hipStream_t stream) {
   const int heads = c.t[0].heads + c.t[1].heads;
   Layout l = layout_of(heads, c.hd / (f32 ? 8 : 16));
-  l.per = rows_per_block(heads << l.shift);
+  l.per = rows_per_block(heads << l.shift, c.n, kRounds, kBlocks);
+  set_heads(l, c);
   const dim3 grid((unsigned)((c.n + l.per - 1) / l.per));
   const size_t lds = (size_t)l.per * (f.rot / 2) * sizeof(float2);
   hipLaunchKernelGGL(f32 ? norm_rope_kernel<float> : norm_rope_kernel<uint16_t>, grid, dim3(kThreads), lds, stream, f, c, l);
@@ -522,7 +547,8 @@ size_t norm_grad_workspace(int64_t n, int hd) {
 }
 
 hipError_t launch_norm_grad(const RopeFreq& f, const NormCall& c, bool f32, void* ws, hipStream_t stream) {
-  const Layout l = grad_layout(c.t[0].heads + c.t[1].heads, c.hd, f32);
+  Layout l = grad_layout(c.t[0].heads + c.t[1].heads, c.hd, f32, c.n);
+  set_heads(l, c);
   const int parts = grad_parts(c.n, l);
   float* part = static_cast<float*>(ws);
   if (parts) {
@@ -530,7 +556,7 @@ hipError_t launch_norm_grad(const RopeFreq& f, const NormCall& c, bool f32, void
     hipLaunchKernelGGL(f32 ? norm_grad_kernel<float> : norm_grad_kernel<uint16_t>, dim3(parts), dim3(kThreads),
                        turns > sums ? turns : sums, stream, f, c, l, part);
   }
-  hipLaunchKernelGGL(norm_grad_sum_kernel, dim3(2 * c.hd / 16), dim3(kThreads), 0, stream, c, part, parts);
+  hipLaunchKernelGGL(norm_grad_sum_kernel, dim3(2 * c.hd / 16), dim3(1024), 0, stream, c, part, parts);
   return hipGetLastError();
 }
 
@@ -556,7 +582,7 @@ void launch_read_type(bool scan, unsigned grid, hipStream_t stream, const Batch&
 hipError_t launch_hold(const RopeFreq& f, const Batch& b, const HoldCall& c, hipStream_t stream) {
   const int heads = c.a.n_q + 2 * b.n_kv;
   Layout l = layout_of(heads, b.hd / 16);
-  l.per = rows_per_block(heads << l.shift);
+  l.per = rows_per_block(heads << l.shift, c.a.n, kRounds, kBlocks);
   const bool scan = scans_rows(c.a.n, heads * b.hd);
   if (!scan) {
     const hipError_t e = launch_clear_status(c.a.status, stream);
