@@ -173,10 +173,13 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q, bool joined = fal
   const int rows = max_q * p.group;
   p.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.mblocks = (rows + p.rows - 1) / p.rows;
-  // enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS
+  // Enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS.  Beside prefixes
+  // sequences are short, and their parts are joined in any case: with 512 rows to a workgroup, not 256, and of
+  // codes half as many workgroups, 64 sequences of up to 512 rows take 104 instead of 110 us (bf16, their prefix's
+  // 32,768 rows included), 48 of up to 2,048 rows 137 instead of 145 (fp8).
   p.heads = heads_together(b, p.rows, codes);
-  const int per_part = b.n_kv / p.heads * p.mblocks, want = p.rows == 16 ? 1024 : 256;
-  p.least = p.rows == 16 ? 256 / p.heads : 128;
+  const int per_part = b.n_kv / p.heads * p.mblocks, want = p.rows == 16 ? (joined && codes ? 512 : 1024) : 256;
+  p.least = p.rows == 16 ? (joined ? 512 : 256) / p.heads : 128;
   p.goal = parts_goal(want, per_part);
   if (p.goal <= b.batch || b.max_len <= p.least) p.goal = 0;
   const int64_t most = (int64_t)b.batch * ((b.max_len + p.least - 1) / p.least);
@@ -231,10 +234,13 @@ template <int HD, bool kShared>
 void launch_join(const AttendArgs& a, int most_parts, int parts, bool many, hipStream_t stream) {
   const int64_t rows = (int64_t)a.b.batch * a.b.n_kv * a.q.max_q * a.group;
   const int64_t scans = (int64_t)a.b.batch * a.scan_parts + (kShared ? (int64_t)a.sh.groups * a.sh.scan_parts : 0);
-  // a sequence can have more parts than a wave has under way; not where there are rows for all waves
-  if (many && parts > 128 && rows <= 65536)
+  // More waves to a row where it has more parts than a wave has under way, and the chip has room for them: with
+  // 33 parts 7,680 rows take 425 us of a call with one wave each and 437 with four, 6,144 rows of 11 parts 137
+  // and 145; 2,048 rows of 33 parts 104 with either.
+  const bool room = rows <= 2048;
+  if (many && parts > 128 && room)
     hipLaunchKernelGGL((join_kernel<HD, kManyWaves, kShared>), dim3((unsigned)(rows + scans)), dim3(64 * kManyWaves), 0, stream, a);
-  else if (most_parts > 32 && (!kShared || rows <= 65536))
+  else if (kShared ? parts > 16 && room : most_parts > 32)
     hipLaunchKernelGGL((join_kernel<HD, kWaves, kShared>), dim3((unsigned)(rows + scans)), dim3(kThreads), 0, stream, a);
   else
     hipLaunchKernelGGL((join_kernel<HD, 1, kShared>), dim3((unsigned)((rows + kWaves - 1) / kWaves + scans)),

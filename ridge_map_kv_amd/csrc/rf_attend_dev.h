@@ -1095,7 +1095,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   if (!prefix) place_block(a, &unit, &mb);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
-  const int wm = wave % WM, e0 = wave / WM;   // this wave's query rows; its first group
+  // this wave's query rows, and its first group.  Few query rows are spread over the SIMDs (wave % 4): for 32 and 64
+  // of 4 int8 sequences of up to 32,768 rows 89 and 95 us; both groups of a row's on one SIMD: 116 and 119.
+  const int wm = WM == 4 ? wave % 4 / 2 + wave / 4 * 2 : wave, e0 = WM == 4 ? wave % 2 : 0;
 
   Part pt;
   if (prefix ? !find_prefix(a, unit - a.own, &pt, &mb) : !find_part<kShared>(a, unit, &pt)) return;
