@@ -39,15 +39,19 @@ __device__ __forceinline__ u32x2 codes_of(const float (&x)[8], int byte) {
     for (int i = 0; i < 4; ++i) {
       // values of a block whose exponent is cut to 118 stay finite
       const float most = kType == RF_CACHE_FP8 ? 448.f : 127.f;
-      y[i] = fminf(fmaxf(x[4 * h + i] * inv, -most), most);
+      y[i] = __builtin_amdgcn_fmed3f(x[4 * h + i] * inv, -most, most);
     }
     if constexpr (kType == RF_CACHE_FP8) {
       int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
       c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
       w[h] = (unsigned)c;
     } else {
+      // beside 1.5 2^23 a value is rounded to a whole number, nearest even, in the last bits
+      unsigned c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[h] |= ((unsigned)(int)rintf(y[i]) & 0xffu) << (8 * i);
+      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(y[i] + 12582912.f);
+      const unsigned lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400u);
+      w[h] = hi << 16 | lo;
     }
   }
   return w;
