@@ -679,7 +679,8 @@ rf_status ridgefill_norm_rope(const rf_rope* rope, const rf_head_norm* norm, int
 
 /* Its gradient: of the inputs q and k (as they went in) and the gradients gq and gk of the
  * outputs, q_grad and k_grad, and in fp32 [head_dim] those of the weights, qw_grad and kw_grad
- * (each may be NULL; not written for a tensor without a weight).  With g = R^T gy, xh = r x:
+ * (each may be NULL, not the same memory; not written for a tensor without a weight).  A weight that
+ * q and k share has the sum of both as its gradient.  With g = R^T gy, xh = r x:
  *     q_grad = r (w g - xh mean(w g xh)),   qw_grad = sum over rows and heads of g xh
  * q and k may be NULL where they have no weight (their values are not needed), q_grad may be gq
  * and k_grad gk with equal strides.  The weights' sums are fp32, added in a fixed order.
@@ -763,7 +764,7 @@ typedef struct rf_prefix {
 
 /*   prefix      NULL: sequences of their own rows alone, which over a bf16 cache is
  *               ridgefill_tree_attention
- *   cache       v_pages (and v_scales) may be NULL with out
+ *   cache       v_pages (and v_scales) may be NULL where out is
  *   n_q         with a prefix batch * n_q_heads * max_q <= 2^25
  *   ws          >= ridgefill_cache_attention_workspace_bytes(kv, prefix, n_q_heads, max_q, n_q), of
  *               which the pointers in kv and prefix are not read; 256-byte aligned; its first 256

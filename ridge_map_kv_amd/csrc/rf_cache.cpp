@@ -472,6 +472,7 @@ rf_status ridgefill_norm_rope_grad(const rf_rope* rope, const rf_head_norm* norm
     if (t[i].g && t[i].g == t[i].out && t[i].g_stride != t[i].out_stride)
       return fail(RF_E_INVALID, "%s_grad in place of g%s needs equal strides", name, name);
   }
+  if (qw_grad && qw_grad == kw_grad) return fail(RF_E_INVALID, "qw_grad and kw_grad are the same memory");
   if (n_rows > 0 && rope && !positions) return fail(RF_E_INVALID, "positions is NULL");
   if (!aligned(positions, 4)) return fail(RF_E_SHAPE, "positions needs 4-byte alignment");
   if (!ws) return fail(RF_E_INVALID, "workspace is NULL");

@@ -134,3 +134,41 @@ def test_another_stream():
         return outs + dws + [p.view(torch.uint8) for p in pools]
     for a, b in zip(all_calls(None), all_calls(side)):
         assert torch.equal(a, b) and a.any()
+
+
+def test_two_graphs_with_one_workspace():
+    # attention of two calls, plain and after a prefix, captured with one workspace and replayed in turn
+    heads, n_kv, hd = 8, 2, 64
+    cases = [S.SharedCache([700, 33, 250], [], [0], n_kv, hd, 16, "int8", 1), S.SharedCache([40, 9, 64, 30], [300, 77], [0, 2, 4], n_kv, hd, 16, "fp8", 2)]
+    counts = [[1, 1, 1], [20, 9, 17, 30]]
+    calls = []
+    for c, n in zip(cases, counts):
+        starts = torch.tensor(S.starts_of(n), dtype=torch.int32, device=DEV)
+        q = _randn(9, sum(n), heads, hd)
+        calls.append((c.kv(B), c.cache(B), q, starts, max(n), c.prefix(B), torch.empty_like(q), torch.empty(sum(n), heads, device=DEV)))
+    need = max(B.ridgefill_cache_attention_workspace_bytes(kv, heads, mq, q.shape[0], pre) for kv, _, q, _, mq, pre, _, _ in calls)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def run(i):
+        kv, cache, q, starts, max_q, pre, out, lse = calls[i]
+        B.ridgefill_cache_attention(kv, cache, q, starts, max_q, 0.125, out, ws, prefix=pre, lse=lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = []
+    with torch.cuda.stream(side):
+        for i in range(2):
+            run(i)
+            want.append((calls[i][6].clone(), calls[i][7].clone()))
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            run(i)
+    for i in (0, 1, 1, 0, 0, 1):
+        calls[i][6].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert B.ridgefill_read_status(ws) == B.RF_OK
+        assert torch.equal(calls[i][6], want[i][0]) and torch.equal(calls[i][7], want[i][1])
+        run(1 - i)                                        # eager work of the other call between
+        assert torch.equal(calls[1 - i][6], want[1 - i][0])

@@ -35,6 +35,10 @@ CASES = {
     "no prefix, 128 rows, split": ([400, 129], [30, 64], [], [0], 4, 2, 128, 16, True),
     "no prefix, 256 rows": ([64, 100, 70], [64, 40, 11], [], [0], 16, 4, 128, 3, True),
     "no prefix, 320 rows, split": ([300], [64], [], [0], 10, 2, 128, 100, True),
+    "four key heads a workgroup, split": ([900, 70, 3], [1, 1, 1], [], [0], 8, 4, 128, 16, False),
+    "eight key heads, prefix in registers": ([20, 9], [2, 1], [700], [0, 2], 16, 8, 64, 16, True),
+    "more parts than four waves join": ([20000], [1], [], [0], 4, 4, 64, 16, False),
+    "many rows of many parts": ([64] * 9, [64] * 9, [2600], [0, 9], 4, 1, 64, 16, True),
     "key heads that are no power of two": ([50, 20, 9, 30], [3, 1, 2, 9], [90, 200], [0, 2, 4], 6, 3, 128, 16, True),
 }
 

@@ -29,7 +29,7 @@ def _forward(norm=None, kind=0, n=4, hd=64, pos=FAKE, q=FAKE, hq=2, qs=128, qo=F
 
 
 def _backward(norm=None, kind=0, n=4, hd=64, pos=FAKE, q=FAKE, hq=2, qs=128, gq=FAKE, gqs=128, qg=FAKE + 65536, qgs=128, qw=FAKE,
-              k=FAKE, hk=1, ks=64, gk=FAKE, gks=64, kg=FAKE + 65536, kgs=64, kw_=FAKE, ws=FAKE, ws_bytes=1 << 20, **kw):
+              k=FAKE, hk=1, ks=64, gk=FAKE, gks=64, kg=FAKE + 65536, kgs=64, kw_=FAKE + 1024, ws=FAKE, ws_bytes=1 << 20, **kw):
     r = B.make_rope(**kw)
     return B.lib().ridgefill_norm_rope_grad(C.byref(r), C.byref(norm or _norm()), kind, n, hd, pos, q, hq, qs, gq, gqs, qg, qgs, qw,
                                             k, hk, ks, gk, gks, kg, kgs, kw_, ws, ws_bytes, None)
@@ -62,7 +62,7 @@ def test_backward_refusals():
                dict(kg=FAKE + 8), dict(qw=FAKE + 2), dict(kw_=FAKE + 1)):
         _refused(_backward(**kw), B.RF_E_SHAPE)
     for kw in (dict(gq=None), dict(gk=None), dict(qg=None), dict(kg=None), dict(qg=FAKE, qgs=136), dict(kg=FAKE, kgs=72),
-               dict(ws=None), dict(hk=0, k=None, gk=None, kg=None)):
+               dict(ws=None), dict(hk=0, k=None, gk=None, kg=None), dict(kw_=FAKE)):        # the last: one gradient for two weights
         _refused(_backward(**kw), B.RF_E_INVALID)
     need = B.ridgefill_norm_rope_grad_workspace_bytes(4, 2, 1, 64)
     for kw in (dict(ws=FAKE + 64), dict(ws_bytes=need - 1)):
