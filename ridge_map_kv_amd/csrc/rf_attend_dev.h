@@ -1097,7 +1097,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   const int c = lane & 31, h = lane >> 5;
   // this wave's query rows, and its first group.  Few query rows are spread over the SIMDs (wave % 4): for 32 and 64
   // of 4 int8 sequences of up to 32,768 rows 89 and 95 us; both groups of a row's on one SIMD: 116 and 119.
-  const int wm = WM == 4 ? wave % 4 / 2 + wave / 4 * 2 : wave, e0 = WM == 4 ? wave % 2 : 0;
+  const int wm = WM == 4 ? wave / 2 : wave, e0 = WM == 4 ? wave % 2 : 0;
 
   Part pt;
   if (prefix ? !find_prefix(a, unit - a.own, &pt, &mb) : !find_part<kShared>(a, unit, &pt)) return;
@@ -1113,6 +1113,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   // is the largest score, and a scale of 0 makes them 0
   const int m = m0 + 32 * wm + c;
   const bool busy = m0 + 32 * wm < m_rows, in = m < m_rows;
+  // Waves without query rows, where there are two of them or more, turn the codes into values for the others, who share
+  // the SIMDs with them: 4 int8 sequences of up to 32,768 rows, trees of up to 48 (192 to 132 query rows) 174 -> 155
+  // us.  (In workgroups of 128 query rows there are waves to spare: 64 rows 94 -> 110.)
+  const int rest = m_rows - m0, workers = rest < 32 * WM ? (rest + 31) / 32 : WM, idle = kTileWaves - workers;
+  const bool staged = kCodes && WM == 8 && idle >= 2;
   const int qi = in ? m / a.group : 0;
   const uint64_t word = prefix ? 0ull : draft_word(a.q, first + qi, qi);
   const float scale2 = (a.q.scale == 0.f ? 1.f : fabsf(a.q.scale)) * kLog2e;
@@ -1140,16 +1145,27 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   const uint16_t* kbase = a.kp + kh * HD;
   const uint16_t* vbase = kOut ? a.vp + kh * HD : nullptr;
   // of 8 bits: a thread's share of a step's rows, 16 (hd 128) or 8 codes of one row of each, which
-  // wait in registers for their place in LDS
-  Codes<HD> codes[kOut ? 2 : 1];
+  // wait in registers for their place in LDS; a wave takes eight rows, its own or those that it is given
+  struct Share {
+    Codes<HD> k, v;
+  };
+  Share mine;
   const auto k_at = [&](int step) { return sh_kv + step % kBufs * kBufBytes; };
   const auto v_at = [&](int step) { return sh_kv + (kBufs + step % kBufs) * kBufBytes; };
+  const auto load_codes = [&](int step, int eight, Share& to) {
+    const int t = fresh(lane), slot = sh_slot[step * kTileRows + eight * 8 + (t >> 3)];
+    const int64_t at = (int64_t)(slot < 0 ? 0 : slot) * a.b.n_kv + kh;
+    to.k.load(reinterpret_cast<const uint8_t*>(a.kp), a.ks, at, t & 7);
+    if constexpr (kOut) to.v.load(reinterpret_cast<const uint8_t*>(a.vp), a.vs, at, t & 7);
+  };
+  const auto store_codes = [&](int step, int eight, const Share& from) {
+    const int t = fresh(lane), row = eight * 8 + (t >> 3), p = t & 7;
+    from.k.template store<kType>(k_at(step) + row * kRowBytes, p, k_turn<HD>(row));
+    if constexpr (kOut) from.v.template store<kType>(v_at(step) + row * kRowBytes, p, v_turn<HD>(row) << 2);
+  };
   const auto load = [&](int step) {
     if constexpr (kCodes) {
-      const int slot = sh_slot[step * kTileRows + (fresh(tid) >> 3)];
-      const int64_t at = (int64_t)(slot < 0 ? 0 : slot) * a.b.n_kv + kh;
-      codes[0].load(reinterpret_cast<const uint8_t*>(a.kp), a.ks, at, fresh(tid) & 7);
-      if constexpr (kOut) codes[1].load(reinterpret_cast<const uint8_t*>(a.vp), a.vs, at, fresh(tid) & 7);
+      if (!staged) load_codes(step, wave, mine);
       return;
     }
     const unsigned ln = fresh(lane), at = ln % kPieces;   // where the lane's piece goes
@@ -1167,12 +1183,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
   };
 
   const auto store = [&](int step) {
-    const int t = fresh(tid), row = t >> 3, p = t & 7;
-    codes[0].template store<kType>(k_at(step) + row * kRowBytes, p, k_turn<HD>(row));
-    if constexpr (kOut) codes[1].template store<kType>(v_at(step) + row * kRowBytes, p, v_turn<HD>(row) << 2);
+    if (!staged) store_codes(step, wave, mine);
   };
 
-  for (int part = begin; part < end; part += kSlots) {
+  // Looks the slots of up to kSlots rows up and returns the steps that they take.
+  const auto look_up_slots = [&](int part) {
     const int rows = end - part < kSlots ? end - part : kSlots;
     const int steps = (rows + kTileRows - 1) / kTileRows;
     if (part > begin) __syncthreads();                    // the slots before are done with
@@ -1195,10 +1210,64 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
     if (tid == 0 && part == begin) sh_wild = 0ull;
     __builtin_amdgcn_s_waitcnt(0x0f70);                   // vmcnt(0): only direct loads from here on
     __syncthreads();
+    return steps;
+  };
+  // rows of a step that exist, and whether some query does not see all 64
+  const auto there_at = [&](int step) -> uint64_t { return __ballot(sh_slot[step * kTileRows + lane] >= 0); };
+  const auto masked_at = [&](int part, int step, uint64_t there) { return ~there || part + (step + 1) * kTileRows > ctx; };
+  // Hands a step's rows to all waves.
+  const auto meet = [&](int part, int step) {
+    __syncthreads();
+    const uint64_t there = there_at(step);
+    if (kOut && masked_at(part, step, there)) {
+      // 0 times what a query does not see has to be 0: rows that are not there become 0, and so do
+      // pieces of a draft's row with an infinity or NaN, which is remembered for the end
+      for (int x = tid; x < kTileRows * kPieces; x += 64 * kTileWaves) {
+        u32x4* p = reinterpret_cast<u32x4*>(v_at(step)) + x;
+        const int r = x / kPieces, draft = part + step * kTileRows + r - ctx;
+        const bool is = there >> r & 1, wild = is && draft >= 0 && not_finite(*p);
+        if (!is || wild) *p = u32x4{0u, 0u, 0u, 0u};
+        if (wild) atomicOr(&sh_wild, 1ull << draft);
+      }
+      __syncthreads();
+    }
+  };
+  if constexpr (kCodes && WM == 8) {
+    if (staged && !busy) {
+      // up to four times eight rows of a step (rows past the last ones are loaded, and not stored)
+      Share shares[4];
+      const auto send = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int eight = wave - workers + i * idle;
+          load_codes(step, eight < kTileRows / 8 ? eight : kTileRows / 8 - 1, shares[i]);
+        }
+      };
+      const auto keep = [&](int step) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int eight = wave - workers + i * idle;
+          if (eight < kTileRows / 8) store_codes(step, eight, shares[i]);
+        }
+      };
+      for (int part = begin; part < end; part += kSlots) {
+        const int steps = look_up_slots(part);
+        send(0);
+        keep(0);
+        if (1 < steps) send(1);
+        for (int step = 0; step < steps; ++step) {
+          meet(part, step);
+          if (step + 1 < steps) keep(step + 1);
+          if (step + 2 < steps) send(step + 2);
+        }
+      }
+      return;
+    }
+  }
+
+  for (int part = begin; part < end; part += kSlots) {
+    const int steps = look_up_slots(part);
     f32x16 s[kE];
-    // rows of a step that exist, and whether some query does not see all 64
-    const auto there_at = [&](int step) -> uint64_t { return __ballot(sh_slot[step * kTileRows + lane] >= 0); };
-    const auto masked_at = [&](int step, uint64_t there) { return ~there || part + (step + 1) * kTileRows > ctx; };
     // The order of reads, products and exponentials is pinned: fragments are read four products
     // ahead, and between two products of V the exponentials of the next sixteen rows.
     const auto scores = [&](int step) {
@@ -1225,7 +1294,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
     const auto finish = [&](int step) {
       const int ln = fresh(lane), base = part + step * kTileRows;
       const uint64_t there = there_at(step);
-      if (masked_at(step, there)) {
+      if (masked_at(part, step, there)) {
         uint64_t seen = there;
         if (base + kTileRows > ctx) seen &= seen64(word, base - ctx);
 #pragma unroll
@@ -1311,7 +1380,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
     load(0);
     if constexpr (kCodes) store(0);
     if (1 < steps) load(1);
-    // Hands a step's rows to all waves and sends for those of two steps on.
+    // Meets the others and sends for the rows of two steps on.
     const auto sync = [&](int step) {
       // the step's loads are done when only those of the next are under way
       if constexpr (!kCodes) {
@@ -1320,20 +1389,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attend_tile_kernel(AttendA
         else
           dma_wait<0>();
       }
-      __syncthreads();
-      const uint64_t there = there_at(step);
-      if (kOut && masked_at(step, there)) {
-        // 0 times what a query does not see has to be 0: rows that are not there become 0, and so do
-        // pieces of a draft's row with an infinity or NaN, which is remembered for the end
-        for (int x = tid; x < kTileRows * kPieces; x += 64 * kTileWaves) {
-          u32x4* p = reinterpret_cast<u32x4*>(v_at(step)) + x;
-          const int r = x / kPieces, draft = part + step * kTileRows + r - ctx;
-          const bool is = there >> r & 1, wild = is && draft >= 0 && not_finite(*p);
-          if (!is || wild) *p = u32x4{0u, 0u, 0u, 0u};
-          if (wild) atomicOr(&sh_wild, 1ull << draft);
-        }
-        __syncthreads();
-      }
+      meet(part, step);
       if constexpr (kCodes) {
         if (step + 1 < steps) store(step + 1);
       }
