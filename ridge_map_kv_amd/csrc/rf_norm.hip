@@ -6,7 +6,10 @@
 // For a head x of hd features with weight w, r = (mean x^2 + eps)^-1/2 and the rotation R:
 //   y = R (w r x);    backward, with g = R^T gy and xh = r x:
 //   gx = r (w g - xh mean(w g xh)),   gw = sum over rows and heads of g xh.
-// One read of the inputs and one write of the outputs: bound by memory.  A thread holds a unit of a
+// One read of the inputs and one write of the outputs: bound by memory (8,191 rows of 40 heads
+// of 128 in bf16: 35.8 us a call, 4.7 TB/s; backward, 8,192 rows of 48 heads: 66 us, 4.6 TB/s, and 4.6 for the
+// sum of the weights' gradients; 4,097 rows of 40 in fp32: 50 and 4.8), the append of codes by its
+// instructions as well (4,096 rows of 48 heads into int8: 22 us, 3.9 TB/s).  A thread holds a unit of a
 // head, two 16-byte pieces that turn together; a head's units lie in neighbouring lanes, as many as
 // the next power of two, so that its sums are a few lane exchanges, and a thread's place in a head
 // stays the same from row to row (its weights stay in registers).  Everything is fp32 between the
