@@ -39,6 +39,7 @@ CASES = {
     "eight key heads, prefix in registers": ([20, 9], [2, 1], [700], [0, 2], 16, 8, 64, 16, True),
     "more parts than four waves join": ([20000], [1], [], [0], 4, 4, 64, 16, False),
     "many rows of many parts": ([64] * 9, [64] * 9, [2600], [0, 9], 4, 1, 64, 16, True),
+    "more rows of a workgroup than slots looked up at a time": ([5000] + [1] * 31, [48] + [1] * 31, [], [0], 24, 8, 64, 16, True),
     "key heads that are no power of two": ([50, 20, 9, 30], [3, 1, 2, 9], [90, 200], [0, 2, 4], 6, 3, 128, 16, True),
 }
 
@@ -154,7 +155,7 @@ def test_masks_that_leave_nothing_of_a_sequence(kind, plen, hd, page, counts):
 
 @pytest.mark.parametrize("kind", H.KINDS)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min])
-@pytest.mark.parametrize("hd,counts", [(64, 3), (128, 24), (64, 60), (128, 2)])
+@pytest.mark.parametrize("hd,counts", [(64, 3), (128, 24), (64, 60), (128, 2), (128, 50)])
 def test_rows_that_a_query_does_not_see(kind, bad, hd, counts):
     # drafts that only they themselves see, and another group's prefix, may hold anything
     case = ([40 + counts, 12 + counts], [counts, counts], [90, 33], [0, 1, 2], 6, 2, hd, 8, True)
