@@ -770,8 +770,10 @@ typedef struct rf_prefix {
  *               which the pointers in kv and prefix are not read; 256-byte aligned; its first 256
  *               bytes hold the status
  * A group whose length or sequences are out of range, or whose queries are out of order or more
- * than max_q for each sequence, sets RF_E_ROWS, and its sequences are skipped; where groups overlap,
- * a sequence belongs to the first.  Precision and repeatability as in ridgefill_tree_attention. */
+ * than max_q for each sequence, sets RF_E_ROWS, and its sequences are skipped.  So does a group that
+ * begins, in sequences or in queries, before the end of one in front of it that has none of these
+ * faults.  Where groups overlap, a sequence belongs to the first.  Precision and repeatability as in
+ * ridgefill_tree_attention. */
 size_t ridgefill_cache_attention_workspace_bytes(const rf_paged_batch* kv, const rf_prefix* prefix,
                                                  int32_t n_q_heads, int32_t max_q, int64_t n_q);
 rf_status ridgefill_cache_attention(const rf_paged_batch* kv, const rf_prefix* prefix,

@@ -13,6 +13,12 @@ __device__ inline void scan_prefix(const AttendArgs& a, int g, int part) {
   const int pages = r.ok && r.len > 0 ? (r.len - 1) / a.b.page_size + 1 : 0, step = blockDim.x;
   const int32_t* table = a.sh.tables + (int64_t)g * a.sh.table_stride;
   int bits = !r.ok;
+  if (part == 0 && g % 64 == 0) {                   // the order of this group and the 63 after it
+    GroupLine line = {0, 0};
+    Group of_lane = {};
+    for (int g0 = 0; g0 <= g; g0 += 64) of_lane = look_up_groups(a, g0, &line);
+    bits |= g + (int)(threadIdx.x & 63) < a.sh.groups && !of_lane.ok;
+  }
   for (int64_t i = (int64_t)part * step + threadIdx.x; i < pages; i += (int64_t)a.sh.scan_parts * step) {
     const int page = table[i];
     bits |= page < 0 || page >= a.b.num_pages;
@@ -64,23 +70,24 @@ __global__ __launch_bounds__(kPer > kWaves ? 64 * kPer : kThreads, 8) void join_
   int64_t more_at = 0, more_step = 0;
   int parts = own;
   if constexpr (kShared) {
-    int g = -1;
-    for (int g0 = 0; g0 < a.sh.groups && g < 0; g0 += 64) {
-      const int l = g0 + lane;
-      const uint64_t has = __ballot(l < a.sh.groups && a.sh.starts[l] <= seq && seq < a.sh.starts[l + 1]);
-      if (has) g = g0 + __ffsll((unsigned long long)has) - 1;
-    }
-    if (g >= 0) {
-      const Group r = look_up_group(a, g);
+    GroupLine line = {0, 0};
+    for (int g0 = 0; g0 < a.sh.groups; g0 += 64) {
+      const Group r = look_up_groups(a, g0, &line);
+      const uint64_t has = __ballot(r.from <= seq && seq < r.to);
+      if (!has) continue;
+      const int l = __ffsll((unsigned long long)has) - 1;
+      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      const int group_first = of(r.first), group_n = of(r.n);
       // a sequence whose prefix is not known has no answer, nor has one outside its group's queries
-      if (!r.ok || first < r.first || (int64_t)first + n > (int64_t)r.first + r.n) return;
-      if (r.blocks) {
-        const unsigned* plan = a.sh.plan + 4 * (int64_t)g;
-        const int x = (first - r.first) * a.group + m, block = x / a.sh.rows;
+      if (!of(r.ok) || first < group_first || (int64_t)first + n > (int64_t)group_first + group_n) return;
+      if (of(r.blocks)) {
+        const unsigned* plan = a.sh.plan + 4 * (int64_t)(g0 + l);
+        const int x = (first - group_first) * a.group + m, block = x / a.sh.rows;
         parts += (int)plan[2];
         more_at = a.sh.first_row + ((int64_t)(plan[0] + block) * a.b.n_kv + kh) * a.sh.rows + x % a.sh.rows;
         more_step = (int64_t)plan[1] * a.b.n_kv * a.sh.rows;
       }
+      break;
     }
   }
   if (!kShared && parts == 1) return;               // written by its workgroup
@@ -200,16 +207,12 @@ PrefixPlan prefix_plan(const Batch& b, const PrefixCall& pre, int n_heads, int m
   const int group = n_heads / b.n_kv;
   const int64_t most = (int64_t)b.batch * max_q, n = n_q < most ? n_q : most;      // queries that can have sequences
   const int64_t groups = n < pre.groups ? n : pre.groups, all = n * group, mean = groups ? all / groups : 0;
-  // Few query rows to a prefix: in registers, unless one prefix could have many of them, since each
-  // block of 16 reads its rows again.
-  p.rows = mean <= 16 && all <= 64 ? 16 : mean <= 128 ? 128 : 256;
+  p.rows = prefix_block(mean, all);
   p.heads = heads_together(b, p.rows, codes);
   p.least = p.rows == 16 ? 256 / p.heads : 128;
   p.goal = parts_goal(p.rows == 16 ? 1024 : 256, b.n_kv / p.heads);
-  const int64_t blocks = all / p.rows + groups;         // at most: each group's last block may not be full
   p.parts = (pre.max_len + p.least - 1) / p.least;      // of one block, at most
-  const int64_t pairs = blocks > p.goal ? blocks : p.goal;
-  p.pairs = blocks == 0 ? 1 : (int)(blocks * p.parts < pairs ? blocks * p.parts : pairs);
+  p.pairs = (int)most_pairs(most_blocks(all, groups, p.rows), p.parts, p.goal);
   return p;
 }
 

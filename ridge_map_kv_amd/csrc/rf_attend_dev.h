@@ -204,24 +204,41 @@ __device__ bool find_part(const AttendArgs& a, int unit, Part* p, int heads = 1,
 
 // One group as a lane looks it up; blocks 0: nothing to do.
 struct Group {
-  int len, first, n, blocks, grains;
+  int from, to, len, first, n, blocks, grains;
   bool ok;
 };
 __device__ __forceinline__ Group look_up_group(const AttendArgs& a, int g) {
   Group r = {};
   if (g >= a.sh.groups) return r;
-  const int from = a.sh.starts[g], to = a.sh.starts[g + 1];
+  r.from = a.sh.starts[g];
+  r.to = a.sh.starts[g + 1];
   r.len = a.sh.lengths[g];
-  if (from < 0 || to < from || to > a.b.batch || r.len < 0 || r.len > a.sh.max_len) return r;
-  r.first = a.q.start[from];
-  const int end = a.q.start[to];
+  if (r.from < 0 || r.from > a.b.batch || r.to < 0 || r.to > a.b.batch) return r;  // not to be looked up
+  r.first = a.q.start[r.from];
+  const int end = a.q.start[r.to];
   r.n = (int)((unsigned)end - (unsigned)r.first);
-  // no more queries than its sequences may have: the rows of a group stay below 2^26
-  if (r.first < 0 || end < r.first || end > a.q.n_q || r.n > (int64_t)(to - from) * a.q.max_q) return r;
-  r.ok = true;
-  if (r.n == 0 || r.len == 0) return r;
-  r.blocks = (r.n * a.group + a.sh.rows - 1) / a.sh.rows;
+  r.ok = is_group(r.from, r.to, r.len, r.first, end, a.b.batch, a.sh.max_len, a.q.max_q, a.q.n_q);
+  if (!r.ok || r.n == 0 || r.len == 0) return r;
+  r.blocks = query_blocks(r.n, a.group, a.sh.rows);
   r.grains = (r.len + kGrain - 1) / kGrain;
+  return r;
+}
+// Groups g0 .. g0 + 63, one a lane; those that do not count (rf_split.h) are not ok.  *line: where the groups before
+// them end, and then where these do.  All lanes take part.  The first launch and the join look groups up by this alike:
+// the join then reads no plan that nobody wrote.
+__device__ __forceinline__ Group look_up_groups(const AttendArgs& a, int g0, GroupLine* line) {
+  const int lane = threadIdx.x & 63;
+  Group r = look_up_group(a, g0 + lane);
+  if (a.sh.groups == 1) return r;                   // nothing before it
+  const int seq = wave_scan_max(r.ok ? r.to : 0), query = wave_scan_max(r.ok ? r.first + r.n : 0);
+  const int seq_before = __shfl_up(seq, 1), query_before = __shfl_up(query, 1);
+  const auto most = [](int x, int y) { return x > y ? x : y; };
+  const GroupLine before = {most(line->seq, lane ? seq_before : 0), most(line->query, lane ? query_before : 0)};
+  if (!begins_at(r.from, r.first, before)) {
+    r.ok = false;
+    r.blocks = r.grains = 0;
+  }
+  *line = {most(line->seq, __builtin_amdgcn_readlane(seq, 63)), most(line->query, __builtin_amdgcn_readlane(query, 63))};
   return r;
 }
 
@@ -229,29 +246,33 @@ __device__ __forceinline__ Group look_up_group(const AttendArgs& a, int g) {
 // pairs of a part and a block take turns with the key heads, blocks first, so that the workgroups
 // that read the same rows run side by side.  *mb: the block.
 inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* mb, int heads = 1, int head = 0) {
-  const int lane = threadIdx.x & 63, groups = a.b.n_kv / heads, id = unit / groups;
-  p->kh = unit % groups * heads + head;
-  Group r = look_up_group(a, lane);
-  long long total = (long long)r.blocks * r.grains;
-  int blocks = r.blocks;
-  for (int g = 64 + lane; g < a.sh.groups; g += 64) {
-    const Group o = look_up_group(a, g);
-    total += (long long)o.blocks * o.grains;
-    blocks += o.blocks;
-  }
+  const int lane = threadIdx.x & 63, per = a.b.n_kv / heads, id = unit / per;
+  p->kh = unit % per * heads + head;
+  GroupLine line = {0, 0};
+  const Group first64 = look_up_groups(a, 0, &line);
+  const GroupLine line64 = line;
+  const auto past_first64 = [&](auto use) {
+    GroupLine l = line64;
+    for (int g0 = 64; g0 < a.sh.groups; g0 += 64) use(look_up_groups(a, g0, &l));
+  };
+  long long total = (long long)first64.blocks * first64.grains;
+  int blocks = first64.blocks;
+  past_first64([&](const Group& r) {
+    total += (long long)r.blocks * r.grains;
+    blocks += r.blocks;
+  });
   total = wave_sum(total);
   blocks = wave_sum(blocks);
-  const auto parts_of = [](const Group& x, int each) { return x.blocks * ((x.grains + each - 1) / each); };
-  int each = kMostGrains;
-  if (blocks < a.sh.goal)
-    each = part_grains(total, blocks, a.sh.goal, a.sh.least / kGrain, [&](int e) {
-      int parts = parts_of(r, e);
-      for (int g = 64 + lane; g < a.sh.groups; g += 64) parts += parts_of(look_up_group(a, g), e);
-      return wave_sum(parts);
-    });
+  const auto parts_of = [](const Group& r, int each) { return r.blocks * ((r.grains + each - 1) / each); };
+  const int each = group_grains(total, blocks, a.sh.goal, a.sh.least / kGrain, [&](int e) {
+    int parts = parts_of(first64, e);
+    past_first64([&](const Group& r) { parts += parts_of(r, e); });
+    return wave_sum(parts);
+  });
   int before = 0;
+  line = line64;
   for (int g0 = 0; g0 < a.sh.groups; g0 += 64) {
-    if (g0) r = look_up_group(a, g0 + lane);
+    const Group r = g0 ? look_up_groups(a, g0, &line) : first64;
     const int mine = parts_of(r, each);
     const int upto = wave_scan(mine);
     const uint64_t past = __ballot(before + upto > id);

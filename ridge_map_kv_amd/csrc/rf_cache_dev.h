@@ -25,22 +25,26 @@ __device__ __forceinline__ unsigned quotient(unsigned x, Divide v) {
   return (__umulhi(x, v.m) + x) >> v.s;
 }
 
-// Sums of a wave's lanes up to each one, by moves between lanes (six steps of a few cycles, where
-// exchanges through LDS take a hundred each); all lanes take part.
-__device__ __forceinline__ int wave_scan(int v) {
-  const auto add = [&](auto control, auto rows) {
-    v += __builtin_amdgcn_update_dpp(0, v, decltype(control)::value, decltype(rows)::value, 0xf, false);
+// What `op` (with 0 neutral) makes of a wave's lanes up to each one, by moves between lanes (six steps of a few
+// cycles, where exchanges through LDS take a hundred each); all lanes take part.
+template <typename Op>
+__device__ __forceinline__ int wave_scan_of(int v, Op op) {
+  const auto take = [&](auto control, auto rows) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, decltype(control)::value, decltype(rows)::value, 0xf, false));
   };
   using std::integral_constant;
   const integral_constant<int, 0xf> all;
-  add(integral_constant<int, 0x111>{}, all);                              // the lane 1 before, in its sixteen
-  add(integral_constant<int, 0x112>{}, all);                              // 2
-  add(integral_constant<int, 0x114>{}, all);                              // 4
-  add(integral_constant<int, 0x118>{}, all);                              // 8
-  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});    // the sixteen before, of sixteens 1 and 3
-  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});    // the first half, of the second
+  take(integral_constant<int, 0x111>{}, all);                             // the lane 1 before, in its sixteen
+  take(integral_constant<int, 0x112>{}, all);                             // 2
+  take(integral_constant<int, 0x114>{}, all);                             // 4
+  take(integral_constant<int, 0x118>{}, all);                             // 8
+  take(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});   // the sixteen before, of sixteens 1 and 3
+  take(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});   // the first half, of the second
   return v;
 }
+__device__ __forceinline__ int wave_scan(int v) { return wave_scan_of(v, [](int x, int y) { return x + y; }); }
+// Of numbers not below 0.
+__device__ __forceinline__ int wave_scan_max(int v) { return wave_scan_of(v, [](int x, int y) { return x > y ? x : y; }); }
 // Their sum, the same in all lanes.
 __device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 __device__ __forceinline__ long long wave_sum(long long v) {   // not below 0, below 2^62

@@ -36,6 +36,39 @@ constexpr int part_grains(int64_t total, int batch, int goal, int least, Count p
   return hi;
 }
 
+// Groups of sequences that share prefixes.  Query rows of a block: few to a prefix stay in registers, unless one
+// prefix could have many of them, since each block of 16 reads its rows again.  `all`: the batch's query rows, `mean`:
+// a group's.
+constexpr int prefix_block(int64_t mean, int64_t all) { return mean <= 16 && all <= 64 ? 16 : mean <= 128 ? 128 : 256; }
+constexpr int query_blocks(int n, int group, int rows) { return (n * group + rows - 1) / rows; }
+
+// Whether sequences from .. to - 1, with queries first .. end - 1, can be a group whose prefix has `len` rows; no more
+// queries than its sequences may have, so that its query rows stay below 2^26.
+constexpr bool is_group(int from, int to, int len, int first, int end, int batch, int max_len, int max_q, int64_t n_q) {
+  return from >= 0 && to >= from && to <= batch && len >= 0 && len <= max_len && first >= 0 && end >= first &&
+         end <= n_q && (int64_t)end - first <= (int64_t)(to - from) * max_q;
+}
+// A group counts if it also begins where those before it (of which is_group holds) have ended, in sequences and in
+// queries: no sequence and no query is in two of them, so that all have at most as many blocks and pairs of a block
+// and a part as the two functions below say, whatever the lists hold.
+struct GroupLine {
+  int seq, query;
+};
+constexpr bool begins_at(int from, int first, GroupLine line) { return from >= line.seq && first >= line.query; }
+
+// `all` query rows of at most `groups` groups with queries; each group's last block may not be full.
+constexpr int64_t most_blocks(int64_t all, int64_t groups, int rows) { return all / rows + groups; }
+// `parts`: of one block, at most.
+constexpr int64_t most_pairs(int64_t blocks, int64_t parts, int goal) {
+  const int64_t pairs = blocks > goal ? blocks : goal;
+  return blocks == 0 ? 1 : blocks * parts < pairs ? blocks * parts : pairs;
+}
+// Grains of a part of groups whose `blocks` blocks have `total` grains together.
+template <typename Count>
+constexpr int group_grains(int64_t total, int blocks, int goal, int least, Count parts_of) {
+  return blocks < goal ? part_grains(total, blocks, goal, least, parts_of) : kMostGrains;
+}
+
 // Rows of a workgroup where `units` axes of `rows` rows are split over workgroups that each want a
 // compute unit (of kUnitsOfChip), in multiples of `step` rows: as many as fit into one round or, if those of
 // a second round are so much shorter that both are over sooner, as many as leave no compute unit out.

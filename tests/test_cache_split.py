@@ -77,6 +77,92 @@ int main() {
 }
 """
 
+# random lists of groups and queries, in order and not: the pairs of a part and a block of query rows that the groups
+# which count come to, and those for which there is room; the same without the order of the groups
+GROUPS = r"""
+#include "rf_split.h"
+#include <algorithm>
+#include <random>
+#include <stdio.h>
+#include <vector>
+
+int main() {
+  std::mt19937_64 g(11);
+  const auto below = [&](int64_t n) { return (int64_t)(g() % (uint64_t)n); };
+  int over = 0, over_unordered = 0, left_out = 0, bad = 0, twice = 0;
+  for (int trial = 0; trial < 60000; ++trial) {
+    const int batch = 1 + (int)below(trial % 2 ? 12 : 300), groups = 1 + (int)below(trial % 3 ? 9 : 200);
+    const int max_q = 1 + (int)below(trial % 5 ? 4 : 64), group = 1 + (int)below(trial % 7 ? 8 : 512);
+    const int max_len = 1 + (int)below((int64_t)1 << (trial % 50 ? 9 : 30));
+    // lists in order, of any numbers, and in order but for some entries or a part that comes again
+    const auto list = [&](int n, int most, int kind) {
+      std::vector<int> x(n);
+      for (auto& v : x) v = (int)below(most + 1);
+      if (kind != 1) std::sort(x.begin(), x.end());
+      if (kind == 2) for (int i = 0; i < 1 + n / 8; ++i) x[below(n)] = (int)below(most + 4) - 2;
+      if (kind == 3) for (int i = 0; i + 1 < n; ++i) x[i] = i % 2 ? x[n / 2] : 0;
+      return x;
+    };
+    const bool ordered = trial % 4 == 0;
+    std::vector<int> starts = list(groups + 1, batch, ordered ? 0 : (int)below(4)), queries(batch + 1), lens(groups);
+    const int kind = ordered ? 0 : (int)below(4);
+    if (kind == 0) {
+      for (int i = 0; i < batch; ++i) queries[i + 1] = queries[i] + (int)below(max_q + 1);
+    } else {
+      queries = list(batch + 1, (int)below((int64_t)batch * max_q + 1), kind);
+    }
+    const int64_t n_q = kind == 0 || below(2) ? *std::max_element(queries.begin(), queries.end()) : queries[batch];
+    for (auto& v : lens) v = ordered || below(9) ? (int)below((int64_t)max_len + 1) : (int)below(2) - 1;
+    if (n_q < 0) continue;
+    // as the host lays a call out
+    const int64_t most = (int64_t)batch * max_q, n = n_q < most ? n_q : most, with = n < groups ? n : groups, all = n * group;
+    const int rows = rf::prefix_block(with ? all / with : 0, all), least = rows == 16 ? 64 << below(3) : 128;
+    const int goal = rf::parts_goal(rows == 16 ? 1024 : 256, 1 + (int)below(64));
+    const int64_t launched = rf::most_pairs(rf::most_blocks(all, with, rows), (max_len + least - 1) / least, goal);
+    // as the device counts them
+    struct Seen { int blocks, grains; };
+    const auto numbered = [&](bool in_order, int* counted) {
+      std::vector<Seen> seen;
+      std::vector<char> of_query(n_q), of_seq(batch);
+      rf::GroupLine line = {0, 0};
+      int64_t total = 0, blocks = 0;
+      *counted = 0;
+      for (int i = 0; i < groups; ++i) {
+        const int from = starts[i], to = starts[i + 1];
+        if (from < 0 || from > batch || to < 0 || to > batch) continue;
+        const int first = queries[from], end = queries[to];
+        if (!rf::is_group(from, to, lens[i], first, end, batch, max_len, max_q, n_q)) continue;
+        const bool counts = !in_order || rf::begins_at(from, first, line);
+        line = {std::max(line.seq, to), std::max(line.query, end)};
+        if (!counts) continue;
+        ++*counted;
+        if (in_order) {
+          for (int q = first; q < end; ++q) twice += of_query[q]++ != 0;
+          for (int s = from; s < to; ++s) twice += of_seq[s]++ != 0;
+        }
+        if (end == first || lens[i] == 0) continue;
+        seen.push_back({rf::query_blocks(end - first, group, rows), (lens[i] + 63) / 64});
+        total += (int64_t)seen.back().blocks * seen.back().grains;
+        blocks += seen.back().blocks;
+      }
+      const auto parts = [&](int each) {
+        int64_t x = 0;
+        for (auto s : seen) x += (int64_t)s.blocks * ((s.grains + each - 1) / each);
+        return x;
+      };
+      if (in_order) bad += blocks > 1 << 26;
+      return parts(rf::group_grains(total, (int)blocks, goal, least / 64, [&](int each) { return (int)parts(each); }));
+    };
+    int counted, loose;
+    over += numbered(true, &counted) > launched;
+    over_unordered += numbered(false, &loose) > launched;
+    left_out += ordered && counted != groups;
+  }
+  printf("%d %d %d %d %d\n", over, left_out, bad, twice, over_unordered);
+  return 0;
+}
+"""
+
 
 def _run(tmp_path, source):
     gxx = shutil.which("g++")
@@ -91,6 +177,13 @@ def _run(tmp_path, source):
 def test_parts_never_exceed_the_goal(tmp_path):
     over, large = _run(tmp_path, PARTS)
     assert int(over) == 0 and int(large) == 0
+
+
+def test_groups_never_exceed_the_pairs_that_are_launched(tmp_path):
+    over, left_out, bad, twice, over_unordered = (int(x) for x in _run(tmp_path, GROUPS))
+    assert over == 0 and bad == 0 and twice == 0
+    assert left_out == 0                                  # in lists that are in order every group counts
+    assert over_unordered > 100                           # the lists would, without the order
 
 
 @pytest.mark.parametrize("heads,n_kv,max_q", [(5, 5, 64), (6, 3, 64), (6, 6, 33), (80, 8, 64), (8, 8, 64), (24, 3, 20),

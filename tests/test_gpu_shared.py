@@ -288,6 +288,53 @@ def test_bad_sequences_among_good_ones():
     assert st == B.RF_E_ROWS
 
 
+# own lengths, queries, prefix lengths, group starts that fall and rise again, heads, n_kv, and the sequences that
+# have no answer: those whose first group begins before an earlier one ends
+UNORDERED = {
+    "the same two again and again": ([20, 30, 9], [1, 1, 1], [40] * 6, [0, 2, 0, 2, 0, 2, 3], 8, 2, []),
+    "all but one again and again, 128 rows": ([12 + i for i in range(64)], [8] * 64, [128 - i for i in range(16)], [0, 63] * 8 + [64], 32, 8, []),
+    "256 rows, again and again": ([70, 80, 66, 64], [64, 40, 64, 60], [200, 90, 130, 70, 20], [0, 3, 0, 3, 0, 4], 10, 2, [3]),
+    "the second begins in the first": ([20, 30, 9, 15, 8, 50], [1, 2, 1, 3, 1, 2], [40, 33, 70], [0, 4, 2, 6], 4, 2, [4, 5]),
+    "one of 130 begins at the first": ([3 + i % 40 for i in range(130)], [1 + i % 2 for i in range(130)], [i % 90 for i in range(130)],
+                                       list(range(70)) + [0] + list(range(71, 131)), 4, 2, [69, 70]),
+    "one of 130 takes a hundred": ([3 + i % 40 for i in range(130)], [1 + i % 2 for i in range(130)], [i % 90 + 1 for i in range(130)],
+                                   list(range(20)) + [120] + list(range(21, 131)), 4, 2, []),
+}
+
+
+@pytest.mark.parametrize("kind", H.KINDS)
+@pytest.mark.parametrize("name", UNORDERED)
+def test_groups_out_of_order(name, kind):
+    lens, counts, plens, groups, heads, n_kv, gone = UNORDERED[name]
+    c, q, starts, words, max_q = _make((lens, counts, plens, groups, heads, n_kv, 64, 16, False), kind, seed=len(name))
+    out, lse, st = _attend(c, q, starts, words, max_q, 0.1)
+    assert st == B.RF_E_ROWS
+    skipped = [i for b in gone for i in range(starts[b], starts[b + 1])]
+    _check(c, q, starts, words, max_q, 0.1, out, lse, which=[i for i in range(q.shape[0]) if i not in skipped])
+    assert (out[skipped] == 3).all() and (lse[skipped] == 3).all()
+
+
+@pytest.mark.parametrize("kind", H.KINDS)
+@pytest.mark.parametrize("heads,n,batch", [(64, 64, 200), (8, 5, 90), (16, 1, 150)])
+def test_queries_that_run_backwards_between_groups(kind, heads, n, batch):
+    # every other sequence has all the queries, and a group of its own: they are the first one's
+    c, _, _, _, _ = _make(([70] * batch, [1] * batch, [100 - i % 30 for i in range(batch)], list(range(batch + 1)), heads, 8, 64, 16, False), kind, seed=n)
+    q = _randn(n, n, heads, 64)
+    out, lse, st = _attend(c, q, [0, n] * (batch // 2) + [0], None, 64, 0.1)
+    assert st == B.RF_E_ROWS
+    _check(c, q, [0] + [n] * batch, None, 64, 0.1, out, lse)
+
+
+def test_outputs_beside_sequences_that_run_backwards():
+    c, q, _, words, _ = _status_case("int8")
+    for wrong, right in (([0, 1, 3, 2, 6], [0, 1, 3, 3, 3]),     # the last one has queries from before its group's
+                         ([4, 6, 0, 1, 2], [0, 0, 0, 1, 2])):    # the first group's end before they begin
+        out, lse, st = _attend(c, q, wrong, words, 6, 0.1)
+        assert st == B.RF_E_ROWS
+        _check(c, q, right, words, 6, 0.1, out, lse, which=list(range(right[-1])))
+        assert (out[right[-1]:] == 3).all() and (lse[right[-1]:] == 3).all()
+
+
 @pytest.mark.parametrize("kind", H.KINDS)
 @pytest.mark.parametrize("name", ["one token each, prefix split", "128 rows of both"])
 def test_rows_on_bad_pages_are_not_there(name, kind):
