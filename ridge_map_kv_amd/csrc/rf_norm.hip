@@ -60,25 +60,30 @@ struct Layout {
 
 // turn_of with what the angle's rounding to fp32 takes off added back: cos and sin are then as near as
 // their own rounding.  An fp32 angle of half a turn puts them up to 2^-23 off, and twice as many
-// codes of 8 bits (of some in a million, next to a border) on the other side as need be.
-__device__ __forceinline__ float2 near_turn_of(const RopeFreq& f, int j, int pos) {
+// codes of 8 bits (of some in a million, next to a border) on the other side as need be.  For those, and
+// for normed fp32 rows; rows that are only rotated are ridgefill_rope's, bit for bit.
+__device__ __forceinline__ float2 near_turn_of(const RopeFreq& f, int j, int pos, float sign) {
   double t = (double)pos * f.turns[j];
   t -= rint(t);
   const float x = 2.0f * (float)t, rest = (float)((2.0 * t - (double)x) * 3.14159265358979323846);
   float s, c;
   sincospif(x, &s, &c);
-  return make_float2(f.m * fmaf(-rest, s, c), f.m * fmaf(rest, c, s));
+  return make_float2(f.m * fmaf(-rest, s, c), sign * f.m * fmaf(rest, c, s));
 }
 
 // cos and sin of the rows from row0 on.
-template <bool kNear = false>
 __device__ __forceinline__ void fill_turns(float2* cs, const RopeFreq& f, const int32_t* pos, int64_t row0, int rows,
-                                           float sign) {
+                                           float sign, bool near) {
   const int pairs = f.rot / 2;
   for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
     const int p = pos[row0 + i / pairs];
-    cs[i] = kNear ? near_turn_of(f, i % pairs, p) : turn_of(f, i % pairs, p, sign);
+    cs[i] = near ? near_turn_of(f, i % pairs, p, sign) : turn_of(f, i % pairs, p, sign);
   }
+}
+
+template <typename T>
+__device__ __forceinline__ bool near_turns(const NormCall& c) {
+  return sizeof(T) == 4 && (c.t[0].w || c.t[1].w);
 }
 
 template <int kN>
@@ -146,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeFreq f, NormCal
         hi.r = *reinterpret_cast<const u32x4*>(x + u.hi);
       }
       if (!filled) {
-        fill_turns(cs, f, c.pos, row0, rows, 1.f);
+        fill_turns(cs, f, c.pos, row0, rows, 1.f, near_turns<T>(c));
         __syncthreads();
         filled = true;
       }
@@ -223,7 +228,7 @@ __global__ __launch_bounds__(kThreads, kGradGroups) void norm_grad_kernel(RopeFr
           }
         }
         if (!filled) {
-          fill_turns(cs, f, c.pos, row0, rows, -1.f);
+          fill_turns(cs, f, c.pos, row0, rows, -1.f, near_turns<T>(c));
           __syncthreads();
           filled = true;
         }
@@ -360,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(RopeFreq f, Batch b, Hol
         places[r] = s < 0 ? -2 : p;                   // -2: a padding row
         if (!kScan && s >= 0 && p < 0) atomicOr(c.a.status, kStatusRowsBit);
       }
-      fill_turns<kType != RF_CACHE_BF16>(cs, f, pos, row0, rows, 1.f);
+      fill_turns(cs, f, pos, row0, rows, 1.f, kType != RF_CACHE_BF16);
       __syncthreads();
     }
     float x[kN], y[kN];

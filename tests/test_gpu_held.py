@@ -189,6 +189,37 @@ def test_norm_rope_grad_of_differences():
         assert abs(got - float(dw[feature])) <= off + float(dw_off[feature]) * 1.01
 
 
+@pytest.mark.parametrize("layout", [B.RF_ROPE_HALF, B.RF_ROPE_INTERLEAVED])
+def test_turns_of_normed_fp32_rows_are_as_near_as_their_rounding(layout):
+    # 1 at one feature alone: r is 8, and y is 8 cos p and 8 sin p, exactly as the kernel holds them.  At positions
+    # near half a turn, where the sine is below 2^-3 and its last place 2^-27: within four of those and its rounding,
+    # 3.4e-8; the rounding of the angle to fp32 alone would put it up to pi 2^-25 = 9.4e-8 off
+    p = np.arange(70000)
+    turn = p / (2 * np.pi)
+    p = p[np.abs(2 * (turn - np.rint(turn))) > 0.97]
+    n, other, tol = len(p), 32 if layout == B.RF_ROPE_HALF else 1, 4.5 * 2.0 ** -27
+    assert n > 1000 and np.abs(np.sin(p)).max() < 2.0 ** -3
+    pos = torch.from_numpy(p.astype(np.int32)).to(DEV)
+    w, rope = torch.ones(64, device=DEV), B.make_rope(layout=layout)
+    norm = B.make_head_norm(w, w, 0.0)
+    cos, sin = torch.from_numpy(np.cos(p)), torch.from_numpy(np.sin(p))
+    x, g = torch.zeros(n, 1, 64, device=DEV), torch.zeros(n, 1, 64, device=DEV)
+    x[:, :, 0] = 1
+    q, k = torch.empty_like(x), torch.empty_like(x)
+    B.ridgefill_norm_rope(rope, norm, pos, x, q, x, k)
+    for y in (q, k):
+        y = y.cpu().to(F64)[:, 0] / 8
+        assert float((y[:, 0] - cos).abs().max()) <= 4.5 * 2.0 ** -24 and float((y[:, other] - sin).abs().max()) <= tol
+    # backward: the row's norm lies in a feature that the gradient does not touch, so that dx is 8 g
+    x.zero_()
+    x[:, :, 63] = 1
+    g[:, :, 0] = 1
+    (dq, dk), _ = _grads(rope, norm, pos, x, g, x, g, torch.float32, 64)
+    for y in (dq, dk):
+        y = y.cpu().to(F64)[:, 0] / 8
+        assert float((y[:, 0] - cos).abs().max()) <= 4.5 * 2.0 ** -24 and float((y[:, other] + sin).abs().max()) <= tol
+
+
 def test_norm_empty():
     q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
     pos = torch.empty(0, dtype=torch.int32, device=DEV)
