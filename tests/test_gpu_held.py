@@ -432,3 +432,71 @@ def test_many_short_rows_of_append_and_read(n, n_kv):
                  lambda: B.ridgefill_read_rows(kv, cache, rows, status, k_out=k_out)):
         call()
         assert B.ridgefill_read_status(status) == B.RF_E_ROWS
+
+
+# ---------------------------------------------------------------------------------- many rows
+# Enough rows that workgroups take several at a time, or block after block of them, with a rest in the last.
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,hq,hk,hd,rot", [(4099, 40, 8, 128, 0), (65601, 2, 1, 64, 32)])
+def test_norm_rope_of_many_rows(dtype, n, hq, hk, hd, rot):
+    qw, kw = _weights(hd, dtype, 4)
+    q, k = _randn(1, n, hq, hd, dtype=dtype), _randn(2, n, hk, hd, dtype=dtype) * 8
+    pos, rope = _positions(n, 3), B.make_rope(rotary_dim=rot)
+    outs = [torch.full_like(t, 9.0) for t in (q, k)]
+    B.ridgefill_norm_rope(rope, B.make_head_norm(qw, kw, 1e-5), pos.to(DEV), q, outs[0], k, outs[1])
+    for t, out, w in zip((q, k), outs, (qw, kw)):
+        want, off = H.norm_rope(t, w, 1e-5, pos, rot or hd, 0)
+        _close(out, want, _rounded(want, off, dtype), "many rows")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,hq,hk,hd,rot", [(1601, 40, 8, 128, 64), (25001, 2, 1, 64, 0)])
+def test_norm_rope_grad_of_many_rows(dtype, n, hq, hk, hd, rot):
+    qw, kw = _weights(hd, dtype, 5)
+    q, k, gq, gk = (_randn(s, n, h, hd, dtype=dtype) for s, h in ((1, hq), (2, hk), (3, hq), (4, hk)))
+    pos, rope = _positions(n, 6), B.make_rope(rotary_dim=rot)
+    outs, dws = _grads(rope, B.make_head_norm(qw, kw, 1e-5), pos.to(DEV), q, gq, k, gk, dtype, hd)
+    for t, g, out, dw, w in zip((q, k), (gq, gk), outs, dws, (qw, kw)):
+        dx, want, off, _ = H.norm_rope_grad(t, w, 1e-5, g, pos, rot or hd, 0)
+        _close(out, dx, _rounded(dx, off, dtype), "x")
+        # A weight's sum: a thread adds the heads of its place, at most nine of these sizes; then 64 lanes by pairs, four
+        # waves, and of at most 768 workgroups twelve rows and 64 sums: below 96 additions one after another,
+        # each of which errs by half a place of no more than the sum of the magnitudes, which are within
+        # those of the rotated gradient (cos and sin 2^-20), the row's sum of squares and a few products
+        x, gy = t.cpu().to(F64), g.cpu().to(F64)
+        size = R.rotate(gy, pos, rot or hd, 0, True)[1]
+        size[..., rot or hd:] = gy[..., rot or hd:].abs()
+        xh = (x * (x.square().mean(-1, keepdim=True) + float(np.float32(1e-5))) ** -0.5).abs()
+        tol = (size * xh).sum((0, 1)) * (2.0 ** -20 + (hd / 2 + 8 + 96) * R.U_FP32)
+        _close(dw, want, tol, "w")
+
+
+@pytest.mark.parametrize("kind", H.KINDS)
+def test_append_of_many_rows(kind):
+    n, n_q, n_kv, hd, page, max_len = 4099, 32, 8, 128, 16, 2100
+    per = -(-max_len // page)
+    g = np.random.default_rng(8)
+    table_np = g.permutation(2 * per + 1)[:2 * per].reshape(2, per).astype(np.int32)
+    places = g.permutation(2 * max_len)[:n]
+    seq_np, rows_np = (places // max_len).astype(np.int32), (places % max_len).astype(np.int32)
+    qkv = _randn(9, n, n_q + 2 * n_kv, hd)
+    q, k, v = qkv[:, :n_q], qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:]
+    qw, kw = _weights(hd, torch.bfloat16, 7)
+    kv = B.make_batch(torch.from_numpy(table_np).to(DEV), None, page, 2 * per + 1, n_kv, hd, max_len)
+    status = torch.full((1,), -1, dtype=torch.int32, device=DEV)
+    kp, vp, ks, vs = H.pools(2 * per + 1, page, n_kv, hd, kind)
+    seq, rows, q_out = torch.from_numpy(seq_np).to(DEV), torch.from_numpy(rows_np).to(DEV), torch.full((n, n_q, hd), 9.0, dtype=torch.bfloat16, device=DEV)
+    cache = B.make_cache(kp, vp, ks, vs)
+    B.ridgefill_append_cache(B.make_rope(), B.make_head_norm(qw, kw, 1e-5), kv, cache, k, v, rows, status, seq=seq, q=q, q_out=q_out)
+    assert B.ridgefill_read_status(status) == B.RF_OK
+    at = torch.from_numpy(rows_np)
+    want, off = H.norm_rope(q, qw, 1e-5, at, hd, 0)
+    _close(q_out, want, _rounded(want, off, torch.bfloat16), "q")
+    k_out, v_out = torch.empty(n, n_kv, hd, device=DEV), torch.empty(n, n_kv, hd, device=DEV)
+    B.ridgefill_read_rows(kv, cache, rows, status, seq=seq, k_out=k_out, v_out=v_out)
+    assert B.ridgefill_read_status(status) == B.RF_OK
+    want, off = H.norm_rope(k, kw, 1e-5, at, hd, 0)
+    page_of, slot = _place(seq_np, rows_np, table_np, page)
+    _check_held(k_out.cpu().to(F64), None if ks is None else ks[page_of, slot], want, off, kind, "k")
+    assert torch.equal(v_out.cpu().to(F64), H.held(v, kind)[0])
