@@ -180,13 +180,11 @@ AttendPlan attend_plan(const Batch& b, int n_heads, int max_q, bool joined = fal
   const int rows = max_q * p.group;
   p.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.mblocks = (rows + p.rows - 1) / p.rows;
-  // Enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS.  Beside prefixes
-  // sequences are short, and their parts are joined in any case: with 512 rows to a workgroup, not 256, and of
-  // codes half as many workgroups, 64 sequences of up to 512 rows take 104 instead of 110 us (bf16, their prefix's
-  // 32,768 rows included), 48 of up to 2,048 rows 137 instead of 145 (fp8).
+  // Enough workgroups for the chip: up to four a compute unit with registers alone, one with LDS; of codes beside
+  // prefixes half as many (48 sequences of up to 2,048 rows on four prefixes in fp8 137 instead of 145 us).
   p.heads = heads_together(b, p.rows, codes);
   const int per_part = b.n_kv / p.heads * p.mblocks, want = p.rows == 16 ? (joined && codes ? 512 : 1024) : 256;
-  p.least = p.rows == 16 ? (joined ? 512 : 256) / p.heads : 128;
+  p.least = p.rows == 16 ? least_rows(b.batch, b.max_len, per_part, want, p.heads, joined) : 128;
   p.goal = parts_goal(want, per_part);
   if (p.goal <= b.batch || b.max_len <= p.least) p.goal = 0;
   const int64_t most = (int64_t)b.batch * ((b.max_len + p.least - 1) / p.least);

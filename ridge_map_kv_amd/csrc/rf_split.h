@@ -12,6 +12,17 @@ constexpr int kMostGrains = 1 << 24;    // of one sequence: 2^30 rows in grains 
 // workgroups, since one too many costs a round of its own.
 constexpr int parts_goal(int want, int per_part) { return want / per_part > 1 ? want / per_part : 1; }
 
+// Least rows of a part of up to 16 query rows, where a workgroup takes `heads` key heads and a part `per_part`
+// workgroups.  Parts that are joined in any case (beside prefixes, where sequences are short) have 512 rows to a workgroup,
+// not 256, unless that makes less than a quarter of the workgroups wanted: with a prefix of 8,192 rows, 32 query and 8
+// key heads of 128 in bf16, 1, 4 and 16 sequences of 2,048 rows take 21.6, 23.8 and 64 us with 256, 24.0, 24.9 and 61
+// with 512; in fp8 4 of 512 rows 22.6 and 23.6, 8 of 2,048 37.5 and 34.9.
+constexpr int least_rows(int batch, int max_len, int per_part, int want, int heads, bool joined) {
+  const int many = 512 / heads;
+  const int64_t workgroups = (int64_t)batch * ((max_len + many - 1) / many) * per_part;
+  return joined && 4 * workgroups >= want ? many : 256 / heads;
+}
+
 // Grains of one part where sequences of together `total` grains, cut into parts each of its own, come to
 // `goal` parts at most; goal > batch, and `least` grains are taken at least.  parts_of(each) counts the
 // parts for a size; it never rises with the size.  The smallest that might do is total / goal, and

@@ -163,6 +163,29 @@ int main() {
 }
 """
 
+# least rows of a part, printed; never so few workgroups because of long parts that most of the chip is left out
+LEAST = r"""
+#include "rf_split.h"
+#include <initializer_list>
+#include <stdio.h>
+
+int main() {
+  for (int batch = 1; batch < 100; batch += batch / 8 + 1)
+    for (int len = 1; len < 40000; len = len * 5 / 4 + 1)
+      for (int heads : {1, 2, 4})
+        for (int per_part : {1, 2, 8, 16})
+          for (int want : {512, 1024}) {
+            const int alone = rf::least_rows(batch, len, per_part, want, heads, false), least = rf::least_rows(batch, len, per_part, want, heads, true);
+            const auto workgroups = [&](int rows) { return batch * ((len + rows - 1) / rows) * per_part; };
+            if (alone != 256 / heads || (least != alone && least != 2 * alone)) return 1;
+            if (least != alone && 4 * workgroups(least) < want) return 2;
+          }
+  const auto show = [](int batch, int len, int per_part, int want, int heads) { printf("%d ", rf::least_rows(batch, len, per_part, want, heads, true)); };
+  show(64, 512, 8, 1024, 1), show(4, 2048, 8, 1024, 1), show(1, 65536, 8, 1024, 1), show(48, 2048, 2, 512, 4), show(4, 512, 2, 512, 4);
+  return 0;
+}
+"""
+
 
 def _run(tmp_path, source):
     gxx = shutil.which("g++")
@@ -203,3 +226,7 @@ def test_weight_chunks_leave_no_stragglers(tmp_path):
     chunks = [int(x) for x in _run(tmp_path, CHUNKS)]
     for batch, chunk in zip((3, 5, 6, 9, 12), chunks):
         assert 8 * batch * -(-32768 // chunk) <= 256
+
+
+def test_parts_beside_prefixes_are_not_too_long_for_few_sequences(tmp_path):
+    assert [int(x) for x in _run(tmp_path, LEAST)] == [512, 256, 512, 128, 64]
