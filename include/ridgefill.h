@@ -651,7 +651,8 @@ rf_status ridgefill_evict_rows(const rf_paged_batch* kv, const rf_layer* layers,
  * with weight w, r = (mean x^2 + eps)^(-1/2) over its head_dim features and R the rotation:
  *     y = R (w r x)
  * A tensor without a weight is only rotated.  Sums of squares are fp32 (magnitudes above 2^60
- * overflow them), results are rounded once.  With eps = 0 a head of zeros gives NaN.
+ * overflow them), results are rounded once.  With eps = 0 a head of zeros gives NaN, one whose
+ * magnitudes are all below 2^-75 infinities, and r has fewer bits where they are all below 2^-58.
  * ------------------------------------------------------------------------------ */
 typedef struct rf_head_norm {
   const void* q_w;              /* device [head_dim], of the tensors' type, 16-byte aligned;
@@ -698,9 +699,11 @@ rf_status ridgefill_norm_rope_grad(const rf_rope* rope, const rf_head_norm* norm
                                    float* kw_grad, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------
- * Caches in 16 or 8 bits.  RF_CACHE_BF16 is the cache of the calls above.  The others hold codes
+ * Caches in 16 or 8 bits.  RF_CACHE_BF16 is the cache of the calls above, which take no other: the
+ * fill writes, and ridgefill_attention_weight and ridgefill_evict_rows read bf16 pools.  The others hold codes
  * of 8 bits (e4m3 floats, or whole numbers) in blocks of 32 features of a head that share a power
- * of two, as the OCP microscaling formats do: for a block x, e is the smallest exponent with
+ * of two, much as in the OCP microscaling formats (there int8 codes count in steps of 2^-6 of the scale,
+ * and e4m3 blocks above 1.75 2^k are cut off): for a block x, e is the smallest exponent with
  * max |x| <= M 2^e (M = 448 for e4m3, 127 for int8), kept to -110 .. 118; a code is x 2^-e rounded
  * to its type (ties to even, magnitudes above M to M) and stands for code * 2^e; the scale byte is
  * e + 127.  A block with an infinity or NaN is NaN altogether: scale byte 255, and codes 0 (int8) or
@@ -735,7 +738,8 @@ rf_status ridgefill_append_cache(const rf_rope* rope, const rf_head_norm* norm,
 
 /* Cached rows back: k_out[i] and v_out[i] receive cache row rows[i] of sequence seq[i].
  *   k_out, v_out   device [n_rows][n_kv_heads][head_dim] of `type` (RF_TYPE_BF16 or RF_TYPE_F32;
- *                  both exact), 16-byte aligned, strides as in ridgefill_norm_rope; one may be NULL
+ *                  both exact), 16-byte aligned, strides as in ridgefill_norm_rope, no overlap; one
+ *                  may be NULL
  *   seq, rows, status   as in ridgefill_append_rows, but the same row may come more than once;
  *                  rows that are out of range, on a bad page or padding are left as they were
  * kv->lengths is not read.  n_rows: 0 .. 2^23, n_rows * n_kv_heads * head_dim <= 2^34. */
@@ -749,9 +753,10 @@ rf_status ridgefill_read_rows(const rf_paged_batch* kv, const rf_cache* cache, i
  * filled once, under many answers).  Queries, q_start, max_q, tree_mask, scale, out and lse as in
  * ridgefill_tree_attention; kv->lengths and its block tables are the sequences' own rows.  With
  * `prefix`, sequences group_start[g] .. group_start[g+1]-1 all see the lengths[g] rows of prefix g
- * before their own: one softmax over both.  A prefix's rows are read once for all its queries (for
- * every 256 rows of the matrix of queries and query heads that share a key head).  Sequences before
- * group_start[0] and from group_start[groups] on have no prefix.
+ * before their own: one softmax over both.  A prefix's rows are read once for every block of its
+ * matrix of queries and query heads that share a key head: of 256 rows, of 128 where n_q queries come to
+ * 128 rows a group or less, of 16 where they come to 16 and to no more than 64 in all.  Sequences
+ * before group_start[0] and from group_start[groups] on have no prefix.
  * ------------------------------------------------------------------------------ */
 typedef struct rf_prefix {
   const int32_t* block_tables;  /* device int32 [groups][table_stride]: pages of the same pools */

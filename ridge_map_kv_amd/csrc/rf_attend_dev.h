@@ -1062,7 +1062,7 @@ __device__ __forceinline__ unsigned v_turn(unsigned row) {
 
 // A thread's codes of a step: the eighth p of a row's, all in one block.  Trees of up to 48 tokens on 4 int8 sequences
 // of up to 32,768 rows: 155 us a call (the same from bf16: 170); 8 trees of 24 after a prefix of 65,536 rows, 40
-// query heads: 422, 620 TFLOP/s.
+// query heads: 419 to 433, 605 to 620 TFLOP/s.
 template <int HD>
 struct Codes {
   unsigned w[HD / 32];

@@ -1,5 +1,5 @@
 // How a cache holds its values (rf_cache.type): bf16 as they are, or codes of 8 bits in blocks of 32
-// features that share a power of two, as the OCP microscaling formats do.  For a block whose largest
+// features that share a power of two, much as in the OCP microscaling formats.  For a block whose largest
 // magnitude is top, the exponent e is the smallest with top <= M 2^e (M = 448 for e4m3, 127 for int8),
 // kept to -110 .. 118; a code is the nearest value of its type (ties to even) to x 2^-e, and stands for
 // code 2^e; the scale byte is e + 127.  These values have at most eight significant bits and are

@@ -7,13 +7,13 @@
 //   y = R (w r x);    backward, with g = R^T gy and xh = r x:
 //   gx = r (w g - xh mean(w g xh)),   gw = sum over rows and heads of g xh.
 // One read of the inputs and one write of the outputs: bound by memory (8,191 rows of 40 heads
-// of 128 in bf16: 35.8 us a call, 4.7 TB/s; backward, 8,192 rows of 48 heads: 66 us, 4.6 TB/s, and 4.6 for the
-// sum of the weights' gradients; 4,097 rows of 40 in fp32: 50 and 4.8), the append of codes by its
-// instructions as well (4,096 rows of 48 heads into int8: 22 us, 3.9 TB/s).  A thread holds a unit of a
-// head, two 16-byte pieces that turn together; a head's units lie in neighbouring lanes, as many as
-// the next power of two, so that its sums are a few lane exchanges, and a thread's place in a head
-// stays the same from row to row (its weights stay in registers).  Everything is fp32 between the
-// one load and the one rounding.
+// of 128 in bf16: 35.8 us a call, 4.7 TB/s, in fp32 62.8, 5.3 TB/s; backward, 8,192 rows of 48 heads: 66 us,
+// 4.6 TB/s, and 4.6 for the sum of the weights' gradients; 4,097 rows of 40 in fp32: 50 and 4.8), the append of
+// codes by its instructions as well (4,096 rows of 48 heads into int8 or fp8: 22 us, 4.2 TB/s; into bf16 24,
+// 4.2).  A thread holds a unit of a head, two 16-byte pieces that turn together; a head's units lie in
+// neighbouring lanes, as many as the next power of two, so that its sums are a few lane exchanges, and a
+// thread's place in a head stays the same from row to row (its weights stay in registers).  Everything is
+// fp32 between the one load and the one rounding.
 #include "rf_held_dev.h"
 #include "rf_rope_dev.h"
 
@@ -24,7 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 // Heads that a thread takes in turn where there are rows for kBlocks workgroups, forward: for 8,191 rows of 40 heads
 // of 128 features in bf16 (168 MB read and written) 37.5 us with 3, 39.3 with 4, 41.8 with 2, 57.7 with 2 under way
-// at a time.
+// at a time (timed side by side in one process).
 constexpr int kRounds = 3, kBlocks = 2048;
 // Backward, and its workgroups to a compute unit: 8,192 rows of 48 heads of 128 in bf16 (302 MB) 70.5 us with 4 and 3,
 // 81 with 8 and 3, 80.5 with 2 workgroups, 128 with 4 (registers in scratch memory).
