@@ -96,6 +96,14 @@ __device__ __forceinline__ float squares(const float (&a)[kN], const float (&b)[
   return s;
 }
 
+// m^-1/2 within half a place: a root and a division leave about one, which the residual 1 - m r^2, its product
+// taken in two parts, puts right.  Of 0 and infinity (whose residual is NaN) infinity and 0.
+__device__ __forceinline__ float inverse_root(float m) {
+  const float r = 1.f / sqrtf(m), h = m * r;
+  const float e = fmaf(-fmaf(m, r, -h), r, fmaf(-h, r, 1.f));
+  return e == e ? fmaf(0.5f * e, r, r) : r;
+}
+
 // A thread's two pieces of a weight.
 template <typename T>
 struct Weight {
@@ -160,14 +168,14 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeFreq f, NormCal
       hi.get(b);
       const bool turned = u.pair_lo >= 0;
       if (t.w) {
-        const float r = 1.f / sqrtf(sum_lanes(squares(a, b), l.lp) * inv_hd + c.eps);
+        const float r = inverse_root(sum_lanes(squares(a, b), l.lp) * inv_hd + c.eps);
         float x[kN], y[kN];
         w.lo.get(x);
         w.hi.get(y);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          a[i] = a[i] * r * x[i];
-          b[i] = b[i] * r * y[i];
+          a[i] = a[i] * x[i] * r;                     // of two bf16 the first product is exact
+          b[i] = b[i] * y[i] * r;
         }
       }
       if (turned) turn_values<kN>(a, b, cs + row * pairs, u, f.layout != RF_ROPE_HALF);
@@ -252,7 +260,7 @@ __global__ __launch_bounds__(kThreads, kGradGroups) void norm_grad_kernel(RopeFr
           const float mean = sum_lanes(squares(xa, xb), l.lp) * inv_hd;
           dot = sum_lanes(in ? dot : 0.f, l.lp);
           // no head, no share (r may be infinite there)
-          const float r = 1.f / sqrtf(mean + c.eps), back = r * r * dot * inv_hd;
+          const float r = inverse_root(mean + c.eps), back = r * r * dot * inv_hd;
 #pragma unroll
           for (int e = 0; e < kN; ++e) {
             const float da = ga[e] * xa[e] * r, db = gb[e] * xb[e] * r;
@@ -376,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(RopeFreq f, Batch b, Hol
     // A wave's heads are mostly of one kind: what none of them needs is left out (23.7 us for 4,096 rows of 32 + 16
     // heads of 128 into int8 with all of it for all, 22.2 without).
     if (__any(normed)) {
-      const float r = 1.f / sqrtf(sum_lanes(squares(x, y), l.lp) * inv_hd + c.eps);
+      const float r = inverse_root(sum_lanes(squares(x, y), l.lp) * inv_hd + c.eps);
       float s[kN], t[kN];
       Weight<uint16_t> one;                           // chosen, not indexed: they stay in registers
 #pragma unroll
@@ -389,8 +397,8 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(RopeFreq f, Batch b, Hol
       if (normed) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          x[i] = x[i] * r * s[i];
-          y[i] = y[i] * r * t[i];
+          x[i] = x[i] * s[i] * r;
+          y[i] = y[i] * t[i] * r;
         }
       }
     }

@@ -220,6 +220,19 @@ def test_turns_of_normed_fp32_rows_are_as_near_as_their_rounding(layout):
         assert float((y[:, 0] - cos).abs().max()) <= 4.5 * 2.0 ** -24 and float((y[:, other] + sin).abs().max()) <= tol
 
 
+def test_root_of_the_mean_is_within_half_a_place():
+    # rows of v = 1 + k / 1024, 1 and zeros: the mean of squares is (v^2 + 1) / 64, exact in fp32 (at most 23 bits), and
+    # what a weight of 1 makes of the 1 is the root itself; second-order terms of its correction are below 2^-20
+    k = np.arange(1024)
+    x = torch.zeros(1024, 1, 64, device=DEV)
+    x[:, 0, 3], x[:, 0, 40] = torch.from_numpy((1 + k / 1024).astype(np.float32)).to(DEV), 1
+    out = torch.empty_like(x)
+    B.ridgefill_norm_rope(None, B.make_head_norm(torch.ones(64, device=DEV), None, 0.0), None, x, out)
+    want = (((1 + k / 1024) ** 2 + 1) / 64) ** -0.5
+    got = out[:, 0, 40].cpu().numpy()
+    assert np.abs(got - want).max() > 0 and (np.abs(got - want) <= (0.5 + 2.0 ** -10) * np.spacing(got)).all()
+
+
 def test_norm_empty():
     q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
     pos = torch.empty(0, dtype=torch.int32, device=DEV)
