@@ -7,18 +7,21 @@ namespace rf {
 
 namespace {
 
+// The plan of more than 64 groups.
+__global__ __launch_bounds__(64) void plan_kernel(AttendArgs a) {
+  GroupLine line = {0, 0};
+  const Group first = look_up_groups(a, 0, &line);
+  const int each = grains_of_prefix_part<true>(a, first, line);
+  write_plan<true>(a, first, line, each);
+  if (threadIdx.x == 0) *a.sh.each = each;
+}
+
 // What is wrong with a group or its prefix's pages, part `part` of them.
 __device__ inline void scan_prefix(const AttendArgs& a, int g, int part) {
-  const Group r = look_up_group(a, g);
-  const int pages = r.ok && r.len > 0 ? (r.len - 1) / a.b.page_size + 1 : 0, step = blockDim.x;
+  const bool counts = a.sh.plan[g].w;
+  const int len = a.sh.lengths[g], pages = counts && len > 0 ? (len - 1) / a.b.page_size + 1 : 0, step = blockDim.x;
   const int32_t* table = a.sh.tables + (int64_t)g * a.sh.table_stride;
-  int bits = !r.ok;
-  if (part == 0 && g % 64 == 0) {                   // the order of this group and the 63 after it
-    GroupLine line = {0, 0};
-    Group of_lane = {};
-    for (int g0 = 0; g0 <= g; g0 += 64) of_lane = look_up_groups(a, g0, &line);
-    bits |= g + (int)(threadIdx.x & 63) < a.sh.groups && !of_lane.ok;
-  }
+  int bits = !counts;
   for (int64_t i = (int64_t)part * step + threadIdx.x; i < pages; i += (int64_t)a.sh.scan_parts * step) {
     const int page = table[i];
     bits |= page < 0 || page >= a.b.num_pages;
@@ -70,24 +73,23 @@ __global__ __launch_bounds__(kPer > kWaves ? 64 * kPer : kThreads, 8) void join_
   int64_t more_at = 0, more_step = 0;
   int parts = own;
   if constexpr (kShared) {
-    GroupLine line = {0, 0};
-    for (int g0 = 0; g0 < a.sh.groups; g0 += 64) {
-      const Group r = look_up_groups(a, g0, &line);
-      const uint64_t has = __ballot(r.from <= seq && seq < r.to);
-      if (!has) continue;
-      const int l = __ffsll((unsigned long long)has) - 1;
-      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      const int group_first = of(r.first), group_n = of(r.n);
+    int g = -1;
+    for (int g0 = 0; g0 < a.sh.groups && g < 0; g0 += 64) {
+      const int l = g0 + lane;
+      const uint64_t has = __ballot(l < a.sh.groups && a.sh.starts[l] <= seq && seq < a.sh.starts[l + 1]);
+      if (has) g = g0 + __ffsll((unsigned long long)has) - 1;
+    }
+    if (g >= 0) {
+      const uint4 plan = a.sh.plan[g];
+      const Group r = look_up_group(a, g);
       // a sequence whose prefix is not known has no answer, nor has one outside its group's queries
-      if (!of(r.ok) || first < group_first || (int64_t)first + n > (int64_t)group_first + group_n) return;
-      if (of(r.blocks)) {
-        const unsigned* plan = a.sh.plan + 4 * (int64_t)(g0 + l);
-        const int x = (first - group_first) * a.group + m, block = x / a.sh.rows;
-        parts += (int)plan[2];
-        more_at = a.sh.first_row + ((int64_t)(plan[0] + block) * a.b.n_kv + kh) * a.sh.rows + x % a.sh.rows;
-        more_step = (int64_t)plan[1] * a.b.n_kv * a.sh.rows;
+      if (!plan.w || first < r.first || (int64_t)first + n > (int64_t)r.first + r.n) return;
+      if (plan.y) {
+        const int x = (first - r.first) * a.group + m, block = x / a.sh.rows;
+        parts += (int)plan.z;
+        more_at = a.sh.first_row + ((int64_t)(plan.x + block) * a.b.n_kv + kh) * a.sh.rows + x % a.sh.rows;
+        more_step = (int64_t)plan.y * a.b.n_kv * a.sh.rows;
       }
-      break;
     }
   }
   if (!kShared && parts == 1) return;               // written by its workgroup
@@ -223,7 +225,7 @@ CacheLayout cache_layout(const Batch& b, const PrefixCall& pre, const AttendPlan
   l.own_rows = (int64_t)p.parts * b.n_kv * rows;
   const size_t held = (size_t)(l.own_rows + (int64_t)q.pairs * b.n_kv * q.rows);
   l.plan = kStatusBytes;
-  l.ml = l.plan + align256((size_t)pre.groups * 16);
+  l.ml = l.plan + align256((size_t)pre.groups * sizeof(uint4));
   l.o = l.ml + align256(held * sizeof(float2));
   l.total = l.o + align256(held * b.hd * sizeof(float));
   return l;
@@ -340,7 +342,8 @@ hipError_t launch_cache_attend(const Batch& b, const PrefixCall* prefix, const P
   Batch as = b;                                     // for the pages to look over
   as.max_len = prefix->max_len;
   a.sh = {prefix->tables, prefix->lengths, prefix->starts, prefix->table_stride, prefix->groups, prefix->max_len,
-          pp.goal, pp.least, pp.rows, l.own_rows, scan_parts(as), reinterpret_cast<unsigned*>(w + l.plan)};
+          pp.goal, pp.least, pp.rows, l.own_rows, scan_parts(as), reinterpret_cast<uint4*>(w + l.plan), a.status + 2};
+  if (prefix->groups > 64) hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(64), 0, stream, a);
   // The sequences' own rows and the prefixes, in one launch where both take the same kernel.
   const int own = (int)((int64_t)p.parts * (b.n_kv / p.heads) * p.mblocks), more = pp.pairs * (b.n_kv / pp.heads);
   a.own = own;

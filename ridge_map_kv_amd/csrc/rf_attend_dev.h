@@ -49,7 +49,8 @@ struct Shared {
   int rows;                     // query rows of a block
   int64_t first_row;            // of the pairs' partial results
   int scan_parts;               // workgroups that look over a prefix's pages
-  unsigned* plan;               // [groups][4]: first pair, blocks, parts; written for groups with work
+  uint4* plan;                  // [groups]: first pair, blocks, parts, and whether the group counts
+  unsigned* each;               // grains of a part, of more than 64 groups
 };
 
 struct AttendArgs {
@@ -224,12 +225,17 @@ __device__ __forceinline__ Group look_up_group(const AttendArgs& a, int g) {
   return r;
 }
 // Groups g0 .. g0 + 63, one a lane; those that do not count (rf_split.h) are not ok.  *line: where the groups before
-// them end, and then where these do.  All lanes take part.  The first launch and the join look groups up by this alike:
-// the join then reads no plan that nobody wrote.
+// them end, and then where these do.  All lanes take part.
 __device__ __forceinline__ Group look_up_groups(const AttendArgs& a, int g0, GroupLine* line) {
   const int lane = threadIdx.x & 63;
   Group r = look_up_group(a, g0 + lane);
-  if (a.sh.groups == 1) return r;                   // nothing before it
+  const auto at = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
+  const int last = a.sh.groups - g0 < 64 ? a.sh.groups - g0 - 1 : 63;
+  if (!__ballot(!r.ok && lane <= last) && begins_at(at(r.from, 0), at(r.first, 0), *line)) {
+    // without a fault among them each ends where the next one begins
+    *line = {at(r.to, last), at(r.first + r.n, last)};
+    return r;
+  }
   const int seq = wave_scan_max(r.ok ? r.to : 0), query = wave_scan_max(r.ok ? r.first + r.n : 0);
   const int seq_before = __shfl_up(seq, 1), query_before = __shfl_up(query, 1);
   const auto most = [](int x, int y) { return x > y ? x : y; };
@@ -238,68 +244,97 @@ __device__ __forceinline__ Group look_up_groups(const AttendArgs& a, int g0, Gro
     r.ok = false;
     r.blocks = r.grains = 0;
   }
-  *line = {most(line->seq, __builtin_amdgcn_readlane(seq, 63)), most(line->query, __builtin_amdgcn_readlane(query, 63))};
+  *line = {most(line->seq, at(seq, 63)), most(line->query, at(query, 63))};
   return r;
 }
 
-// The same for the prefixes: each group's rows are cut into parts, and its query rows into blocks; the
-// pairs of a part and a block take turns with the key heads, blocks first, so that the workgroups
-// that read the same rows run side by side.  *mb: the block.
-inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* mb, int heads = 1, int head = 0) {
-  const int lane = threadIdx.x & 63, per = a.b.n_kv / heads, id = unit / per;
-  p->kh = unit % per * heads + head;
-  GroupLine line = {0, 0};
-  const Group first64 = look_up_groups(a, 0, &line);
-  const GroupLine line64 = line;
-  const auto past_first64 = [&](auto use) {
-    GroupLine l = line64;
-    for (int g0 = 64; g0 < a.sh.groups; g0 += 64) use(look_up_groups(a, g0, &l));
-  };
-  long long total = (long long)first64.blocks * first64.grains;
-  int blocks = first64.blocks;
-  past_first64([&](const Group& r) {
+// How the groups' rows are cut into parts, and their query rows into blocks: the grains of a part, and one wave's plan
+// of all groups, by which the join finds the pairs of a part and a block (it reads nothing that nobody wrote).
+// `first`: groups 0 .. 63, `line`: where they end; kMany: there are more.
+__device__ __forceinline__ int parts_of(const Group& r, int each) { return r.blocks * ((r.grains + each - 1) / each); }
+template <bool kMany, typename Use>
+__device__ __forceinline__ void past_first(const AttendArgs& a, GroupLine line, Use use) {
+  if constexpr (kMany)
+    for (int g0 = 64; g0 < a.sh.groups; g0 += 64) use(g0, look_up_groups(a, g0, &line));
+}
+template <bool kMany>
+__device__ __forceinline__ int grains_of_prefix_part(const AttendArgs& a, const Group& first, GroupLine line) {
+  long long total = (long long)first.blocks * first.grains;
+  int blocks = first.blocks;
+  past_first<kMany>(a, line, [&](int, const Group& r) {
     total += (long long)r.blocks * r.grains;
     blocks += r.blocks;
   });
-  total = wave_sum(total);
-  blocks = wave_sum(blocks);
-  const auto parts_of = [](const Group& r, int each) { return r.blocks * ((r.grains + each - 1) / each); };
-  const int each = group_grains(total, blocks, a.sh.goal, a.sh.least / kGrain, [&](int e) {
-    int parts = parts_of(first64, e);
-    past_first64([&](const Group& r) { parts += parts_of(r, e); });
+  return group_grains(wave_sum(total), wave_sum(blocks), a.sh.goal, a.sh.least / kGrain, [&](int each) {
+    int parts = parts_of(first, each);
+    past_first<kMany>(a, line, [&](int, const Group& r) { parts += parts_of(r, each); });
     return wave_sum(parts);
   });
+}
+template <bool kMany>
+__device__ __forceinline__ void write_plan(const AttendArgs& a, const Group& first, GroupLine line, int each) {
   int before = 0;
-  line = line64;
-  for (int g0 = 0; g0 < a.sh.groups; g0 += 64) {
-    const Group r = g0 ? look_up_groups(a, g0, &line) : first64;
-    const int mine = parts_of(r, each);
-    const int upto = wave_scan(mine);
-    const uint64_t past = __ballot(before + upto > id);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      const int from = before + of(upto) - of(mine), n_blocks = of(r.blocks), at = id - from;
-      const int split = at / n_blocks;
-      *mb = at - split * n_blocks;
-      p->len = p->ctx = of(r.len);
-      p->first = of(r.first);
-      p->n = of(r.n);
-      p->begin = __builtin_amdgcn_readfirstlane((int)((int64_t)split * each * kGrain));
-      p->end = p->len - p->begin < (int64_t)each * kGrain ? p->len : p->begin + each * kGrain;
-      p->table = a.sh.tables + (int64_t)(g0 + l) * a.sh.table_stride;
-      p->at = a.sh.first_row + ((int64_t)id * a.b.n_kv + p->kh) * a.sh.rows - (int64_t)*mb * a.sh.rows;
-      if (at == 0 && p->kh == 0 && threadIdx.x == 0) {
-        unsigned* plan = a.sh.plan + 4 * (int64_t)(g0 + l);
-        plan[0] = from;
-        plan[1] = n_blocks;
-        plan[2] = of(mine) / n_blocks;
-      }
-      return true;
-    }
+  const auto write = [&](int g0, const Group& r) {
+    const int parts = (r.grains + each - 1) / each, mine = r.blocks * parts, upto = wave_scan(mine), g = g0 + (threadIdx.x & 63);
+    if (g < a.sh.groups) a.sh.plan[g] = {(unsigned)(before + upto - mine), (unsigned)r.blocks, (unsigned)parts, r.ok};
     before += __builtin_amdgcn_readlane(upto, 63);
+  };
+  write(0, first);
+  past_first<kMany>(a, line, write);
+}
+
+// What a workgroup computes of the prefixes: the pairs of a part and a block take turns with the key heads, blocks
+// first, so that the workgroups that read the same rows run side by side.  *mb: the block.  Up to 64 groups every wave
+// lays out for itself, and the first unit, which is always there, writes the plan; more are laid out by a launch
+// before, and looked for in its plan (1,000 groups of two sequences, one token each: 725 us, with every wave looking all
+// groups over 1,252; 65 groups 178 and 176).
+inline __device__ bool find_prefix(const AttendArgs& a, int unit, Part* p, int* mb, int heads = 1, int head = 0) {
+  const int lane = threadIdx.x & 63, per = a.b.n_kv / heads, id = unit / per;
+  p->kh = unit % per * heads + head;
+  int g, n_blocks, at, each;
+  if (a.sh.groups <= 64) {
+    GroupLine line = {0, 0};
+    const Group r = look_up_groups(a, 0, &line);
+    each = grains_of_prefix_part<false>(a, r, line);
+    if (unit == 0 && threadIdx.x < 64) write_plan<false>(a, r, line, each);
+    const int mine = parts_of(r, each), upto = wave_scan(mine);
+    const uint64_t past = __ballot(upto > id);
+    if (!past) return false;
+    g = __ffsll((unsigned long long)past) - 1;
+    const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, g); };
+    n_blocks = of(r.blocks);
+    at = id - (of(upto) - of(mine));
+    p->len = of(r.len);
+    p->first = of(r.first);
+    p->n = of(r.n);
+  } else {
+    // the last group whose first pair is not past this one: those without pairs come before the next with some
+    g = 0;
+    for (int count = a.sh.groups; count > 1;) {
+      const int step = (count + 63) / 64;
+      const int upto = __popcll(__ballot(lane * step < count && (int)a.sh.plan[g + lane * step].x <= id)) - 1;
+      g += upto * step;
+      count = count - upto * step < step ? count - upto * step : step;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    const uint4 plan = a.sh.plan[g];
+    n_blocks = (int)plan.y;
+    at = id - (int)plan.x;
+    if (at >= n_blocks * (int)plan.z) return false;
+    each = (int)*a.sh.each;
+    const Group r = look_up_group(a, g);
+    p->len = r.len;
+    p->first = r.first;
+    p->n = r.n;
   }
-  return false;
+  const int split = at / n_blocks;
+  *mb = at - split * n_blocks;
+  p->ctx = p->len;
+  p->begin = __builtin_amdgcn_readfirstlane((int)((int64_t)split * each * kGrain));
+  p->end = p->len - p->begin < (int64_t)each * kGrain ? p->len : p->begin + each * kGrain;
+  p->table = a.sh.tables + (int64_t)g * a.sh.table_stride;
+  p->at = a.sh.first_row + ((int64_t)id * a.b.n_kv + p->kh) * a.sh.rows - (int64_t)*mb * a.sh.rows;
+  return true;
 }
 
 // A workgroup's unit (part and key head) and block of query rows: the blocks of one unit go to

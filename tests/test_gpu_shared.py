@@ -237,6 +237,31 @@ def test_many_sequences_and_groups(batch, groups):
     _check(c, q, starts, words, max_q, 0.125, out, lse)
 
 
+@pytest.mark.parametrize("groups,order,kind", [(64, True, "fp8"), (65, True, "bf16"), (4500, True, "int8"), (4500, False, "bf16")])
+def test_groups_by_the_thousands(groups, order, kind):
+    # some without sequences, queries or rows; and with two that begin too early
+    g = np.random.default_rng(groups)
+    batch = groups + 20
+    lens = [int(x) for x in g.integers(1, 4, batch)]
+    counts = [int(x) for x in g.integers(0, 2, batch)]
+    plens = [int(x) for x in g.integers(0, 7, groups)]
+    cuts = [int(x) for x in np.sort(g.integers(0, batch + 1, groups + 1))]
+    gone = []
+    if not order:
+        for i in (2000, 4200):
+            cuts[i] = cuts[i - 100]
+        for b in range(batch):
+            i = next((i for i in range(groups) if cuts[i] <= b < cuts[i + 1]), None)
+            gone += [b] * (i in (2000, 4200))
+        assert gone
+    c, q, starts, words, max_q = _make((lens, counts, plens, cuts, 2, 1, 64, 4, False), kind, seed=3)
+    out, lse, st = _attend(c, q, starts, words, max_q, 0.125)
+    assert st == (B.RF_OK if order else B.RF_E_ROWS)
+    skipped = [i for b in gone for i in range(starts[b], starts[b + 1])]
+    _check(c, q, starts, words, max_q, 0.125, out, lse, which=[i for i in range(q.shape[0]) if i not in skipped])
+    assert (out[skipped] == 3).all() and (lse[skipped] == 3).all()
+
+
 def _status_case(kind="fp8"):
     case = ([20, 30, 40, 9], [2, 1, 2, 1], [50, 80], [0, 2, 4], 4, 2, 64, 8, False)
     return _make(case, kind, seed=6)
