@@ -7,7 +7,7 @@
 //   y = R (w r x);    backward, with g = R^T gy and xh = r x:
 //   gx = r (w g - xh mean(w g xh)),   gw = sum over rows and heads of g xh.
 // One read of the inputs and one write of the outputs: bound by memory (8,191 rows of 40 heads
-// of 128 in bf16: 35.8 us a call, 4.7 TB/s, in fp32 62.8, 5.3 TB/s; backward, 8,192 rows of 48 heads: 66 us,
+// of 128 in bf16: 35.8 us a call, 4.7 TB/s, in fp32 63, 5.3 TB/s; backward, 8,192 rows of 48 heads: 66 us,
 // 4.6 TB/s, and 4.6 for the sum of the weights' gradients; 4,097 rows of 40 in fp32: 50 and 4.8), the append of
 // codes by its instructions as well (4,096 rows of 48 heads into int8 or fp8: 22 us, 4.2 TB/s; into bf16 24,
 // 4.2).  A thread holds a unit of a head, two 16-byte pieces that turn together; a head's units lie in
